@@ -76,7 +76,8 @@ typedef enum moe_act { MOE_ACT_RELU = 0, MOE_ACT_SWIGLU = 1 } moe_act;
 typedef enum moe_dtype {
   MOE_F32 = 0,
   MOE_BF16 = 1,
-  MOE_Q4_AFFINE_G64 = 2   /* weights only: Edge0 QuantSpec(bits=4, group_size=64, mode=affine) */
+  MOE_Q4_AFFINE_G64 = 2,  /* weights only: Edge0 QuantSpec(bits=4, group_size=64, mode=affine) */
+  MOE_I8_CHANNEL = 3      /* weights only: symmetric 8-bit integer codes, one f32 scale per output channel */
 } moe_dtype;
 
 /* How the gate and up projections are stored ("MoE Spec and Routing",
@@ -104,7 +105,8 @@ typedef struct moe_config {
   float capacity_factor;        /* 0: no capacity limit; else >= 1 */
   int32_t act;                  /* moe_act */
   int32_t act_dtype;            /* MOE_F32 or MOE_BF16 */
-  int32_t weight_dtype;         /* MOE_F32 (with F32 act), MOE_BF16 or MOE_Q4_AFFINE_G64 (with BF16 act) */
+  int32_t weight_dtype;         /* MOE_F32 (with F32 act), MOE_BF16, MOE_Q4_AFFINE_G64 or MOE_I8_CHANNEL (with
+                                   BF16 act) */
   int32_t shared_intermediate;  /* 0: no shared expert; else the shared SwiGLU expert's width */
   float aux_alpha;              /* balancing-loss coefficient >= 0 (blog default 0.01) */
   int32_t weight_layout;        /* moe_weight_layout; FUSED_GATE_UP needs SwiGLU */
@@ -126,9 +128,14 @@ typedef struct moe_config {
  * 4*(j%8) of word j/8), and scale_i / bias_i are bf16 [E, N, K/64]: the
  * weight is scale*q + bias, one scale/bias pair per 64 consecutive elements
  * of the reduction axis K (d for w1/w2, F for w3).
+ * For MOE_I8_CHANNEL, w1..w3 hold signed 8-bit codes, [E, N, K], and scale_i
+ * is f32 [E, N]: the weight is scale*code, one scale per output channel (row
+ * of the matrix; moe_quantize_rows makes both from a dense stack).  bias_i
+ * must be NULL.  The activations are quantised by the library, token row by
+ * token row, in front of both products (see moe_grouped_ffn).
  * With weight_layout = MOE_LAYOUT_FUSED_GATE_UP the gate and up matrices
  * come as ONE tensor in w1, [E, 2F, d] (Q4: codes [E, 2F, d/8], scale1 /
- * bias1 [E, 2F, d/64]): expert e's F gate rows are followed by its F up rows,
+ * bias1 [E, 2F, d/64]; 8-bit: codes [E, 2F, d], scale1 [E, 2F]): expert e's F gate rows are followed by its F up rows,
  * so splitting one expert's projection into two halves along the output axis
  * gives (gate, up), and the experts' blocks are interleaved, not two stacked
  * tensors.  w2, scale2 and bias2 must then be NULL.  The shared expert always
@@ -136,6 +143,7 @@ typedef struct moe_config {
  *   shared1/2/3: the always-active shared expert (MoE competition docs:
  *   "Shared expert"; Edge0 MoESpec.shared_experts), SwiGLU,
  *   [Fs, d], [Fs, d], [d, Fs] in act_dtype; NULL when shared_intermediate = 0.
+ *   (With 8-bit routed experts the shared expert stays in bf16.)
  */
 typedef struct moe_weights {
   const void *w1, *w2, *w3;
@@ -170,10 +178,11 @@ int64_t moe_capacity(int32_t num_tokens, int32_t top_k, int32_t num_experts, flo
  * T, d, F >= 1; sigmoid_group needs E % n_group == 0, E/n_group >= 2,
  * 1 <= topk_group <= n_group <= 32, k <= topk_group*E/n_group; softmax needs
  * routed_scaling == 1.  Then MOE_ERR_UNSUPPORTED for what no kernel covers:
- * E > 256, k > 32, dtype pairs other than F32/F32, BF16/BF16, BF16/Q4;
- * BF16 needs d % 8 == 0 and F % 8 == 0 (16-byte rows); Q4 needs d % 64 == 0,
- * F % 64 == 0 and SwiGLU; a shared expert is offered with F32 and BF16
- * weights. */
+ * E > 256, k > 32, dtype pairs other than F32/F32, BF16/BF16, BF16/Q4,
+ * BF16/I8; BF16 needs d % 8 == 0 and F % 8 == 0 (16-byte rows); Q4 needs d % 64 == 0,
+ * F % 64 == 0 and SwiGLU; I8 needs d % 16 == 0, F % 16 == 0 and both at most
+ * 131056 (int32 sums of 8-bit products stay exact); a shared expert is offered
+ * with F32, BF16 and I8 weights. */
 moe_status moe_validate(const moe_config *cfg);
 
 /* Bytes of workspace any call below needs for this config (0 if invalid). */
@@ -228,7 +237,8 @@ moe_status moe_workspace_status(const void *ws, moe_stream_t stream);
  *   MOE_WS_PERM_TOKEN  perm_token [T*k] int32 (first off[E] valid)
  *   MOE_WS_PERM_W      perm_w [T*k] f32
  *   MOE_WS_SLOT_ROW    slot_row [T,k] int32
- *   MOE_WS_X_PERM      x_perm [T*k, d] act_dtype (0 bytes with the fused gather)
+ *   MOE_WS_X_PERM      x_perm [T*k, d] act_dtype (0 bytes with the fused gather
+ *                      or 8-bit weights)
  *   MOE_WS_H           the grouped FFN intermediate [T*k, F] act_dtype; also
  *                      the intermediate of moe_grouped_ffn
  *   MOE_WS_Y_PERM      y_perm [T*k, d] act_dtype
@@ -424,12 +434,51 @@ moe_status moe_ep_local_ids(const int32_t *recv_counts, int32_t world, int32_t e
  *   ReLU:   y[r] = W_out[e] relu(W_in[e] x[r])
  *   SwiGLU: y[r] = W_down[e] (silu(W_gate[e] x[r]) * (W_up[e] x[r]))
  * fp32 accumulation; with BF16 the intermediate is rounded to bf16 once.
+ * With MOE_I8_CHANNEL weights each row of x_perm, and each row of the bf16
+ * intermediate, is quantised as moe_quantize_rows does it, and the products
+ * are those of moe_quantized_matmul.
  * In:  x_perm [T*k, d], expert_offsets [E+1] (off[0] = 0, non-decreasing,
  *      off[E] <= T*k), weights.  Out: y_perm [T*k, d] (rows >= off[E] untouched).
  * Uses ws (the intermediate). */
 moe_status moe_grouped_ffn(const moe_config *cfg, const void *x_perm,
                            const int32_t *expert_offsets, const moe_weights *w, void *y_perm,
                            void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Symmetric 8-bit quantisation of the rows of a matrix, one scale per row:
+ *   a = max_k |x_k|;  scale = a / 127 (one fp32 division);
+ *   code_k = 127 x_k / a rounded to the nearest integer, ties to even, as if
+ *   the quotient were exact (so -127 <= code <= 127).
+ * A row of zeros gets scale 0 and codes 0.  A row that holds an infinity or a
+ * NaN gets scale NaN and codes 0: what is computed from it is NaN.
+ * In:  x [rows, cols] of dtype (MOE_F32 or MOE_BF16, else
+ *      MOE_ERR_INVALID_ARG); cols % 16 == 0, else MOE_ERR_UNSUPPORTED; rows
+ *      may be 0.  Out: codes [rows, cols] int8, scales [rows] f32.
+ * For a weight stack [E, N, K] pass rows = E*N, cols = K.  One launch, no
+ * workspace. */
+moe_status moe_quantize_rows(const void *x, int32_t dtype, int64_t rows, int32_t cols, int8_t *codes, float *scales,
+                             moe_stream_t stream);
+
+/* Matrix product in 8-bit integers with a scale per row (token) and per
+ * output channel, over one weight matrix or a stack of them:
+ *   out[r, n] = x_scales[r] * w_scales[g, n] * sum_k x_codes[r, k] * w_codes[g, n, k]
+ * for every row r in [group_offsets[g], group_offsets[g+1]).  The sums are
+ * exact 32-bit integers, the scaling is fp32, and bf16 output is rounded once.
+ * In:  x_codes [rows, k] int8, x_scales [rows] f32 (moe_quantize_rows);
+ *      group_offsets [groups+1] int32 device (0-based, non-decreasing, at
+ *      most rows; else a device error is recorded and a repaired copy used),
+ *      or NULL when groups == 1: one group of all rows; w_codes
+ *      [groups, n, k] int8, w_scales [groups, n] f32.
+ * Out: out [rows, n] of out_dtype (MOE_BF16 or MOE_F32); rows at or past the
+ *      last offset are left as they are.
+ * Limits (MOE_ERR_UNSUPPORTED): groups <= 256; k % 16 == 0 and k <= 131056;
+ * groups * n and rows below 2^30.  rows may be 0.  Any n.
+ * Uses ws: moe_quantized_matmul_workspace_size() bytes (0 for arguments that
+ * the call refuses), whose first word is the status moe_workspace_status reads. */
+size_t moe_quantized_matmul_workspace_size(int32_t groups, int32_t rows, int32_t n, int32_t k);
+moe_status moe_quantized_matmul(int32_t groups, int32_t rows, int32_t n, int32_t k, const int8_t *x_codes,
+                                const float *x_scales, const int32_t *group_offsets, const int8_t *w_codes,
+                                const float *w_scales, int32_t out_dtype, void *out, void *ws, size_t ws_bytes,
+                                moe_stream_t stream);
 
 /* Shared expert on every token (MoE competition docs, "Shared expert"):
  * out[t] = W_s3 (silu(W_s1 x[t]) * (W_s2 x[t])), weight 1, no routed scaling.

@@ -36,6 +36,7 @@ MOE_ACT_SWIGLU = 1
 MOE_F32 = 0
 MOE_BF16 = 1
 MOE_Q4_AFFINE_G64 = 2
+MOE_I8_CHANNEL = 3
 # moe_weight_layout
 MOE_LAYOUT_SEPARATE = 0
 MOE_LAYOUT_FUSED_GATE_UP = 1
@@ -105,6 +106,9 @@ SIGNATURES = {
                                     _P, C.c_size_t, _P]),
     "moe_ep_local_ids": (C.c_int, [_P, C.c_int32, C.c_int32, C.c_int32, _P, _P]),
     "moe_grouped_ffn": (C.c_int, [_CFG, _P, _P, _W, _P, _P, C.c_size_t, _P]),
+    "moe_quantize_rows": (C.c_int, [_P, C.c_int32, C.c_int64, C.c_int32, _P, _P, _P]),
+    "moe_quantized_matmul_workspace_size": (C.c_size_t, [C.c_int32] * 4),
+    "moe_quantized_matmul": (C.c_int, [C.c_int32] * 4 + [_P, _P, _P, _P, _P, C.c_int32, _P, _P, C.c_size_t, _P]),
     "moe_shared_expert": (C.c_int, [_CFG, _P, _W, _P, _P, C.c_size_t, _P]),
     "moe_combine": (C.c_int, [_CFG, _P, _P, _P, _P, _P, _P]),
     "moe_forward": (C.c_int, [_CFG, _P, _P, _P, _W, _P, _P, _P, _S, _P, C.c_size_t, _P]),

@@ -18,8 +18,10 @@ from ._lib import check, moe_config, moe_stats, moe_weights
 
 _ROUTERS = {"softmax_topk": L.MOE_ROUTER_SOFTMAX_TOPK, "sigmoid_group": L.MOE_ROUTER_SIGMOID_GROUP}
 _ACTS = {"relu": L.MOE_ACT_RELU, "swiglu": L.MOE_ACT_SWIGLU}
-_DTYPES = {"f32": L.MOE_F32, "bf16": L.MOE_BF16, "q4_affine_g64": L.MOE_Q4_AFFINE_G64}
+_DTYPES = {"f32": L.MOE_F32, "bf16": L.MOE_BF16, "q4_affine_g64": L.MOE_Q4_AFFINE_G64,
+           "i8_channel": L.MOE_I8_CHANNEL}
 _TORCH_DT = {L.MOE_F32: torch.float32, L.MOE_BF16: torch.bfloat16}
+_MOE_DT = {v: k for k, v in _TORCH_DT.items()}
 _LAYOUTS = {"separate": L.MOE_LAYOUT_SEPARATE, "fused_gate_up": L.MOE_LAYOUT_FUSED_GATE_UP}
 
 
@@ -227,6 +229,46 @@ def moe_grouped_ffn(cfg, x_perm, expert_offsets, weights: dict, y_perm, ws, stre
     w = _weights_struct(weights)
     check(L.lib().moe_grouped_ffn(C.byref(cfg), _p(x_perm), _p(expert_offsets), C.byref(w), _p(y_perm),
                                   _p(ws), _nbytes(ws), _s(stream)), "moe_grouped_ffn")
+
+
+def moe_quantize_rows(x, codes, scales, stream=None):
+    """``x`` [..., cols] (bf16 or fp32) to int8 ``codes`` of the same shape and
+    fp32 ``scales`` [...], one per row of the last axis."""
+    if x.dtype not in _MOE_DT:
+        raise ValueError("moe_quantize_rows takes float32 or bfloat16 rows")
+    if codes.dtype != torch.int8 or codes.shape != x.shape:
+        raise ValueError("codes must be an int8 tensor of x's shape")
+    if scales.dtype != torch.float32 or scales.shape != x.shape[:-1]:
+        raise ValueError("scales must be a float32 tensor with one element per row of x")
+    cols = x.shape[-1]
+    check(L.lib().moe_quantize_rows(_p(x), _MOE_DT[x.dtype], scales.numel(), cols, _p(codes), _p(scales), _s(stream)),
+          "moe_quantize_rows")
+
+
+def moe_quantized_matmul_workspace_size(groups: int, rows: int, n: int, k: int) -> int:
+    return L.lib().moe_quantized_matmul_workspace_size(groups, rows, n, k)
+
+
+def moe_quantized_matmul(x_codes, x_scales, w_codes, w_scales, out, ws, group_offsets=None, stream=None):
+    """``out[r] = x_scales[r] * w_scales[g] * (w_codes[g] @ x_codes[r])`` for
+    the rows of each group.  ``w_codes`` [n, k] or [groups, n, k]; ``out``
+    [rows, n] bf16 or fp32; ``group_offsets`` [groups + 1] int32, needed when
+    there is more than one group."""
+    groups = w_codes.shape[0] if w_codes.dim() == 3 else 1
+    n, k = w_codes.shape[-2:]
+    rows = x_codes.shape[0]
+    if x_codes.dtype != torch.int8 or w_codes.dtype != torch.int8 or x_codes.shape != (rows, k):
+        raise ValueError("codes must be int8: x_codes [rows, k], w_codes [n, k] or [groups, n, k]")
+    if x_scales.dtype != torch.float32 or w_scales.dtype != torch.float32 or x_scales.numel() != rows \
+            or w_scales.numel() != groups * n:
+        raise ValueError("scales must be float32: x_scales [rows], w_scales [n] or [groups, n]")
+    if out.dtype not in _MOE_DT or out.shape != (rows, n):
+        raise ValueError("out must be a float32 or bfloat16 tensor [rows, n]")
+    if group_offsets is not None and (group_offsets.dtype != torch.int32 or group_offsets.numel() != groups + 1):
+        raise ValueError("group_offsets must be an int32 tensor [groups + 1]")
+    check(L.lib().moe_quantized_matmul(groups, rows, n, k, _p(x_codes), _p(x_scales), _p(group_offsets), _p(w_codes),
+                                       _p(w_scales), _MOE_DT[out.dtype], _p(out), _p(ws), _nbytes(ws), _s(stream)),
+          "moe_quantized_matmul")
 
 
 def moe_shared_expert(cfg, x, weights: dict, shared_out, ws, stream=None):

@@ -18,6 +18,7 @@ constexpr int kPermTokens = 256;      // tokens per dispatch count block
 constexpr int kMaxExperts = 256;
 constexpr int kMaxTopK = 32;
 constexpr int kMaxGroups = 32;
+constexpr int kMaxI8K = 131056;       // 8-bit products: K * 128 * 128 stays below 2^31
 
 // ---------------------------------------------------------------- device status
 // The first word of the workspace holds 0 or the code of the first failure a
@@ -168,6 +169,8 @@ struct WsLayout {
   size_t shared_out;   // act[T][d]
   size_t x_stage;      // act[T][d]   (moe_forward_host)
   size_t out_stage;    // act[T][d]
+  size_t q_rows;       // int8[T*k][max(d, F)]  8-bit experts: codes of the rows a product reads
+  size_t q_scale;      // float[T*k]            and their scales
   size_t total;
   size_t region_bytes[MOE_WS_REGION_COUNT];   // unpadded sizes of the moe_ws_region buffers
 };
@@ -222,14 +225,18 @@ inline WsLayout ws_layout(const moe_config &c) {
   L.kept_counts = take(sizeof(int32_t) * E);
   L.prob_sum = take(sizeof(float) * E);
   L.dropped = take(sizeof(int32_t));
-  // bf16 experts with the fused gather read their rows from x directly: no copy buffer
-  L.x_perm = take(rb[MOE_WS_X_PERM] = c.weight_dtype == MOE_BF16 && c.fused_gather ? 0 : es * slots * d);
+  // bf16 experts with the fused gather read their rows from x directly, 8-bit
+  // experts read codes (q_rows): no copy buffer
+  const bool i8 = c.weight_dtype == MOE_I8_CHANNEL;
+  L.x_perm = take(rb[MOE_WS_X_PERM] = i8 || (c.weight_dtype == MOE_BF16 && c.fused_gather) ? 0 : es * slots * d);
   L.h = take(rb[MOE_WS_H] = es * slots * F);
   L.y_perm = take(rb[MOE_WS_Y_PERM] = es * slots * d);
   L.shared_h = take(rb[MOE_WS_SHARED_H] = es * T * Fs);
   L.shared_out = take(rb[MOE_WS_SHARED_OUT] = Fs ? es * T * d : 0);
   L.x_stage = take(es * T * d);
   L.out_stage = take(es * T * d);
+  L.q_rows = take(i8 ? slots * (d > F ? d : F) : 0);
+  L.q_scale = take(i8 ? sizeof(float) * slots : 0);
   L.total = off;
   return L;
 }
@@ -322,7 +329,7 @@ cudaError_t launch_ep_local_ids(const int32_t *recv_counts, int world, int e_loc
 // `rows` rows (the shared expert).  Writes the intermediate to `h` and the
 // result to `y`.
 struct FfnArgs {
-  int kind;                 // 0 = fp32 SIMT, 1 = bf16 tensor cores, 2 = q4 (bf16 act)
+  int kind;                 // 0 = fp32 SIMT, 1 = bf16 tensor cores, 2 = q4, 3 = 8-bit integers (both bf16 act)
   int act;                  // moe_act
   int E;                    // groups
   int rows_cap;             // allocated rows of x / h / y
@@ -347,6 +354,11 @@ struct FfnArgs {
   const void *shared_w1, *shared_w2, *shared_w3;   // [F, d], [F, d], [d, F]
   void *shared_h;           // [shared_rows, F]
   void *shared_y;           // [shared_rows, d]
+  // 8-bit path only
+  int8_t *q;                // [rows_cap, max(d, F)] codes of the rows the running product reads
+  float *qs;                // [rows_cap] their scales
+  const int32_t *slot_row;  // not null: x is the token matrix [x_rows, d] and token t's codes go to the
+  int top_k;                // rows slot_row[t, 0..top_k)
 };
 
 cudaError_t launch_ffn_simt_f32(const FfnArgs &a, cudaStream_t s);
@@ -357,6 +369,32 @@ bool q4_tc_supported(int d, int F);                                 // the tenso
 cudaError_t launch_ffn_q4_tc(const FfnArgs &a, cudaStream_t s);
 bool q4_mma_supported(int d, int F);                                // the warp-level 4-bit path's shapes
 cudaError_t launch_ffn_q4_mma(const FfnArgs &a, cudaStream_t s);
+
+// Symmetric 8-bit row quantisation (quant.cu): x [rows, K] bf16 or fp32 to
+// codes and one scale per row.  row_count (device, nullable): rows present.
+// slot_row (nullable): [rows, k] destination rows of a token's codes (-1: none).
+cudaError_t launch_quantize_rows(const void *x, bool bf16, long long rows, int K, int8_t *q, float *scale,
+                                 cudaStream_t s, const int32_t *row_count = nullptr,
+                                 const int32_t *slot_row = nullptr, int k = 1);
+
+// Product in 8-bit integers over groups of rows.
+enum MmI8Mode { I8_PLAIN = 0, I8_RELU = 1, I8_SWIGLU = 2, I8_F32 = 3 };   // I8_F32: fp32 output, else bf16
+struct MmI8Args {
+  const int32_t *offsets;   // [G+1] device, or nullptr: one group of rows_cap rows
+  int G, rows_cap;
+  int N, K;                 // outputs per row (SwiGLU: of each projection), reduction length
+  int b_stride;             // weight rows from one group to the next
+  int mode;
+  const int8_t *q;          // [rows_cap, K]
+  const float *xs;          // [rows_cap]
+  const int8_t *w0, *w1;    // [.., K] (w1: the up projection, SwiGLU only)
+  const float *ws0, *ws1;   // channel scales, same rows
+  void *out;                // [rows_cap, N]
+  int *status;
+};
+cudaError_t launch_mm_i8_tc(const MmI8Args &a, cudaStream_t s);
+cudaError_t launch_mm_i8(const MmI8Args &a, cudaStream_t s);     // picks the kernel
+cudaError_t launch_ffn_i8(const FfnArgs &a, cudaStream_t s);
 
 // Replaces the text moe_last_error() returns on this thread.
 void set_last_error_text(const char *text);

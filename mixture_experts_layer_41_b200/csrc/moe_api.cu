@@ -52,6 +52,11 @@ moe_status check_weights(const moe_config &c, const moe_weights *w) {
       return MOE_ERR_INVALID_ARG;
     if (!fused && (!aligned16(w->scale2) || !aligned16(w->bias2))) return MOE_ERR_INVALID_ARG;
   }
+  if (c.weight_dtype == MOE_I8_CHANNEL) {
+    if (w->bias1 || w->bias2 || w->bias3) return MOE_ERR_INVALID_ARG;   // symmetric codes have none
+    if (!aligned16(w->scale1) || !aligned16(w->scale3)) return MOE_ERR_INVALID_ARG;
+    if (c.act == MOE_ACT_SWIGLU && !fused && !aligned16(w->scale2)) return MOE_ERR_INVALID_ARG;
+  }
   if (c.shared_intermediate > 0) {
     if (!aligned16(w->shared1) || !aligned16(w->shared2) || !aligned16(w->shared3)) return MOE_ERR_INVALID_ARG;
   }
@@ -71,7 +76,7 @@ moe_status clear_status(void *ws, cudaStream_t s) {
 
 FfnArgs ffn_args(const moe_config &c, const WsLayout &L, void *ws) {
   FfnArgs a{};
-  a.kind = c.weight_dtype == MOE_F32 ? 0 : (c.weight_dtype == MOE_BF16 ? 1 : 2);
+  a.kind = c.weight_dtype == MOE_F32 ? 0 : (c.weight_dtype == MOE_BF16 ? 1 : (c.weight_dtype == MOE_I8_CHANNEL ? 3 : 2));
   a.act = c.act;
   a.E = c.num_experts;
   a.rows_cap = c.num_tokens * c.top_k;
@@ -80,6 +85,8 @@ FfnArgs ffn_args(const moe_config &c, const WsLayout &L, void *ws) {
   a.F = c.intermediate;
   a.h = ws_ptr<char>(ws, L.h);
   a.status = ws_ptr<int>(ws, L.status);
+  a.q = ws_ptr<int8_t>(ws, L.q_rows);
+  a.qs = ws_ptr<float>(ws, L.q_scale);
   return a;
 }
 
@@ -125,6 +132,7 @@ cudaError_t run_ffn(const FfnArgs &a, cudaStream_t s) {
   switch (a.kind) {
     case 0: return launch_ffn_simt_f32(a, s);
     case 1: return use_pair_gemm(a) ? launch_ffn_tc2_bf16(a, s) : launch_ffn_tc_bf16(a, s);
+    case 3: return launch_ffn_i8(a, s);
     default: return run_q4(a, s);
   }
 }
@@ -155,11 +163,15 @@ moe_status do_permute(const moe_config &c, const void *x, const int32_t *ids, co
 // expert-sorted order is token gather[r] (bf16 tensor-core path only).
 // shared_x / shared_out (nullable): the shared expert's tokens and output,
 // computed as one more group of the same two launches.
+// slot_row (nullable, 8-bit experts only): x_perm is the token matrix and
+// token t's codes go to the rows slot_row[t, :] of the expert-sorted order.
 moe_status do_ffn(const moe_config &c, const void *x_perm, const int32_t *off, const moe_weights *w, void *y,
                   void *ws, cudaStream_t s, cudaEvent_t mid = nullptr, const int32_t *gather = nullptr,
-                  const void *shared_x = nullptr, void *shared_out = nullptr) {
+                  const void *shared_x = nullptr, void *shared_out = nullptr, const int32_t *slot_row = nullptr) {
   const WsLayout L = ws_layout(c);
   FfnArgs a = ffn_args(c, L, ws);
+  a.slot_row = slot_row;
+  a.top_k = c.top_k;
   if (shared_x) {
     a.shared_rows = c.num_tokens;
     a.shared_x = shared_x;
@@ -193,6 +205,9 @@ moe_status do_ffn(const moe_config &c, const void *x_perm, const int32_t *off, c
       a.w2 = static_cast<const char *>(w->w1) + F * (d / 2);
       a.s2 = static_cast<const char *>(w->scale1) + F * (d / 64) * 2;
       a.b2 = static_cast<const char *>(w->bias1) + F * (d / 64) * 2;
+    } else if (c.weight_dtype == MOE_I8_CHANNEL) {
+      a.w2 = static_cast<const char *>(w->w1) + F * d;
+      a.s2 = static_cast<const char *>(w->scale1) + F * sizeof(float);
     } else {
       a.w2 = static_cast<const char *>(w->w1) + F * d * (c.weight_dtype == MOE_F32 ? 4 : 2);
     }
@@ -261,7 +276,8 @@ moe_status moe_validate(const moe_config *cfg) {
   if (c.weight_layout == MOE_LAYOUT_FUSED_GATE_UP && c.act != MOE_ACT_SWIGLU) return MOE_ERR_INVALID_ARG;
   if (c.fused_gather != 0 && c.fused_gather != 1) return MOE_ERR_INVALID_ARG;
   if (c.act_dtype != MOE_F32 && c.act_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
-  if (c.weight_dtype != MOE_F32 && c.weight_dtype != MOE_BF16 && c.weight_dtype != MOE_Q4_AFFINE_G64)
+  if (c.weight_dtype != MOE_F32 && c.weight_dtype != MOE_BF16 && c.weight_dtype != MOE_Q4_AFFINE_G64 &&
+      c.weight_dtype != MOE_I8_CHANNEL)
     return MOE_ERR_INVALID_ARG;
   if (c.shared_intermediate < 0) return MOE_ERR_INVALID_ARG;
   if (c.router == MOE_ROUTER_SOFTMAX_TOPK) {
@@ -282,12 +298,19 @@ moe_status moe_validate(const moe_config *cfg) {
   const bool f32 = c.act_dtype == MOE_F32 && c.weight_dtype == MOE_F32;
   const bool bf16 = c.act_dtype == MOE_BF16 && c.weight_dtype == MOE_BF16;
   const bool q4 = c.act_dtype == MOE_BF16 && c.weight_dtype == MOE_Q4_AFFINE_G64;
-  if (!f32 && !bf16 && !q4) return MOE_ERR_UNSUPPORTED;
+  const bool i8 = c.act_dtype == MOE_BF16 && c.weight_dtype == MOE_I8_CHANNEL;
+  if (!f32 && !bf16 && !q4 && !i8) return MOE_ERR_UNSUPPORTED;
   if (c.act_dtype == MOE_BF16 && (c.hidden % 8 != 0 || c.intermediate % 8 != 0)) return MOE_ERR_UNSUPPORTED;
   if (bf16 && (int64_t)c.num_experts * (c.intermediate > c.hidden ? c.intermediate : c.hidden) > INT32_MAX / 2)
     return MOE_ERR_UNSUPPORTED;
   if (q4 && (c.hidden % 64 != 0 || c.intermediate % 64 != 0 || c.act != MOE_ACT_SWIGLU))
     return MOE_ERR_UNSUPPORTED;
+  if (i8) {
+    if (c.hidden % 16 != 0 || c.intermediate % 16 != 0) return MOE_ERR_UNSUPPORTED;        // 16-byte rows of codes
+    if (c.hidden > kMaxI8K || c.intermediate > kMaxI8K) return MOE_ERR_UNSUPPORTED;        // exact int32 sums
+    const int64_t stride = c.hidden > 2LL * c.intermediate ? c.hidden : 2LL * c.intermediate;
+    if (c.num_experts * stride > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
+  }
   if (c.shared_intermediate > 0) {
     if (q4) return MOE_ERR_UNSUPPORTED;
     if (c.act_dtype == MOE_BF16 && c.shared_intermediate % 8 != 0) return MOE_ERR_UNSUPPORTED;
@@ -559,6 +582,59 @@ moe_status moe_grouped_ffn(const moe_config *cfg, const void *x_perm, const int3
   return do_ffn(c, x_perm, expert_offsets, w, y_perm, ws, s);
 }
 
+moe_status moe_quantize_rows(const void *x, int32_t dtype, int64_t rows, int32_t cols, int8_t *codes, float *scales,
+                             moe_stream_t stream) {
+  if (rows < 0 || cols < 1 || (dtype != MOE_F32 && dtype != MOE_BF16)) return MOE_ERR_INVALID_ARG;
+  if (cols % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
+  cudaError_t err = launch_quantize_rows(x, dtype == MOE_BF16, rows, cols, codes, scales,
+                                         reinterpret_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_quantize_rows");
+}
+
+static moe_status check_matmul(int32_t groups, int32_t rows, int32_t n, int32_t k) {
+  if (groups < 1 || rows < 0 || n < 1 || k < 1) return MOE_ERR_INVALID_ARG;
+  if (groups > kMaxExperts || k % 16 != 0 || k > kMaxI8K) return MOE_ERR_UNSUPPORTED;
+  if (rows > INT32_MAX / 2 || (int64_t)groups * n > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t moe_quantized_matmul_workspace_size(int32_t groups, int32_t rows, int32_t n, int32_t k) {
+  return check_matmul(groups, rows, n, k) == MOE_OK ? 256 : 0;
+}
+
+moe_status moe_quantized_matmul(int32_t groups, int32_t rows, int32_t n, int32_t k, const int8_t *x_codes,
+                                const float *x_scales, const int32_t *group_offsets, const int8_t *w_codes,
+                                const float *w_scales, int32_t out_dtype, void *out, void *ws, size_t ws_bytes,
+                                moe_stream_t stream) {
+  moe_status st = check_matmul(groups, rows, n, k);
+  if (st != MOE_OK) return st;
+  if (out_dtype != MOE_F32 && out_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (groups > 1 && !group_offsets) return MOE_ERR_INVALID_ARG;
+  if (!aligned16_or_null(group_offsets) || !aligned16(w_codes) || !aligned16(w_scales)) return MOE_ERR_INVALID_ARG;
+  if (rows > 0 && (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(out))) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(ws) || ws_bytes < moe_quantized_matmul_workspace_size(groups, rows, n, k)) return MOE_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if ((st = clear_status(ws, s)) != MOE_OK || rows == 0) return st;
+  MmI8Args m{};
+  m.offsets = group_offsets;
+  m.G = groups;
+  m.rows_cap = rows;
+  m.N = n;
+  m.K = k;
+  m.b_stride = n;
+  m.mode = out_dtype == MOE_F32 ? I8_F32 : I8_PLAIN;
+  m.q = x_codes;
+  m.xs = x_scales;
+  m.w0 = w_codes;
+  m.ws0 = w_scales;
+  m.out = out;
+  m.status = ws_ptr<int>(ws, 0);
+  cudaError_t err = launch_mm_i8(m, s);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_quantized_matmul");
+}
+
 moe_status moe_shared_expert(const moe_config *cfg, const void *x, const moe_weights *w, void *shared_out,
                              void *ws, size_t ws_bytes, moe_stream_t stream) {
   moe_status st = moe_validate(cfg);
@@ -606,8 +682,10 @@ static moe_status forward_impl(const moe_config &c, const void *x, const float *
   // with the fused gather, bf16 tensor-core experts read their token rows
   // straight from x: the permutation is built but no row is copied
   const bool fused_gather = c.weight_dtype == MOE_BF16 && c.fused_gather;
+  // 8-bit experts: the FFN's quantisation writes each token's codes to its slots' rows
+  const bool i8 = c.weight_dtype == MOE_I8_CHANNEL;
   int32_t *perm_token = ws_ptr<int32_t>(ws, L.perm_token);
-  void *x_perm = fused_gather ? nullptr : ws_ptr<char>(ws, L.x_perm);
+  void *x_perm = fused_gather || i8 ? nullptr : ws_ptr<char>(ws, L.x_perm);
   if ((st = do_permute(c, x, ids, wts, off, perm_token, ws_ptr<float>(ws, L.perm_w),
                        ws_ptr<int32_t>(ws, L.slot_row), x_perm, raw, kept, dropped, ws, s)) != MOE_OK)
     return st;
@@ -615,9 +693,10 @@ static moe_status forward_impl(const moe_config &c, const void *x, const float *
   void *y_perm = ws_ptr<char>(ws, L.y_perm);
   void *shared = c.shared_intermediate > 0 ? ws_ptr<char>(ws, L.shared_out) : nullptr;
   const bool shared_fused = shared && shared_in_grouped_gemm(c);
-  if ((st = do_ffn(c, fused_gather ? x : x_perm, off, w, y_perm, ws, s, g_nevents ? g_events[MOE_PHASE_FFN1] : nullptr,
-                   fused_gather ? perm_token : nullptr, shared_fused ? x : nullptr,
-                   shared_fused ? shared : nullptr)) != MOE_OK)
+  if ((st = do_ffn(c, fused_gather || i8 ? x : x_perm, off, w, y_perm, ws, s,
+                   g_nevents ? g_events[MOE_PHASE_FFN1] : nullptr, fused_gather ? perm_token : nullptr,
+                   shared_fused ? x : nullptr, shared_fused ? shared : nullptr,
+                   i8 ? ws_ptr<int32_t>(ws, L.slot_row) : nullptr)) != MOE_OK)
     return st;
   if ((err = mark(MOE_PHASE_FFN2, s)) != cudaSuccess) return cuda_fail(err, "phase event");
   if (shared && !shared_fused && (st = do_shared(c, x, w, shared, ws, s)) != MOE_OK) return st;
