@@ -509,6 +509,26 @@ moe_status moe_forward(const moe_config *cfg, const void *x, const float *w_rout
                        int32_t *topk_ids, float *topk_w, const moe_stats *stats, void *ws,
                        size_t ws_bytes, moe_stream_t stream);
 
+/* moe_forward for a few tokens (a decoding step between two sampled tokens):
+ * the whole layer, router to combine, in one kernel that streams the chosen
+ * experts' weights once.  Same arguments, outputs and semantics as
+ * moe_forward, for bf16 activations and at most MOE_FEW_TOKENS tokens (else
+ * MOE_ERR_UNSUPPORTED, the reason in moe_last_error()), with bf16, 4-bit or
+ * 8-bit experts, either layout, with or without a shared expert.
+ * Results agree with moe_forward's within bf16 rounding, not bit for bit: ids
+ * can differ only for tokens whose selection margin is within 1e-4, expert
+ * outputs are kept in fp32 up to the combine, and the intermediate keeps 16
+ * significant bits (8-bit experts: bf16, which is then quantised).
+ * A token whose router scores are NaN chooses no expert: ids -1, and a device
+ * status.  The kernel's blocks wait for one another, so it is launched
+ * cooperatively: it starts when every SM has room for its block, and two
+ * such calls on different streams run one after the other.  No phase events
+ * are recorded.  Uses ws. */
+#define MOE_FEW_TOKENS 16
+moe_status moe_forward_few(const moe_config *cfg, const void *x, const float *w_router, const float *router_bias,
+                           const moe_weights *w, void *out, int32_t *topk_ids, float *topk_w, const moe_stats *stats,
+                           void *ws, size_t ws_bytes, moe_stream_t stream);
+
 /* moe_forward with the activations on the HOST: copies x_host [T,d] to the
  * device, runs the layer and copies back out_host [T,d] plus, when not NULL,
  * kept_counts_host [E], prob_sum_host [E] and dropped_host [1] (what the

@@ -26,6 +26,8 @@ MOE_PHASE_START, MOE_PHASE_ROUTE, MOE_PHASE_PERMUTE, MOE_PHASE_FFN1, MOE_PHASE_F
 # moe_ws_region
 MOE_WS_OFFSETS, MOE_WS_PERM_TOKEN, MOE_WS_PERM_W, MOE_WS_SLOT_ROW, MOE_WS_X_PERM, MOE_WS_H, MOE_WS_Y_PERM, \
     MOE_WS_SHARED_H, MOE_WS_SHARED_OUT, MOE_WS_ROUTER_LOGITS, MOE_WS_REGION_COUNT = range(11)
+# most tokens of moe_forward_few
+MOE_FEW_TOKENS = 16
 # moe_router_kind
 MOE_ROUTER_SOFTMAX_TOPK = 0
 MOE_ROUTER_SIGMOID_GROUP = 1
@@ -112,6 +114,7 @@ SIGNATURES = {
     "moe_shared_expert": (C.c_int, [_CFG, _P, _W, _P, _P, C.c_size_t, _P]),
     "moe_combine": (C.c_int, [_CFG, _P, _P, _P, _P, _P, _P]),
     "moe_forward": (C.c_int, [_CFG, _P, _P, _P, _W, _P, _P, _P, _S, _P, C.c_size_t, _P]),
+    "moe_forward_few": (C.c_int, [_CFG, _P, _P, _P, _W, _P, _P, _P, _S, _P, C.c_size_t, _P]),
     "moe_forward_host": (C.c_int, [_CFG, _P, _P, _P, _W, _P, _P, _P, _P, _P, C.c_size_t, _P]),
 }
 

@@ -290,6 +290,18 @@ def moe_forward(cfg, x, w_router, router_bias, weights: dict, out, topk_ids, top
                               _nbytes(ws), _s(stream)), "moe_forward")
 
 
+def moe_forward_few(cfg, x, w_router, router_bias, weights: dict, out, topk_ids, topk_w, stats, ws, stream=None):
+    """``moe_forward`` for at most ``MOE_FEW_TOKENS`` tokens, in one kernel."""
+    w = _weights_struct(weights)
+    st = _stats_struct(stats)
+    code = L.lib().moe_forward_few(C.byref(cfg), _p(x), _p(w_router), _p(router_bias), C.byref(w), _p(out),
+                                   _p(topk_ids), _p(topk_w), C.byref(st) if st is not None else None, _p(ws),
+                                   _nbytes(ws), _s(stream))
+    if code == L.MOE_ERR_UNSUPPORTED:
+        raise L.MoEError(code, "moe_forward_few: " + (L.lib().moe_last_error().decode() or "unsupported"))
+    check(code, "moe_forward_few")
+
+
 def moe_forward_host(cfg, x_host, w_router, router_bias, weights: dict, out_host, kept_counts_host,
                      prob_sum_host, dropped_host, ws, stream=None):
     w = _weights_struct(weights)
@@ -370,6 +382,14 @@ class MoELayer:
         if st["shared"] is not None:
             moe_shared_expert(cfg, x, self.weights, st["shared"], self.ws, stream)
         moe_combine(cfg, st["y_perm"], st["slot_row"], o.topk_w, st["shared"], o.out, stream)
+        return o
+
+    def forward_few(self, x: torch.Tensor, stream=None) -> Outputs:
+        """One layer forward in a single kernel, for layers of at most
+        ``MOE_FEW_TOKENS`` tokens (moe_forward_few)."""
+        o = self.o
+        moe_forward_few(self.cfg, x, self.w_router, self.router_bias, self.weights, o.out, o.topk_ids, o.topk_w,
+                        self.stats(), self.ws, stream)
         return o
 
     def update_bias(self, coeff: float, stream=None) -> None:

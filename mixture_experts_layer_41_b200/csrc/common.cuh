@@ -18,6 +18,7 @@ constexpr int kPermTokens = 256;      // tokens per dispatch count block
 constexpr int kMaxExperts = 256;
 constexpr int kMaxTopK = 32;
 constexpr int kMaxGroups = 32;
+constexpr int kFewTokens = 16;        // most tokens of moe_forward_few
 constexpr int kMaxI8K = 131056;       // 8-bit products: K * 128 * 128 stays below 2^31
 
 // ---------------------------------------------------------------- device status
@@ -144,6 +145,9 @@ __device__ __forceinline__ bool warp_group_offsets(const int32_t *src, int n, in
 size_t route_logits_bytes(const moe_config &c);       // defined in router.cu
 size_t route_logits_f64_bytes(const moe_config &c);   // its float64 logits partials [ks][T][E]
 
+bool few_supported(const moe_config &c);              // defined in few.cu
+size_t few_bytes(const moe_config &c);                // its workspace (0: not supported)
+
 // ---------------------------------------------------------------- workspace
 struct WsLayout {
   size_t status;       // int32[64]
@@ -171,6 +175,7 @@ struct WsLayout {
   size_t out_stage;    // act[T][d]
   size_t q_rows;       // int8[T*k][max(d, F)]  8-bit experts: codes of the rows a product reads
   size_t q_scale;      // float[T*k]            and their scales
+  size_t few;          // moe_forward_few's intermediates
   size_t total;
   size_t region_bytes[MOE_WS_REGION_COUNT];   // unpadded sizes of the moe_ws_region buffers
 };
@@ -237,6 +242,7 @@ inline WsLayout ws_layout(const moe_config &c) {
   L.out_stage = take(es * T * d);
   L.q_rows = take(i8 ? slots * (d > F ? d : F) : 0);
   L.q_scale = take(i8 ? sizeof(float) * slots : 0);
+  L.few = take(few_bytes(c));
   L.total = off;
   return L;
 }
@@ -395,6 +401,26 @@ struct MmI8Args {
 cudaError_t launch_mm_i8_tc(const MmI8Args &a, cudaStream_t s);
 cudaError_t launch_mm_i8(const MmI8Args &a, cudaStream_t s);     // picks the kernel
 cudaError_t launch_ffn_i8(const FfnArgs &a, cudaStream_t s);
+
+// The whole layer for at most kFewTokens tokens in one cooperative kernel (few.cu).
+struct FewArgs {
+  const moe_config *cfg;
+  int64_t capacity;
+  const void *x;
+  const float *w_router, *router_bias;
+  const void *w1, *w2, *w3;
+  const void *s1, *s2, *s3, *b1, *b2, *b3;
+  int w_stride;
+  const void *shared_w1, *shared_w2, *shared_w3;
+  void *out;
+  int32_t *ids;
+  float *wts;
+  int32_t *raw_counts, *kept_counts, *dropped;
+  float *prob_sum;
+  int *status;              // the workspace's first 256 bytes, zeroed: status word and barrier counters
+  void *ws;                 // few_bytes() bytes
+};
+cudaError_t launch_few(const FewArgs &a, cudaStream_t s);
 
 // Replaces the text moe_last_error() returns on this thread.
 void set_last_error_text(const char *text);

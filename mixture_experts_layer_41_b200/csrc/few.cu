@@ -1,0 +1,1248 @@
+// The whole layer for a few tokens (at most 16) in one cooperative kernel.
+//
+// Between two sampled tokens a server runs the layer on a handful of rows:
+// nearly all of its time is reading the chosen experts' weights once.  The
+// staged layer spends 9-10 launches on it and gives each weight tile a
+// 128-row operand; here one persistent block per SM streams weight rows
+// through shared memory without a pause, from the first product to the last.
+//
+//   router    each warp dots one expert's slice of the hidden dimension with
+//             every token (fp32 products over runs of 8, float64 sums);
+//   choice    after a grid barrier every block selects for all tokens from
+//             the same partial sums (float64, ties to the lower expert) and
+//             builds the same plan: per expert a 16-bit mask of its tokens in
+//             token order, cut to the capacity;
+//   phase 1   tasks of 16 weight rows: 8 gate rows and the 8 up rows of the
+//             same features (ReLU: 16 rows), times the expert's tokens;
+//   phase 2   tasks of 16 rows of the down projection, times h;
+//   combine   after a last grid barrier: out = sum_j w_j y_j (+ shared).
+//
+// A block is one producer warp and eight consumer warps.  The producer copies
+// rows, 1024 bytes of each of a task's 16 at a time, into a ring of stages
+// (cp.async.bulk, one mbarrier per stage) and runs ahead of the consumers
+// across tasks, phases and grid barriers: the ring is full of the next
+// phase's weights when a barrier opens, and of the shared expert's while the
+// router runs.  The row pitch in shared memory is 64 bytes more than a
+// multiple of 128 (32 for 4-bit codes), so a warp reads its matrix fragments
+// straight from the copied rows without bank conflicts.
+// The consumers split a stage's K into 64-byte segments; per segment a thread
+// takes 16 bytes of weight rows g and g + 8 and of token g's row, which is
+// one A and one B operand of mma.sync m16n8 for a permuted order of K (a sum
+// over K has no order).  mma.sync is the right unit here: 8 tokens are its N,
+// and at a row of weights per 23 bytes a clock it is idle most of the time.
+// The eight partial 16 x 8 results meet in shared memory.
+//
+// Precision: bf16 and 4-bit weights take h as the sum of two bf16 (16 bits),
+// 4-bit codes are multiplied as exact small integers and scaled per group of
+// 64 in fp32 (w = s q + b: s sum(q x) + b sum(x)), expert outputs stay fp32
+// until the combine: one rounding to bf16, at the end.  8-bit weights follow
+// the 8-bit layer's definition (rows of x and of the bf16 h quantised).
+//
+// Results do not depend on timing: every sum has a fixed order, and the row
+// maxima behind the 8-bit codes of h are integer maxima.
+// Bound by HBM.  All waits are bounded (moe_set_wait_timeout_ns): one that runs
+// out records a status and turns every later wait of its block into a
+// no-op, so the block runs through its (in-bounds) work, meets every barrier
+// and ends.
+#include "tc_ptx.cuh"
+
+#include <math.h>
+
+namespace moe {
+namespace {
+
+using namespace ptx;
+
+constexpr int CW = 8;                       // consumer warps
+constexpr int CT = 32 * CW;
+constexpr int THREADS = CT + 32;
+constexpr int CH = 1024;                    // bytes of a row per stage
+constexpr int ROWS = 16;                    // weight rows per task
+constexpr int STAGE_BYTES = ROWS * (CH + 64);
+constexpr int MAX_STAGES = 12;
+constexpr int MAX_SC = 12;                  // 4-bit: tasks whose scales and biases are held at once
+constexpr int SC_BYTES = 40 * 1024;         // and the shared memory they may take (two tasks at least)
+constexpr int MAX_T = kFewTokens;
+constexpr int MAX_SLOTS = MAX_T * kMaxTopK;
+constexpr int SMEM_LIMIT = 227 * 1024;
+
+enum Fmt { BF16 = 0, I8 = 1, Q4 = 2 };
+
+__host__ __device__ constexpr int pitch_of(int fmt) { return CH + (fmt == Q4 ? 32 : 64); }
+
+struct FewParams {
+  uint64_t timeout_ns;
+  int T, d, F, E, k, Fs;
+  int router, norm;
+  double scaling;
+  int n_group, topk_group;
+  int cap;                                  // slots an expert keeps, -1: all
+  int swiglu;
+  const uint16_t *x;
+  const float *w_router, *bias;
+  const void *w1, *w2, *w3;
+  const void *s1, *s2, *s3, *b1, *b2, *b3;
+  int w_stride;                             // w1 / w2 rows from one expert to the next
+  const uint16_t *sw1, *sw2, *sw3;          // shared expert, bf16
+  uint16_t *out;
+  int32_t *ids;
+  float *wts;
+  int32_t *raw_counts, *kept_counts, *dropped;
+  float *prob_sum;
+  // workspace
+  int *status;
+  unsigned *bar;                            // grid barrier counters, zeroed before the launch
+  double *part;                             // [ks][T][E] partial logits
+  int ks, kslice;
+  int8_t *xq;                               // 8-bit: [T][d] codes and scales of x
+  float *xs;
+  uint16_t *h;                              // [T*k][F], the low parts h_lo elements further
+  size_t h_lo;
+  uint16_t *hs;                             // [T][Fs] of the shared expert, likewise
+  size_t hs_lo;
+  unsigned *rowmax;                         // 8-bit: [T*k] largest |h| of a row, as fp32 bits
+  int8_t *hq;                               // 8-bit: [T*k][F]
+  float *y;                                 // [T*k + T][d] expert outputs, then the shared expert's
+  int stages;
+  int sc_slot, sc_slots;                    // 4-bit: bytes of one task's scales and biases, and how many are held
+};
+
+struct Shared {
+  uint64_t full[MAX_STAGES];
+  uint64_t empty[MAX_STAGES];
+  uint64_t sc_full[MAX_SC], sc_empty[MAX_SC];
+  uint64_t plan;
+  int abort_flag;
+  int nact;                                 // experts with rows
+  uint32_t mask[kMaxExperts];               // tokens an expert keeps
+  int16_t act[kMaxExperts];                 // the experts with rows
+  int16_t row0[kMaxExperts + 1];            // first row of active expert i
+  int sel_id[MAX_SLOTS];
+  float sel_w[MAX_SLOTS];
+  int16_t slot_row[MAX_SLOTS];
+  // partial results of the consumer warps, two tasks in turn; scratch of the choice
+  __align__(16) uint32_t red[2][CW][2][32][4];
+};
+static_assert(sizeof(((Shared *)0)->red) >= CW * kMaxExperts * sizeof(double), "selection scratch");
+
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(CT) : "memory"); }
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// ---------------------------------------------------------------- grid barrier
+// Arrival and wait are apart, so work that does not depend on the other blocks
+// can run between them.  Both are called by all consumer threads.
+__device__ __forceinline__ void grid_arrive(unsigned *ctr) {
+  consumer_sync();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(ctr) : "memory");
+  }
+}
+__device__ __forceinline__ void grid_wait(unsigned *ctr, volatile int *abort_flag, const FewParams &p) {
+  if (threadIdx.x == 0) {
+    const uint64_t t0 = global_ns();
+    uint32_t spins = 0;
+    for (;;) {
+      unsigned v;
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(ctr) : "memory");
+      if (v >= gridDim.x || *abort_flag) break;
+      if (((++spins & 31u) == 0 || p.timeout_ns < 1000u) && global_ns() - t0 > p.timeout_ns) {
+        *abort_flag = 1;
+        record_status(p.status, kDevTimeoutEpilogue);
+        break;
+      }
+    }
+    __threadfence();
+  }
+  consumer_sync();
+}
+
+// ---------------------------------------------------------------- tasks
+// One task: 16 weight rows.  The order of a block's tasks is the same for the
+// producer and the consumers: shared phase 1, routed phase 1, shared phase 2,
+// routed phase 2, each strided over the blocks, the stride running on from
+// one part to the next.
+enum Part { S1 = 0, R1 = 1, S2 = 2, R2 = 3 };
+
+struct Dims {
+  int nb;        // row blocks per expert
+  int count;     // tasks of the part
+  int first;     // this block's first
+};
+
+__device__ __forceinline__ Dims part_dims(const FewParams &p, int part, int nact) {
+  const int nbs1 = p.Fs / 8, nbs2 = p.Fs ? (p.d + ROWS - 1) / ROWS : 0;
+  const int nb1 = p.swiglu ? p.F / 8 : (p.F + ROWS - 1) / ROWS, nb2 = (p.d + ROWS - 1) / ROWS;
+  const int counts[4] = {nbs1, nact * nb1, nbs2, nact * nb2};
+  const int nbs[4] = {nbs1, nb1, nbs2, nb2};
+  long long before = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < part) before += counts[i];
+  Dims r;
+  r.nb = nbs[part];
+  r.count = counts[part];
+  const int skip = (int)(before % gridDim.x);
+  r.first = ((int)blockIdx.x - skip + (int)gridDim.x) % (int)gridDim.x;
+  return r;
+}
+
+template <int FMT>
+__device__ __forceinline__ int row_bytes(int K) {
+  return FMT == BF16 ? 2 * K : (FMT == I8 ? K : K / 2);
+}
+
+// Weight rows of a task: rows 0-7 from w0, 8-15 from w1, both `bytes` long
+struct Src {
+  const char *w0, *w1;
+  int n0, n1;                               // valid rows of each half
+  size_t r0, r1;                            // row index of each half's first (channel scales)
+};
+
+template <int FMT>
+__device__ __forceinline__ Src task_src(const FewParams &p, int part, int e, int b) {
+  Src s;
+  if (part == S1 || part == R1) {
+    const size_t base = part == S1 ? 0 : (size_t)e * p.w_stride;
+    const size_t rb = row_bytes<FMT>(p.d);
+    const char *g = static_cast<const char *>(part == S1 ? (const void *)p.sw1 : p.w1);
+    const char *u = static_cast<const char *>(part == S1 ? (const void *)p.sw2 : p.w2);
+    if (part == S1 || p.swiglu) {
+      s.r0 = s.r1 = base + (size_t)b * 8;
+      s.w0 = g + s.r0 * rb;
+      s.w1 = u + s.r1 * rb;
+      s.n0 = s.n1 = 8;
+    } else {
+      s.r0 = base + (size_t)b * ROWS;
+      s.r1 = s.r0 + 8;
+      s.w0 = g + s.r0 * rb;
+      s.w1 = g + s.r1 * rb;
+      s.n0 = min(8, p.F - b * ROWS);
+      s.n1 = max(0, min(8, p.F - b * ROWS - 8));
+    }
+  } else {
+    const size_t base = part == S2 ? 0 : (size_t)e * p.d;
+    const size_t rb = row_bytes<FMT>(part == S2 ? p.Fs : p.F);
+    const char *w = static_cast<const char *>(part == S2 ? (const void *)p.sw3 : p.w3);
+    s.r0 = base + (size_t)b * ROWS;
+    s.r1 = s.r0 + 8;
+    s.w0 = w + s.r0 * rb;
+    s.w1 = w + s.r1 * rb;
+    s.n0 = min(8, p.d - b * ROWS);
+    s.n1 = max(0, min(8, p.d - b * ROWS - 8));
+  }
+  return s;
+}
+
+// ---------------------------------------------------------------- producer
+struct Ring {
+  Shared *sh;
+  uint8_t *tiles;
+  uint8_t *sc;                              // 4-bit: the slots of scales and biases
+  uint32_t it, sc_it;                       // stages / scale slots used so far
+  bool ok;
+};
+
+template <int FMT>
+__device__ __forceinline__ void produce_part(const FewParams &p, Ring &r, int part, int nact) {
+  const Dims dm = part_dims(p, part, nact);
+  const int lane = threadIdx.x & 31;
+  volatile int *abort_flag = &r.sh->abort_flag;
+  const int K = part == S1 || part == R1 ? p.d : (part == S2 ? p.Fs : p.F);
+  const int rb = row_bytes<FMT>(K);
+  for (int task = dm.first; task < dm.count && r.ok; task += gridDim.x) {
+    const int i = task / dm.nb, b = task - i * dm.nb;
+    const Src s = task_src<FMT>(p, part, part == R1 || part == R2 ? r.sh->act[i] : 0, b);
+    const bool mine = lane < 8 ? lane < s.n0 : (lane < ROWS && lane - 8 < s.n1);
+    const char *row = lane < 8 ? s.w0 + (size_t)lane * rb : s.w1 + (size_t)(lane - 8) * rb;
+    if (FMT == Q4) {
+      // scales and biases of the task's two blocks of 8 rows, each contiguous
+      const int slot = r.sc_it % p.sc_slots;
+      int good = 1;
+      if (lane == 0)
+        good = wait_bounded(&r.sh->sc_empty[slot], ((r.sc_it / p.sc_slots) & 1u) ^ 1u, abort_flag, p.status,
+                            kDevTimeoutProducer, p.timeout_ns) &&
+               !*abort_flag;
+      if (!__shfl_sync(0xffffffffu, good, 0)) {
+        r.ok = false;
+        break;
+      }
+      const int blk = K / 64 * 2 * 8;       // bytes: a multiple of 16
+      if (lane == 0) mbar_expect_tx(&r.sh->sc_full[slot], 4 * blk);
+      __syncwarp();
+      if (lane < 4) {
+        const char *base = static_cast<const char *>(
+            part == R2 ? (lane & 1 ? p.b3 : p.s3)
+                       : (lane < 2 ? (lane & 1 ? p.b1 : p.s1) : (lane & 1 ? p.b2 : p.s2)));
+        const size_t row_i = lane < 2 ? s.r0 : s.r1;
+        bulk_load(smem_u32(r.sc + (size_t)slot * p.sc_slot + lane * blk), base + row_i * (size_t)(K / 64 * 2), blk,
+                  smem_u32(&r.sh->sc_full[slot]));
+      }
+      ++r.sc_it;
+    }
+    for (int off = 0; off < rb; off += CH, ++r.it) {
+      const int st = r.it % p.stages;
+      int good = 1;
+      if (lane == 0)
+        // a consumer that gave up releases stages it did not wait for, having
+        // raised the flag first: nothing may be copied into them
+        good = wait_bounded(&r.sh->empty[st], ((r.it / p.stages) & 1u) ^ 1u, abort_flag, p.status, kDevTimeoutProducer,
+                            p.timeout_ns) &&
+               !*abort_flag;
+      if (!__shfl_sync(0xffffffffu, good, 0)) {
+        r.ok = false;
+        break;
+      }
+      const uint32_t bytes = min(CH, rb - off);
+      if (lane == 0) mbar_expect_tx(&r.sh->full[st], bytes * (s.n0 + s.n1));
+      __syncwarp();
+      if (mine)
+        bulk_load(smem_u32(r.tiles + (size_t)st * STAGE_BYTES + lane * pitch_of(FMT)), row + off, bytes,
+                  smem_u32(&r.sh->full[st]));
+    }
+  }
+}
+
+// ---------------------------------------------------------------- consumers
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t bf2_sub(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// nibbles i and i + 4 of a code word as an exact bf16 pair
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) {
+  const uint32_t magic = 0x43004300u;       // bf16 128.0 in both halves
+  return bf2_sub(((w >> (4 * i)) & 0x000F000Fu) | magic, magic);
+}
+__device__ __forceinline__ uint4 lds128(const uint8_t *p) { return *reinterpret_cast<const uint4 *>(p); }
+
+// B operand of one 64-byte segment of weight rows.  bf16 and 8-bit: 16 bytes
+// of the token row (and of its low part).  4-bit: a segment is two groups of
+// 64 codes; 16 elements of the token row per group.
+template <int FMT, bool LO>
+struct BSeg {
+  uint4 v[FMT == Q4 ? 4 : 1][LO ? 2 : 1];
+};
+
+constexpr int SEGS = CH / 64 / CW;          // segments per warp and stage
+
+// Where a task's B operand comes from, per lane: token row g (and g + 8)
+template <int NB>
+struct BSrc {
+  const char *row[NB];                      // null: no such token
+};
+
+// wo: byte of the weight row at which this warp's segment starts
+template <int FMT, bool LO>
+__device__ __forceinline__ void load_b(BSeg<FMT, LO> &bv, const char *row, size_t lo_bytes, int wo, int rb, int c) {
+  // bytes of the token row per byte of the weight row
+  constexpr int R = FMT == Q4 ? 4 : 1;
+#pragma unroll
+  for (int q = 0; q < (FMT == Q4 ? 4 : 1); ++q) {
+    // 4-bit: group q / 2 of the segment, elements 16 c + 8 (q % 2) ..
+    const int at = wo + (FMT == Q4 ? (q >> 1) * 32 + c * 8 + (q & 1) * 4 : c * 16);
+    const bool ok = row != nullptr && at < rb;
+    const char *a = row + (size_t)at * R;
+#pragma unroll
+    for (int l = 0; l < (LO ? 2 : 1); ++l)
+      bv.v[q][l] = ok ? __ldcg(reinterpret_cast<const uint4 *>(a + (l ? lo_bytes : 0))) : make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+template <int FMT, int NB>
+struct Acc {
+  float f[NB][4];
+};
+template <int NB>
+struct Acc<I8, NB> {
+  int f[NB][4];
+};
+
+// One 64-byte segment of the 16 rows (seg: its first byte in the stage, left:
+// valid bytes of the stage) times the tokens.  The first NBP blocks of eight
+// tokens have their operand in registers; a further one (4-bit weights, whose
+// operand is four times as long, and only for an expert that more than eight
+// tokens chose) fetches it here.
+template <int FMT, bool LO, int NB, int NBP>
+__device__ __forceinline__ void consume(Acc<FMT, NB> &acc, const BSeg<FMT, LO> (&bv)[NBP], const BSrc<NB> &src,
+                                        size_t lo_bytes, const uint8_t *tile, int seg, int left, int off, int rb, int rows,
+                                        int g, int c, const uint8_t *sc, int groups) {
+  constexpr int P = pitch_of(FMT);
+  if constexpr (FMT != Q4) {
+    uint4 lo = lds128(tile + g * P + seg + c * 16), hi = lds128(tile + (g + 8) * P + seg + c * 16);
+    if (seg + c * 16 >= left) lo = hi = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      if (n > 0 && rows <= 8) break;
+#pragma unroll
+      for (int l = 0; l < (LO ? 2 : 1); ++l) {
+        const uint4 b = bv[n].v[0][l];
+        if constexpr (FMT == BF16) {
+          mma_bf16(acc.f[n], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+          mma_bf16(acc.f[n], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+        } else {
+          mma_s8(acc.f[n], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+          mma_s8(acc.f[n], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+        }
+      }
+    }
+  } else {
+    const uint16_t *t = reinterpret_cast<const uint16_t *>(sc);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int go = seg + q * 32;
+      if (go >= left) break;
+      const uint2 lo = *reinterpret_cast<const uint2 *>(tile + g * P + go + c * 8);
+      const uint2 hi = *reinterpret_cast<const uint2 *>(tile + (g + 8) * P + go + c * 8);
+      // scale and bias of rows g and g + 8 for this group
+      const int gi = (off + go) / 32;
+      const float s_lo = bf16_to_f32(t[g * groups + gi]), b_lo = bf16_to_f32(t[(8 + g) * groups + gi]);
+      const float s_hi = bf16_to_f32(t[(16 + g) * groups + gi]), b_hi = bf16_to_f32(t[(24 + g) * groups + gi]);
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        if (n > 0 && rows <= 8) break;
+        BSeg<FMT, LO> own;
+        if (n >= NBP) load_b<FMT, LO>(own, src.row[n], lo_bytes, off + seg, rb, c);
+        float dq[4] = {0.f, 0.f, 0.f, 0.f}, dx[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t wl = u ? lo.y : lo.x, wh = u ? hi.y : hi.x;
+          constexpr uint32_t one = 0x3F803F80u;
+#pragma unroll
+          for (int l = 0; l < (LO ? 2 : 1); ++l) {
+            // elements (i, i + 4) of the token's 8, in the order of the nibble pairs
+            const uint4 b = n < NBP ? bv[n < NBP ? n : 0].v[2 * q + u][l] : own.v[2 * q + u][l];
+            const uint32_t p0 = __byte_perm(b.x, b.z, 0x5410), p1 = __byte_perm(b.x, b.z, 0x7632);
+            const uint32_t p2 = __byte_perm(b.y, b.w, 0x5410), p3 = __byte_perm(b.y, b.w, 0x7632);
+            mma_bf16(dq, code_pair(wl, 0), code_pair(wh, 0), code_pair(wl, 1), code_pair(wh, 1), p0, p1);
+            mma_bf16(dq, code_pair(wl, 2), code_pair(wh, 2), code_pair(wl, 3), code_pair(wh, 3), p2, p3);
+            mma_bf16(dx, one, one, one, one, p0, p1);
+            mma_bf16(dx, one, one, one, one, p2, p3);
+          }
+        }
+        acc.f[n][0] = fmaf(s_lo, dq[0], fmaf(b_lo, dx[0], acc.f[n][0]));
+        acc.f[n][1] = fmaf(s_lo, dq[1], fmaf(b_lo, dx[1], acc.f[n][1]));
+        acc.f[n][2] = fmaf(s_hi, dq[2], fmaf(b_hi, dx[2], acc.f[n][2]));
+        acc.f[n][3] = fmaf(s_hi, dq[3], fmaf(b_hi, dx[3], acc.f[n][3]));
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float silu_f(float g) { return g / (1.f + expf(-g)); }
+
+// n-th set bit of a mask (the mask has more than n)
+__device__ __forceinline__ int nth_bit(uint32_t m, int n) {
+  for (int i = 0; i < n; ++i) m &= m - 1;
+  return __ffs(m) - 1;
+}
+
+struct Cursor {
+  int task, e, rows, row0, b;               // row0: first row of h / y
+  uint32_t mask;
+};
+
+template <int PART>
+__device__ __forceinline__ void place(const FewParams &p, const Shared *sh, const Dims &dm, Cursor &cu) {
+  const int i = cu.task / dm.nb;
+  cu.b = cu.task - i * dm.nb;
+  if (PART == S1 || PART == S2) {
+    cu.e = 0;
+    cu.mask = (1u << p.T) - 1u;
+    cu.row0 = 0;
+    cu.rows = p.T;
+  } else {
+    cu.e = sh->act[i];
+    cu.mask = sh->mask[cu.e];
+    cu.row0 = sh->row0[i];
+    cu.rows = sh->row0[i + 1] - cu.row0;
+  }
+}
+
+template <int FMT, int PART, int NB>
+__device__ __forceinline__ BSrc<NB> b_src(const FewParams &p, const Cursor &cu, int g) {
+  BSrc<NB> s;
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    const int r = g + 8 * n;
+    s.row[n] = nullptr;
+    if (r < cu.rows) {
+      if (PART == S1 || PART == R1) {
+        const int t = PART == S1 ? r : nth_bit(cu.mask, r);
+        s.row[n] = FMT == I8 ? reinterpret_cast<const char *>(p.xq + (size_t)t * p.d)
+                             : reinterpret_cast<const char *>(p.x + (size_t)t * p.d);
+      } else if (PART == S2) {
+        s.row[n] = reinterpret_cast<const char *>(p.hs + (size_t)r * p.Fs);
+      } else {
+        s.row[n] = FMT == I8 ? reinterpret_cast<const char *>(p.hq + (size_t)(cu.row0 + r) * p.F)
+                             : reinterpret_cast<const char *>(p.h + (size_t)(cu.row0 + r) * p.F);
+      }
+    }
+  }
+  return s;
+}
+
+// The block's tasks of one part.  ITEMS: FMT of the weights read.
+template <int FMT, int PART, int NB>
+__device__ __forceinline__ void consume_part(const FewParams &p, Ring &r, uint32_t &red_it) {
+  Shared *sh = r.sh;
+  constexpr bool PHASE2 = PART == S2 || PART == R2;
+  constexpr bool LO = PHASE2 && FMT != I8;
+  const Dims dm = part_dims(p, PART, sh->nact);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int K = !PHASE2 ? p.d : (PART == S2 ? p.Fs : p.F);
+  const int rb = row_bytes<FMT>(K);
+  const size_t lo_bytes = 2 * (PART == S2 ? p.hs_lo : p.h_lo);
+  volatile int *abort_flag = &sh->abort_flag;
+  if (dm.first >= dm.count) return;
+
+  constexpr int NBP = FMT == Q4 ? 1 : NB;
+  const int groups = K / 64;
+  Cursor cu;
+  cu.task = dm.first;
+  place<PART>(p, sh, dm, cu);
+  BSrc<NB> bs = b_src<FMT, PART, NB>(p, cu, g);
+  BSeg<FMT, LO> bv[SEGS][NBP];
+#pragma unroll
+  for (int s = 0; s < SEGS; ++s)
+#pragma unroll
+    for (int n = 0; n < NBP; ++n) load_b<FMT, LO>(bv[s][n], bs.row[n], lo_bytes, (warp + CW * s) * 64, rb, c);
+
+  for (;;) {
+    Acc<FMT, NB> acc;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc.f[n][j] = 0;
+    Cursor nx = cu;
+    nx.task += gridDim.x;
+    const bool more = nx.task < dm.count;
+    const uint8_t *sc = nullptr;
+    if (FMT == Q4) {
+      const int slot = r.sc_it % p.sc_slots;
+      wait_bounded(&sh->sc_full[slot], (r.sc_it / p.sc_slots) & 1u, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns);
+      sc = r.sc + (size_t)slot * p.sc_slot;
+    }
+    for (int off = 0; off < rb; off += CH, ++r.it) {
+      // where the next stage's token operand comes from: its loads take the
+      // registers of each segment as soon as that has been used
+      const bool last = off + CH >= rb;
+      BSrc<NB> bn = bs;
+      if (last && more) {
+        place<PART>(p, sh, dm, nx);
+        bn = b_src<FMT, PART, NB>(p, nx, g);
+      }
+      const int next_off = last ? 0 : off + CH;
+      const int st = r.it % p.stages;
+      const uint8_t *tile = r.tiles + (size_t)st * STAGE_BYTES;
+      const int left = min(CH, rb - off);
+      wait_bounded(&sh->full[st], (r.it / p.stages) & 1u, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns);
+      __syncwarp();
+#pragma unroll
+      for (int s = 0; s < SEGS; ++s) {
+        const int seg = (warp + CW * s) * 64;
+        if (seg < left)
+          consume<FMT, LO, NB, NBP>(acc, bv[s], bs, lo_bytes, tile, seg, left, off, rb, cu.rows, g, c, sc, groups);
+        if (!last || more) {
+#pragma unroll
+          for (int n = 0; n < NBP; ++n) load_b<FMT, LO>(bv[s][n], bn.row[n], lo_bytes, next_off + seg, rb, c);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->empty[st]);
+      if (last) bs = bn;
+    }
+    // the eight warps' partial results meet; two buffers in turn, so one
+    // barrier per task keeps writers and readers apart
+    uint32_t(*red)[2][32][4] = sh->red[red_it & 1u];
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+      *reinterpret_cast<uint4 *>(red[warp][n][lane]) =
+          FMT == I8 ? make_uint4((uint32_t)acc.f[n][0], (uint32_t)acc.f[n][1], (uint32_t)acc.f[n][2],
+                                 (uint32_t)acc.f[n][3])
+                    : make_uint4(__float_as_uint((float)acc.f[n][0]), __float_as_uint((float)acc.f[n][1]),
+                                 __float_as_uint((float)acc.f[n][2]), __float_as_uint((float)acc.f[n][3]));
+    consumer_sync();
+    if (FMT == Q4) {
+      if (threadIdx.x == 0) mbar_arrive(&sh->sc_empty[r.sc_it % p.sc_slots]);
+      ++r.sc_it;
+    }
+    ++red_it;
+    // value (row, token) of the task: accumulator j of lane 4 (row % 8) + (token % 8) / 2
+    auto total = [&](int row, int tok) {
+      const int ln = (row & 7) * 4 + ((tok & 7) >> 1), j = (tok & 1) + (row >> 3) * 2, n = tok >> 3;
+      if (FMT == I8) {
+        int v = 0;
+#pragma unroll
+        for (int w = 0; w < CW; ++w) v += (int)red[w][n][ln][j];
+        return (float)v;
+      }
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < CW; ++w) v += __uint_as_float(red[w][n][ln][j]);
+      return v;
+    };
+    const bool pairs = PART == S1 || (PART == R1 && p.swiglu);
+    const int cols = pairs ? 8 : ROWS;
+    const int N = PART == S1 ? p.Fs : (PART == R1 ? p.F : p.d);
+    for (int i = threadIdx.x; i < cols * 8 * NB; i += CT) {       // whole warps take part
+      const int tok = i / cols, f = i - tok * cols, col = cu.b * cols + f;
+      const bool live = tok < cu.rows && col < N;
+      const size_t row = (size_t)cu.row0 + tok;
+      float v = 0.f;
+      if (live) {
+        v = total(f, tok);
+        float xs = 1.f;
+        size_t r0 = 0;
+        if (FMT == I8) {
+          // row scale: of the token (phase 1), of the row of h (phase 2)
+          xs = PHASE2 ? __fdiv_rn(__uint_as_float(__ldcg(p.rowmax + row)), 127.f) : __ldcg(p.xs + nth_bit(cu.mask, tok));
+          if (PHASE2 && __ldcg(p.rowmax + row) >= 0x7F800000u) xs = __uint_as_float(0x7FC00000u);
+          r0 = (size_t)cu.e * (PHASE2 ? p.d : p.w_stride) + col;
+          v *= xs * __ldg(static_cast<const float *>(PHASE2 ? p.s3 : p.s1) + r0);
+        }
+        if (pairs) {
+          float u = total(f + 8, tok);
+          if (FMT == I8) u *= xs * __ldg(static_cast<const float *>(p.s2) + r0);
+          v = silu_f(v) * u;
+        } else if (PART == R1) {
+          v = v < 0.f ? 0.f : v;            // a NaN stays one
+        }
+        if (PHASE2) {
+          p.y[(PART == S2 ? (size_t)p.T * p.k + tok : row) * p.d + col] = v;
+        } else {
+          const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+          uint16_t *h = PART == S1 ? p.hs + (size_t)tok * p.Fs + col : p.h + row * p.F + col;
+          *h = *reinterpret_cast<const uint16_t *>(&hi);
+          if (FMT != I8) {
+            const float rest = v - __bfloat162float(hi);
+            const __nv_bfloat16 lo = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
+            h[PART == S1 ? p.hs_lo : p.h_lo] = *reinterpret_cast<const uint16_t *>(&lo);
+          }
+          v = __bfloat162float(hi);
+        }
+      }
+      if (FMT == I8 && !PHASE2) {
+        // the row's largest |h|: over the task's columns (8 or 16 neighbouring lanes), then the grid
+        uint32_t m = __float_as_uint(v) & 0x7FFFFFFFu;
+        for (int o = 1; o < cols; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (f == 0 && tok < cu.rows) atomicMax(p.rowmax + row, m);
+      }
+    }
+    if (!more) break;
+    cu = nx;
+  }
+}
+
+// ---------------------------------------------------------------- router
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ double warp_max(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+// Warp arg-max of (v, i), ties to the lower index (i >= 0): three warp
+// reductions on the order-preserving 64-bit image of v.
+__device__ __forceinline__ void warp_argmax(double &v, int &i) {
+  const unsigned full = 0xffffffffu;
+  const unsigned long long u = (unsigned long long)__double_as_longlong(v + 0.0);   // -0 as +0
+  const unsigned long long key = (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+  const uint32_t hi = (uint32_t)(key >> 32), lo = (uint32_t)key;
+  const uint32_t mhi = __reduce_max_sync(full, hi);
+  const uint32_t mlo = __reduce_max_sync(full, hi == mhi ? lo : 0u);
+  i = (int)__reduce_min_sync(full, hi == mhi && lo == mlo ? (uint32_t)i : 0xFFFFFFFFu);
+  const unsigned long long mk = ((unsigned long long)mhi << 32) | mlo;
+  v = __longlong_as_double((long long)((mk >> 63) ? (mk & 0x7FFFFFFFFFFFFFFFull) : ~mk));
+}
+
+// Partial logits: unit (expert, slice of the hidden dimension) per warp.
+template <int TP>
+__device__ __forceinline__ void route_partials(const FewParams &p) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int units = p.E * p.ks;
+  // consecutive units go to different blocks
+  for (int u = blockIdx.x + gridDim.x * warp; u < units; u += gridDim.x * CW) {
+    const int e = u % p.E, sl = u / p.E;
+    const int k0 = sl * p.kslice, k1 = min(p.d, k0 + p.kslice);
+    double acc[TP];
+#pragma unroll
+    for (int t = 0; t < TP; ++t) acc[t] = 0.0;
+    const float *w = p.w_router + (size_t)e * p.d;
+#pragma unroll 2
+    for (int k = k0 + lane * 8; k < k1; k += 256) {
+      const float4 wa = __ldg(reinterpret_cast<const float4 *>(w + k));
+      const float4 wb = __ldg(reinterpret_cast<const float4 *>(w + k + 4));
+#pragma unroll
+      for (int t = 0; t < TP; ++t) {
+        if (t < p.T) {
+          const uint4 xv = __ldg(reinterpret_cast<const uint4 *>(p.x + (size_t)t * p.d + k));
+          float run = __uint_as_float(xv.x << 16) * wa.x;
+          run = fmaf(__uint_as_float(xv.x & 0xffff0000u), wa.y, run);
+          run = fmaf(__uint_as_float(xv.y << 16), wa.z, run);
+          run = fmaf(__uint_as_float(xv.y & 0xffff0000u), wa.w, run);
+          run = fmaf(__uint_as_float(xv.z << 16), wb.x, run);
+          run = fmaf(__uint_as_float(xv.z & 0xffff0000u), wb.y, run);
+          run = fmaf(__uint_as_float(xv.w << 16), wb.z, run);
+          run = fmaf(__uint_as_float(xv.w & 0xffff0000u), wb.w, run);
+          acc[t] += (double)run;
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < TP; ++t) {
+      if (t < p.T) {
+        const double s = warp_sum(acc[t]);
+        if (lane == 0) p.part[((size_t)sl * p.T + t) * p.E + e] = s;
+      }
+    }
+  }
+}
+
+constexpr int EPL = kMaxExperts / 32;
+
+// One token's choice: ids and weights to shared memory, probabilities added
+// to psum (expert lane + 32 j).
+__device__ __forceinline__ void choose(const FewParams &p, Shared *sh, int t, double (&psum)[EPL], double *wscr,
+                                       int lane) {
+  const int E = p.E;
+  double prob[EPL], score[EPL];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    const int e = lane + 32 * j;
+    prob[j] = 0.0;
+    score[j] = -INFINITY;
+    if (32 * j < E && e < E) {
+      double l = 0.0;
+      for (int s = 0; s < p.ks; ++s) l += __ldcg(p.part + ((size_t)s * p.T + t) * E + e);
+      prob[j] = l;
+    }
+  }
+  if (p.router == MOE_ROUTER_SOFTMAX_TOPK) {
+    double m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (lane + 32 * j < E) {
+        if (p.bias) prob[j] += (double)__ldg(p.bias + lane + 32 * j);
+        m = fmax(m, prob[j]);
+      }
+    m = warp_max(m);
+    double s = 0.0;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (lane + 32 * j < E) {
+        prob[j] = exp(prob[j] - m);
+        s += prob[j];
+      }
+    s = warp_sum(s);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (lane + 32 * j < E) {
+        prob[j] = prob[j] / s;
+        score[j] = prob[j];
+      }
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (lane + 32 * j < E) {
+        const int e = lane + 32 * j;
+        prob[j] = 1.0 / (1.0 + exp(-prob[j]));
+        score[j] = prob[j] + (p.bias ? (double)__ldg(p.bias + e) : 0.0);
+        wscr[e] = score[j];
+      }
+    __syncwarp();
+    // group score = sum of the two largest selection scores in the group
+    const int G = E / p.n_group;
+    double gs = -INFINITY;
+    if (lane < p.n_group) {
+      double b1 = -INFINITY, b2 = -INFINITY;
+      for (int q = 0; q < G; ++q) {
+        const double v = wscr[lane * G + q];
+        if (v > b1) { b2 = b1; b1 = v; } else if (v > b2) { b2 = v; }
+      }
+      gs = b1 + b2;
+    }
+    __syncwarp();
+    uint32_t keep = 0;
+    for (int r = 0; r < p.topk_group; ++r) {
+      const bool open = lane < p.n_group && !((keep >> lane) & 1u);
+      double v = open ? gs : -INFINITY;
+      int gi = open ? lane : 0x7fffffff;
+      warp_argmax(v, gi);
+      keep |= 1u << (gi & 31);
+    }
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (lane + 32 * j < E && !((keep >> ((lane + 32 * j) / G)) & 1u)) score[j] = -INFINITY;
+  }
+  // a token without a single number among its scores chooses nothing
+  bool number = false;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    psum[j] += prob[j];
+    number |= lane + 32 * j < E && prob[j] == prob[j];
+  }
+  const bool none = !__any_sync(0xffffffffu, number);
+
+  uint32_t taken = 0;
+  int my_e = -1;
+  double my_w = 0.0;
+  for (int r = 0; r < p.k; ++r) {
+    double bv = -INFINITY;
+    int bi = 0x7fffffff;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      const int e = lane + 32 * j;
+      if (e < E && !((taken >> j) & 1u) && (score[j] > bv || (score[j] == bv && e < bi))) {
+        bv = score[j];
+        bi = e;
+      }
+    }
+    warp_argmax(bv, bi);
+    double wv = 0.0;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (lane + 32 * j == bi && bi < E) {
+        wv = prob[j];
+        taken |= 1u << j;
+      }
+    wv = __shfl_sync(0xffffffffu, wv, bi & 31);
+    if (lane == r) { my_e = bi; my_w = wv; }
+  }
+  const double tot = warp_sum(lane < p.k ? my_w : 0.0);
+  double wout;
+  if (p.router == MOE_ROUTER_SOFTMAX_TOPK) wout = p.norm ? my_w / fmax(tot, 1e-12) : my_w;
+  else wout = (p.norm ? my_w / (tot + 1e-20) : my_w) * p.scaling;
+  if (lane < p.k) {
+    const bool bad = none || my_e < 0 || my_e >= E;
+    if (bad && blockIdx.x == 0) record_status(p.status, kDevBadExpertId);
+    sh->sel_id[t * p.k + lane] = bad ? -1 : my_e;
+    sh->sel_w[t * p.k + lane] = (float)wout;
+  }
+}
+
+// Choice for every token and the plan, the same in every block.
+__device__ __forceinline__ void make_plan(const FewParams &p, Shared *sh) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  double *scratch = reinterpret_cast<double *>(sh->red);
+  double psum[EPL];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) psum[j] = 0.0;
+  for (int e = tid; e < kMaxExperts; e += CT) sh->mask[e] = 0u;
+  for (int t = warp; t < p.T; t += CW) choose(p, sh, t, psum, scratch + warp * kMaxExperts, lane);
+  consumer_sync();
+  const int slots = p.T * p.k;
+  for (int i = tid; i < slots; i += CT)
+    if (sh->sel_id[i] >= 0) atomicOr(&sh->mask[sh->sel_id[i]], 1u << (i / p.k));
+  if (blockIdx.x == 0) {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) scratch[warp * kMaxExperts + lane + 32 * j] = psum[j];
+  }
+  consumer_sync();
+  if (blockIdx.x == 0)
+    for (int i = tid; i < slots; i += CT) {
+      p.ids[i] = sh->sel_id[i];
+      p.wts[i] = sh->sel_w[i];
+    }
+  int lost = 0;
+  for (int e = tid; e < p.E; e += CT) {
+    uint32_t m = sh->mask[e];
+    const int raw = __popc(m);
+    // in-order dropping: the first `cap` tokens stay
+    if (p.cap >= 0)
+      while (__popc(m) > p.cap) m &= ~(0x80000000u >> __clz(m));
+    sh->mask[e] = m;
+    lost += raw - __popc(m);
+    if (blockIdx.x == 0) {
+      double s = 0.0;
+      for (int w = 0; w < CW; ++w) s += scratch[w * kMaxExperts + e];
+      p.prob_sum[e] = (float)s;
+      p.raw_counts[e] = raw;
+      p.kept_counts[e] = __popc(m);
+    }
+  }
+  if (blockIdx.x == 0 && lost) atomicAdd(p.dropped, lost);
+  consumer_sync();
+  if (warp == 0) {
+    int n = 0, rows = 0;
+    for (int base = 0; base < p.E; base += 32) {
+      const int e = base + lane;
+      const int cnt = e < p.E ? __popc(sh->mask[e]) : 0;
+      const unsigned live = __ballot_sync(0xffffffffu, cnt > 0);
+      int pre = cnt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, pre, o);
+        if (lane >= o) pre += v;
+      }
+      if (cnt > 0) {
+        const int at = n + __popc(live & ((1u << lane) - 1u));
+        sh->act[at] = (int16_t)e;
+        sh->row0[at] = (int16_t)(rows + pre - cnt);
+      }
+      n += __popc(live);
+      rows += __shfl_sync(0xffffffffu, pre, 31);
+    }
+    if (lane == 0) {
+      sh->nact = n;
+      sh->row0[n] = (int16_t)rows;
+    }
+  }
+  consumer_sync();
+  if (tid == 0) mbar_arrive(&sh->plan);
+  // row of every slot (only the combine needs it)
+  for (int i = tid; i < slots; i += CT) {
+    const int e = sh->sel_id[i], t = i / p.k;
+    int row = -1;
+    if (e >= 0 && (sh->mask[e] >> t & 1u)) {
+      int lo = 0, hi = sh->nact;            // act is ascending
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sh->act[mid] <= e) lo = mid; else hi = mid;
+      }
+      row = sh->row0[lo] + __popc(sh->mask[e] & ((1u << t) - 1u));
+    }
+    sh->slot_row[i] = (int16_t)row;
+  }
+  consumer_sync();
+}
+
+// ---------------------------------------------------------------- 8-bit codes
+__device__ __forceinline__ uint32_t abs_max2(uint32_t w, uint32_t m) {
+  return max(m, max((w << 16) & 0x7FFF0000u, w & 0x7FFF0000u));
+}
+
+// Codes of 8 bf16 elements of a row with largest magnitude `top` (fp32 bits):
+// rne(127 x / a), see the row quantisation kernel for why this is exact.
+__device__ __forceinline__ uint2 codes8(uint4 v, uint32_t top) {
+  if (top == 0u || top >= 0x7F800000u) return make_uint2(0u, 0u);
+  float a = __uint_as_float(top);
+  const float pre = a < 0x1p-60f ? 0x1p64f : (a > 0x1p100f ? 0x1p-32f : 1.f);
+  a *= pre;
+  const float r = __frcp_rn(a);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    const float t = 127.f * (x * pre), p0 = t * r;
+    q[i] = __float_as_uint(__fmaf_rn(__fmaf_rn(-p0, a, t), r, p0) + 12582912.f);
+  }
+  uint2 o;
+  o.x = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+  o.y = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
+  return o;
+}
+
+// token rows: one block each, from the last block down (the router's units
+// start at the first)
+__device__ __forceinline__ void quantize_x(const FewParams &p, Shared *sh) {
+  uint32_t *scratch = &sh->red[0][0][0][0][0];
+  for (int t = (int)gridDim.x - 1 - (int)blockIdx.x; t < p.T; t += gridDim.x) {
+    const uint4 *row = reinterpret_cast<const uint4 *>(p.x + (size_t)t * p.d);
+    uint32_t m = 0;
+    for (int i = threadIdx.x; i < p.d / 8; i += CT) {
+      const uint4 v = __ldg(row + i);
+      m = abs_max2(v.x, abs_max2(v.y, abs_max2(v.z, abs_max2(v.w, m))));
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    consumer_sync();
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = m;
+    consumer_sync();
+    for (int w = 0; w < CW; ++w) m = max(m, scratch[w]);
+    for (int i = threadIdx.x; i < p.d / 8; i += CT)
+      reinterpret_cast<uint2 *>(p.xq + (size_t)t * p.d)[i] = codes8(__ldg(row + i), m);
+    if (threadIdx.x == 0)
+      p.xs[t] = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __fdiv_rn(__uint_as_float(m), 127.f);
+  }
+}
+
+// rows of h, all blocks together
+__device__ __forceinline__ void quantize_h(const FewParams &p, const Shared *sh) {
+  const int rows = sh->row0[sh->nact], nv = p.F / 8;
+  for (long long i = (long long)blockIdx.x * CT + threadIdx.x; i < (long long)rows * nv; i += (long long)gridDim.x * CT) {
+    const int r = (int)(i / nv);
+    reinterpret_cast<uint2 *>(p.hq)[i] =
+        codes8(__ldcg(reinterpret_cast<const uint4 *>(p.h) + i), __ldcg(p.rowmax + r));
+  }
+}
+
+// out[t] = sum_j w_j y[slot_row] in slot order (+ the shared expert's row), 4 columns per thread
+__device__ __forceinline__ void combine(const FewParams &p, const Shared *sh) {
+  const int nv = p.d / 4;
+  for (int i = blockIdx.x * CT + threadIdx.x; i < p.T * nv; i += gridDim.x * CT) {
+    const int t = i / nv, c = i - t * nv;
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < p.k; ++j) {
+      const int row = sh->slot_row[t * p.k + j];
+      if (row < 0) continue;
+      const float w = sh->sel_w[t * p.k + j];
+      const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.y + (size_t)row * p.d) + c);
+      a[0] = fmaf(w, v.x, a[0]);
+      a[1] = fmaf(w, v.y, a[1]);
+      a[2] = fmaf(w, v.z, a[2]);
+      a[3] = fmaf(w, v.w, a[3]);
+    }
+    if (p.Fs) {
+      const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.y + (size_t)(p.T * p.k + t) * p.d) + c);
+      a[0] += v.x;
+      a[1] += v.y;
+      a[2] += v.z;
+      a[3] += v.w;
+    }
+    *reinterpret_cast<uint2 *>(p.out + (size_t)t * p.d + 4 * c) = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+  }
+}
+
+template <int FMT, int TP>
+__global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__ FewParams p) {
+  constexpr int NB = TP > 8 ? 2 : 1;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  Ring r;
+  r.tiles = smem_raw;
+  r.sc = smem_raw + (size_t)p.stages * STAGE_BYTES;
+  r.sh = reinterpret_cast<Shared *>(r.sc + (size_t)p.sc_slots * p.sc_slot);
+  r.it = r.sc_it = 0;
+  r.ok = true;
+  Shared *sh = r.sh;
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&sh->full[s], 1);
+      mbar_init(&sh->empty[s], CW);
+    }
+    for (int s = 0; s < MAX_SC; ++s) {
+      mbar_init(&sh->sc_full[s], 1);
+      mbar_init(&sh->sc_empty[s], 1);
+    }
+    mbar_init(&sh->plan, 1);
+    sh->abort_flag = 0;
+    sh->nact = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  __syncthreads();
+  volatile int *abort_flag = &sh->abort_flag;
+
+  if (warp == CW) {
+    if (p.Fs) produce_part<BF16>(p, r, S1, 0);
+    if (r.ok)
+      r.ok = wait_bounded(&sh->plan, 0u, abort_flag, p.status, kDevTimeoutProducer, p.timeout_ns);
+    r.ok = __all_sync(0xffffffffu, r.ok);
+    const int nact = r.ok ? sh->nact : 0;
+    if (r.ok) produce_part<FMT>(p, r, R1, nact);
+    if (r.ok && p.Fs) produce_part<BF16>(p, r, S2, nact);
+    if (r.ok) produce_part<FMT>(p, r, R2, nact);
+    if ((threadIdx.x & 31) == 0 && !r.ok) {
+      // copies already issued land before the block goes away
+      const uint32_t first = r.it > (uint32_t)p.stages ? r.it - p.stages : 0u;
+      for (uint32_t i = first; i < r.it; ++i)
+        if (!wait_drain(&sh->full[i % p.stages], (i / p.stages) & 1u)) record_status(p.status, kDevTimeoutDrain);
+      if (FMT == Q4)
+        for (uint32_t i = r.sc_it > (uint32_t)p.sc_slots ? r.sc_it - p.sc_slots : 0u; i < r.sc_it; ++i)
+          if (!wait_drain(&sh->sc_full[i % p.sc_slots], (i / p.sc_slots) & 1u)) record_status(p.status, kDevTimeoutDrain);
+    }
+  } else {
+    uint32_t red_it = 0;
+    if (FMT == I8) {
+      quantize_x(p, sh);
+      if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < p.T * p.k; i += CT) p.rowmax[i] = 0u;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.dropped = 0;
+    route_partials<TP>(p);
+    grid_arrive(p.bar);
+    if (p.Fs) consume_part<BF16, S1, NB>(p, r, red_it);
+    grid_wait(p.bar, abort_flag, p);
+    make_plan(p, sh);
+    consume_part<FMT, R1, NB>(p, r, red_it);
+    grid_arrive(p.bar + 8);
+    grid_wait(p.bar + 8, abort_flag, p);
+    if (FMT == I8) {
+      quantize_h(p, sh);
+      grid_arrive(p.bar + 16);
+    }
+    if (p.Fs) consume_part<BF16, S2, NB>(p, r, red_it);
+    if (FMT == I8) grid_wait(p.bar + 16, abort_flag, p);
+    consume_part<FMT, R2, NB>(p, r, red_it);
+    grid_arrive(p.bar + 24);
+    grid_wait(p.bar + 24, abort_flag, p);
+    combine(p, sh);
+  }
+  __syncthreads();
+}
+
+template <int FMT, int TP>
+cudaError_t run(FewParams &p, cudaStream_t s) {
+  const size_t fixed = sizeof(Shared) + (size_t)p.sc_slots * p.sc_slot;
+  int stages = (int)((SMEM_LIMIT - fixed) / STAGE_BYTES);
+  p.stages = stages < MAX_STAGES ? stages : MAX_STAGES;
+  const size_t smem = fixed + (size_t)p.stages * STAGE_BYTES;
+  auto kern = few_kernel<FMT, TP>;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return err;
+  note_launch();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;      // the blocks wait for one another
+  attr[0].val.cooperative = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = sm_count();
+  cfg.blockDim = THREADS;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <int FMT>
+cudaError_t run_t(FewParams &p, cudaStream_t s) {
+  if (p.T <= 1) return run<FMT, 1>(p, s);
+  if (p.T <= 4) return run<FMT, 4>(p, s);
+  if (p.T <= 8) return run<FMT, 8>(p, s);
+  return run<FMT, 16>(p, s);
+}
+
+int route_slices(const moe_config &c) {
+  // a warp per (expert, slice) on all SMs, slices of at least 256 elements
+  const int want = (148 * CW) / c.num_experts;
+  const int most = (c.hidden + 255) / 256;
+  const int n = want < most ? want : most;
+  return n < 1 ? 1 : n;
+}
+
+struct FewLayout {
+  size_t part, xq, xs, h, h_lo, hs, hs_lo, rowmax, hq, y, total;
+};
+
+FewLayout few_layout(const moe_config &c) {
+  FewLayout L{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = off;
+    off = align_up(off + bytes, 256);
+    return here;
+  };
+  const size_t T = c.num_tokens, S = T * c.top_k, d = c.hidden, F = c.intermediate;
+  const size_t Fs = c.shared_intermediate > 0 ? c.shared_intermediate : 0;
+  const bool i8 = c.weight_dtype == MOE_I8_CHANNEL;
+  L.part = take(sizeof(double) * route_slices(c) * T * c.num_experts);
+  L.xq = take(i8 ? T * d : 0);
+  L.xs = take(i8 ? sizeof(float) * T : 0);
+  L.h = take(2 * S * F);
+  L.h_lo = take(i8 ? 0 : 2 * S * F);
+  L.hs = take(2 * T * Fs);
+  L.hs_lo = take(2 * T * Fs);
+  L.rowmax = take(i8 ? sizeof(unsigned) * S : 0);
+  L.hq = take(i8 ? S * F : 0);
+  L.y = take(sizeof(float) * (S + (Fs ? T : 0)) * d);
+  L.total = off;
+  return L;
+}
+
+int scale_slot(const moe_config &c) {
+  // 16 rows of K/64 scales and biases, 2 bytes each
+  const int K = c.hidden > c.intermediate ? c.hidden : c.intermediate;
+  return c.weight_dtype == MOE_Q4_AFFINE_G64 ? K / 64 * 2 * 2 * ROWS : 0;
+}
+
+int scale_slots(const moe_config &c) {
+  const int b = scale_slot(c);
+  const int n = b ? SC_BYTES / b : 0;
+  return b == 0 ? 0 : (n < 2 ? 2 : (n > MAX_SC ? MAX_SC : n));
+}
+
+}  // namespace
+
+bool few_supported(const moe_config &c) {
+  if (c.num_tokens > kFewTokens || c.act_dtype != MOE_BF16) return false;
+  // at least four stages beside the scales
+  return sizeof(Shared) + (size_t)scale_slots(c) * scale_slot(c) + 4 * (size_t)STAGE_BYTES <= (size_t)SMEM_LIMIT;
+}
+
+size_t few_bytes(const moe_config &c) { return few_supported(c) ? few_layout(c).total : 0; }
+
+cudaError_t launch_few(const FewArgs &a, cudaStream_t s) {
+  const moe_config &c = *a.cfg;
+  const FewLayout L = few_layout(c);
+  FewParams p{};
+  p.timeout_ns = wait_timeout_ns();
+  p.T = c.num_tokens;
+  p.d = c.hidden;
+  p.F = c.intermediate;
+  p.E = c.num_experts;
+  p.k = c.top_k;
+  p.Fs = c.shared_intermediate > 0 ? c.shared_intermediate : 0;
+  p.router = c.router;
+  p.norm = c.norm_topk_prob;
+  p.scaling = (double)c.routed_scaling;
+  p.n_group = c.n_group;
+  p.topk_group = c.topk_group;
+  p.cap = a.capacity < 0 || a.capacity > kFewTokens ? -1 : (int)a.capacity;
+  p.swiglu = c.act == MOE_ACT_SWIGLU;
+  p.x = static_cast<const uint16_t *>(a.x);
+  p.w_router = a.w_router;
+  p.bias = a.router_bias;
+  p.w1 = a.w1; p.w2 = a.w2; p.w3 = a.w3;
+  p.s1 = a.s1; p.s2 = a.s2; p.s3 = a.s3;
+  p.b1 = a.b1; p.b2 = a.b2; p.b3 = a.b3;
+  p.w_stride = a.w_stride;
+  p.sw1 = static_cast<const uint16_t *>(a.shared_w1);
+  p.sw2 = static_cast<const uint16_t *>(a.shared_w2);
+  p.sw3 = static_cast<const uint16_t *>(a.shared_w3);
+  p.out = static_cast<uint16_t *>(a.out);
+  p.ids = a.ids;
+  p.wts = a.wts;
+  p.raw_counts = a.raw_counts;
+  p.kept_counts = a.kept_counts;
+  p.dropped = a.dropped;
+  p.prob_sum = a.prob_sum;
+  p.status = a.status;
+  p.bar = reinterpret_cast<unsigned *>(a.status) + 16;
+  char *ws = static_cast<char *>(a.ws);
+  p.part = reinterpret_cast<double *>(ws + L.part);
+  p.ks = route_slices(c);
+  p.kslice = ((c.hidden + p.ks - 1) / p.ks + 7) / 8 * 8;
+  p.xq = reinterpret_cast<int8_t *>(ws + L.xq);
+  p.xs = reinterpret_cast<float *>(ws + L.xs);
+  p.h = reinterpret_cast<uint16_t *>(ws + L.h);
+  p.h_lo = (L.h_lo - L.h) / 2;
+  p.hs = reinterpret_cast<uint16_t *>(ws + L.hs);
+  p.hs_lo = (L.hs_lo - L.hs) / 2;
+  p.rowmax = reinterpret_cast<unsigned *>(ws + L.rowmax);
+  p.hq = reinterpret_cast<int8_t *>(ws + L.hq);
+  p.y = reinterpret_cast<float *>(ws + L.y);
+  p.sc_slot = scale_slot(c);
+  p.sc_slots = scale_slots(c);
+  switch (c.weight_dtype) {
+    case MOE_BF16: return run_t<BF16>(p, s);
+    case MOE_I8_CHANNEL: return run_t<I8>(p, s);
+    default: return run_t<Q4>(p, s);
+  }
+}
+
+}  // namespace moe

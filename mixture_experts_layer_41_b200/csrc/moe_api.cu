@@ -90,6 +90,37 @@ FfnArgs ffn_args(const moe_config &c, const WsLayout &L, void *ws) {
   return a;
 }
 
+// The expert weights as the kernels see them: with the fused gate/up layout
+// the up matrices are a second view into w1.
+void set_weights(const moe_config &c, const moe_weights *w, FfnArgs &a) {
+  a.w1 = w->w1;
+  a.w2 = w->w2;
+  a.w3 = w->w3;
+  a.s1 = w->scale1;
+  a.s2 = w->scale2;
+  a.s3 = w->scale3;
+  a.b1 = w->bias1;
+  a.b2 = w->bias2;
+  a.b3 = w->bias3;
+  a.w_stride = c.intermediate;
+  if (fused_gate_up(c)) {
+    // expert e's up rows follow its F gate rows: the up view starts F rows in
+    // and both views step 2F rows per expert
+    const size_t F = (size_t)c.intermediate, d = (size_t)c.hidden;
+    a.w_stride = 2 * c.intermediate;
+    if (c.weight_dtype == MOE_Q4_AFFINE_G64) {
+      a.w2 = static_cast<const char *>(w->w1) + F * (d / 2);
+      a.s2 = static_cast<const char *>(w->scale1) + F * (d / 64) * 2;
+      a.b2 = static_cast<const char *>(w->bias1) + F * (d / 64) * 2;
+    } else if (c.weight_dtype == MOE_I8_CHANNEL) {
+      a.w2 = static_cast<const char *>(w->w1) + F * d;
+      a.s2 = static_cast<const char *>(w->scale1) + F * sizeof(float);
+    } else {
+      a.w2 = static_cast<const char *>(w->w1) + F * d * (c.weight_dtype == MOE_F32 ? 4 : 2);
+    }
+  }
+}
+
 // The bf16 grouped GEMM runs on one SM per tile unless MOE_TC_PAIR=1 is set
 // in the environment, which selects the kernel on pairs of SMs (same
 // results bit for bit; measured slower on the dense workloads, so it is not
@@ -186,32 +217,7 @@ moe_status do_ffn(const moe_config &c, const void *x_perm, const int32_t *off, c
   a.x = x_perm;
   a.gather = gather;
   a.x_rows = c.num_tokens;
-  a.w1 = w->w1;
-  a.w2 = w->w2;
-  a.w3 = w->w3;
-  a.s1 = w->scale1;
-  a.s2 = w->scale2;
-  a.s3 = w->scale3;
-  a.b1 = w->bias1;
-  a.b2 = w->bias2;
-  a.b3 = w->bias3;
-  a.w_stride = c.intermediate;
-  if (fused_gate_up(c)) {
-    // expert e's up rows follow its F gate rows: the up view starts F rows in
-    // and both views step 2F rows per expert
-    const size_t F = (size_t)c.intermediate, d = (size_t)c.hidden;
-    a.w_stride = 2 * c.intermediate;
-    if (c.weight_dtype == MOE_Q4_AFFINE_G64) {
-      a.w2 = static_cast<const char *>(w->w1) + F * (d / 2);
-      a.s2 = static_cast<const char *>(w->scale1) + F * (d / 64) * 2;
-      a.b2 = static_cast<const char *>(w->bias1) + F * (d / 64) * 2;
-    } else if (c.weight_dtype == MOE_I8_CHANNEL) {
-      a.w2 = static_cast<const char *>(w->w1) + F * d;
-      a.s2 = static_cast<const char *>(w->scale1) + F * sizeof(float);
-    } else {
-      a.w2 = static_cast<const char *>(w->w1) + F * d * (c.weight_dtype == MOE_F32 ? 4 : 2);
-    }
-  }
+  set_weights(c, w, a);
   a.y = y;
   cudaError_t err = run_ffn(a, s);
   return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_grouped_ffn");
@@ -723,6 +729,58 @@ moe_status moe_forward(const moe_config *cfg, const void *x, const float *w_rout
   if ((st = check_ws(c, ws, ws_bytes)) != MOE_OK) return st;
   return forward_impl(c, x, w_router, router_bias, w, out, topk_ids, topk_w, stats, ws,
                       reinterpret_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_forward_few(const moe_config *cfg, const void *x, const float *w_router, const float *router_bias,
+                           const moe_weights *w, void *out, int32_t *topk_ids, float *topk_w, const moe_stats *stats,
+                           void *ws, size_t ws_bytes, moe_stream_t stream) {
+  set_error("%s%s", "");
+  moe_status st = moe_validate(cfg);
+  if (st != MOE_OK) return st;
+  const moe_config &c = *cfg;
+  if (!few_supported(c)) {
+    set_error("%s%s", c.act_dtype != MOE_BF16 ? "moe_forward_few needs bf16 activations"
+                      : c.num_tokens > kFewTokens ? "moe_forward_few takes at most MOE_FEW_TOKENS tokens"
+                                                  : "moe_forward_few: 4-bit rows too long for its scale buffers");
+    return MOE_ERR_UNSUPPORTED;
+  }
+  if (!aligned16(x) || !aligned16(w_router) || !aligned16_or_null(router_bias) || !aligned16(out) ||
+      !aligned16_or_null(topk_ids) || !aligned16_or_null(topk_w))
+    return MOE_ERR_INVALID_ARG;
+  if (stats && (!aligned16_or_null(stats->raw_counts) || !aligned16_or_null(stats->kept_counts) ||
+                !aligned16_or_null(stats->prob_sum) || !aligned16_or_null(stats->dropped)))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = check_weights(c, w)) != MOE_OK) return st;
+  if ((st = check_ws(c, ws, ws_bytes)) != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if ((st = clear_status(ws, s)) != MOE_OK) return st;
+  const WsLayout L = ws_layout(c);
+  FfnArgs v{};
+  set_weights(c, w, v);
+  FewArgs a{};
+  a.cfg = cfg;
+  a.capacity = capacity_of(c);
+  a.x = x;
+  a.w_router = w_router;
+  a.router_bias = router_bias;
+  a.w1 = v.w1; a.w2 = v.w2; a.w3 = v.w3;
+  a.s1 = v.s1; a.s2 = v.s2; a.s3 = v.s3;
+  a.b1 = v.b1; a.b2 = v.b2; a.b3 = v.b3;
+  a.w_stride = v.w_stride;
+  a.shared_w1 = w->shared1;
+  a.shared_w2 = w->shared2;
+  a.shared_w3 = w->shared3;
+  a.out = out;
+  a.ids = topk_ids ? topk_ids : ws_ptr<int32_t>(ws, L.topk_ids);
+  a.wts = topk_w ? topk_w : ws_ptr<float>(ws, L.topk_w);
+  a.raw_counts = stats && stats->raw_counts ? stats->raw_counts : ws_ptr<int32_t>(ws, L.raw_counts);
+  a.kept_counts = stats && stats->kept_counts ? stats->kept_counts : ws_ptr<int32_t>(ws, L.kept_counts);
+  a.prob_sum = stats && stats->prob_sum ? stats->prob_sum : ws_ptr<float>(ws, L.prob_sum);
+  a.dropped = stats && stats->dropped ? stats->dropped : ws_ptr<int32_t>(ws, L.dropped);
+  a.status = ws_ptr<int>(ws, L.status);
+  a.ws = ws_ptr<char>(ws, L.few);
+  cudaError_t err = launch_few(a, s);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_forward_few");
 }
 
 moe_status moe_forward_host(const moe_config *cfg, const void *x_host, const float *w_router,
