@@ -18,7 +18,7 @@
 //   combine   after a last grid barrier: out = sum_j w_j y_j (+ shared).
 //
 // A block is one producer warp and eight consumer warps.  The producer copies
-// rows, 1024 bytes of each of a task's 16 at a time, into a ring of stages
+// rows, up to 2048 bytes of each of a task's 16 at a time, into a ring of stages
 // (cp.async.bulk, one mbarrier per stage) and runs ahead of the consumers
 // across tasks, phases and grid barriers: the ring is full of the next
 // phase's weights when a barrier opens, and of the shared expert's while the
@@ -32,10 +32,12 @@
 // and at a row of weights per 23 bytes a clock it is idle most of the time.
 // The eight partial 16 x 8 results meet in shared memory.
 //
-// Precision: bf16 and 4-bit weights take h as the sum of two bf16 (16 bits),
-// 4-bit codes are multiplied as exact small integers and scaled per group of
-// 64 in fp32 (w = s q + b: s sum(q x) + b sum(x)), expert outputs stay fp32
-// until the combine: one rounding to bf16, at the end.  8-bit weights follow
+// Precision: bf16 weights take h as the sum of two bf16 (16 bits); with 4-bit
+// ones, whose products already keep the tensor pipe busy for most of the
+// time a group of codes takes to arrive, h is one bf16, as in the staged
+// layer.  4-bit codes are multiplied as exact small integers and scaled per
+// group of 64 in fp32 (w = s q + b: s sum(q x) + b sum(x)).  Expert outputs
+// stay fp32 until the combine.  8-bit weights follow
 // the 8-bit layer's definition (rows of x and of the bf16 h quantised).
 //
 // Results do not depend on timing: every sum has a fixed order, and the row
@@ -56,10 +58,9 @@ using namespace ptx;
 constexpr int CW = 8;                       // consumer warps
 constexpr int CT = 32 * CW;
 constexpr int THREADS = CT + 32;
-constexpr int CH = 1024;                    // bytes of a row per stage
+constexpr int MAX_CH = 2048;                // most bytes of a row per stage
 constexpr int ROWS = 16;                    // weight rows per task
-constexpr int STAGE_BYTES = ROWS * (CH + 64);
-constexpr int MAX_STAGES = 12;
+constexpr int MAX_STAGES = 24;
 constexpr int MAX_SC = 12;                  // 4-bit: tasks whose scales and biases are held at once
 constexpr int SC_BYTES = 40 * 1024;         // and the shared memory they may take (two tasks at least)
 constexpr int MAX_T = kFewTokens;
@@ -68,7 +69,8 @@ constexpr int SMEM_LIMIT = 227 * 1024;
 
 enum Fmt { BF16 = 0, I8 = 1, Q4 = 2 };
 
-__host__ __device__ constexpr int pitch_of(int fmt) { return CH + (fmt == Q4 ? 32 : 64); }
+// row pitch in a stage beyond its ch bytes (a multiple of 128)
+__host__ __device__ constexpr int pad_of(int fmt) { return fmt == Q4 ? 32 : 64; }
 
 struct FewParams {
   uint64_t timeout_ns;
@@ -103,7 +105,8 @@ struct FewParams {
   unsigned *rowmax;                         // 8-bit: [T*k] largest |h| of a row, as fp32 bits
   int8_t *hq;                               // 8-bit: [T*k][F]
   float *y;                                 // [T*k + T][d] expert outputs, then the shared expert's
-  int stages;
+  int ch;                                   // bytes of a row per stage, a multiple of 128
+  int stage_bytes, stages;
   int sc_slot, sc_slots;                    // 4-bit: bytes of one task's scales and biases, and how many are held
 };
 
@@ -244,9 +247,27 @@ struct Ring {
   Shared *sh;
   uint8_t *tiles;
   uint8_t *sc;                              // 4-bit: the slots of scales and biases
-  uint32_t it, sc_it;                       // stages / scale slots used so far
+  uint32_t st, ph;                          // next stage and the parity of its use
+  uint32_t sc_st, sc_ph;                    // likewise the next scale slot
+  uint32_t issued, sc_issued;               // producer: copies' stages and slots so far
   bool ok;
 };
+__device__ __forceinline__ void advance(uint32_t &st, uint32_t &ph, uint32_t n) {
+  if (++st == n) {
+    st = 0;
+    ph ^= 1u;
+  }
+}
+
+// The slow half of a barrier wait, out of line
+__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status, int code,
+                                       uint64_t limit_ns) {
+  return wait_bounded(bar, parity, abort_flag, status, code, limit_ns);
+}
+__device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, Shared *sh, const FewParams &p, int code) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return wait_slow(bar, parity, &sh->abort_flag, p.status, code, p.timeout_ns);
+}
 
 template <int FMT>
 __device__ __forceinline__ void produce_part(const FewParams &p, Ring &r, int part, int nact) {
@@ -262,48 +283,44 @@ __device__ __forceinline__ void produce_part(const FewParams &p, Ring &r, int pa
     const char *row = lane < 8 ? s.w0 + (size_t)lane * rb : s.w1 + (size_t)(lane - 8) * rb;
     if (FMT == Q4) {
       // scales and biases of the task's two blocks of 8 rows, each contiguous
-      const int slot = r.sc_it % p.sc_slots;
       int good = 1;
       if (lane == 0)
-        good = wait_bounded(&r.sh->sc_empty[slot], ((r.sc_it / p.sc_slots) & 1u) ^ 1u, abort_flag, p.status,
-                            kDevTimeoutProducer, p.timeout_ns) &&
-               !*abort_flag;
+        good = wait_on(&r.sh->sc_empty[r.sc_st], r.sc_ph ^ 1u, r.sh, p, kDevTimeoutProducer) && !*abort_flag;
       if (!__shfl_sync(0xffffffffu, good, 0)) {
         r.ok = false;
         break;
       }
       const int blk = K / 64 * 2 * 8;       // bytes: a multiple of 16
-      if (lane == 0) mbar_expect_tx(&r.sh->sc_full[slot], 4 * blk);
+      if (lane == 0) mbar_expect_tx(&r.sh->sc_full[r.sc_st], 4 * blk);
       __syncwarp();
       if (lane < 4) {
         const char *base = static_cast<const char *>(
             part == R2 ? (lane & 1 ? p.b3 : p.s3)
                        : (lane < 2 ? (lane & 1 ? p.b1 : p.s1) : (lane & 1 ? p.b2 : p.s2)));
         const size_t row_i = lane < 2 ? s.r0 : s.r1;
-        bulk_load(smem_u32(r.sc + (size_t)slot * p.sc_slot + lane * blk), base + row_i * (size_t)(K / 64 * 2), blk,
-                  smem_u32(&r.sh->sc_full[slot]));
+        bulk_load(smem_u32(r.sc + (size_t)r.sc_st * p.sc_slot + lane * blk), base + row_i * (size_t)(K / 64 * 2), blk,
+                  smem_u32(&r.sh->sc_full[r.sc_st]));
       }
-      ++r.sc_it;
+      ++r.sc_issued;
+      advance(r.sc_st, r.sc_ph, p.sc_slots);
     }
-    for (int off = 0; off < rb; off += CH, ++r.it) {
-      const int st = r.it % p.stages;
+    const uint32_t dst_row = smem_u32(r.tiles) + lane * (p.ch + pad_of(FMT));
+    for (int off = 0; off < rb; off += p.ch) {
       int good = 1;
-      if (lane == 0)
+      if (lane == 0) {
         // a consumer that gave up releases stages it did not wait for, having
         // raised the flag first: nothing may be copied into them
-        good = wait_bounded(&r.sh->empty[st], ((r.it / p.stages) & 1u) ^ 1u, abort_flag, p.status, kDevTimeoutProducer,
-                            p.timeout_ns) &&
-               !*abort_flag;
+        good = wait_on(&r.sh->empty[r.st], r.ph ^ 1u, r.sh, p, kDevTimeoutProducer) && !*abort_flag;
+        if (good) mbar_expect_tx(&r.sh->full[r.st], min(p.ch, rb - off) * (s.n0 + s.n1));
+      }
       if (!__shfl_sync(0xffffffffu, good, 0)) {
         r.ok = false;
         break;
       }
-      const uint32_t bytes = min(CH, rb - off);
-      if (lane == 0) mbar_expect_tx(&r.sh->full[st], bytes * (s.n0 + s.n1));
-      __syncwarp();
       if (mine)
-        bulk_load(smem_u32(r.tiles + (size_t)st * STAGE_BYTES + lane * pitch_of(FMT)), row + off, bytes,
-                  smem_u32(&r.sh->full[st]));
+        bulk_load(dst_row + r.st * p.stage_bytes, row + off, min(p.ch, rb - off), smem_u32(&r.sh->full[r.st]));
+      ++r.issued;
+      advance(r.st, r.ph, p.stages);
     }
   }
 }
@@ -325,15 +342,9 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
       : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t bf2_sub(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-// nibbles i and i + 4 of a code word as an exact bf16 pair
+// nibbles i and i + 4 of a code word as the exact bf16 pair (128 + q_i, 128 + q_{i+4})
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) {
-  const uint32_t magic = 0x43004300u;       // bf16 128.0 in both halves
-  return bf2_sub(((w >> (4 * i)) & 0x000F000Fu) | magic, magic);
+  return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
 }
 __device__ __forceinline__ uint4 lds128(const uint8_t *p) { return *reinterpret_cast<const uint4 *>(p); }
 
@@ -345,106 +356,107 @@ struct BSeg {
   uint4 v[FMT == Q4 ? 4 : 1][LO ? 2 : 1];
 };
 
-constexpr int SEGS = CH / 64 / CW;          // segments per warp and stage
+constexpr int SEGS = MAX_CH / 64 / CW;      // segments per warp and stage
 
-// Where a task's B operand comes from, per lane: token row g (and g + 8)
-template <int NB>
-struct BSrc {
-  const char *row[NB];                      // null: no such token
-};
+// bytes of the token row per byte of the weight row
+template <int FMT>
+__host__ __device__ constexpr int ratio_of() {
+  return FMT == Q4 ? 4 : 1;
+}
 
-// wo: byte of the weight row at which this warp's segment starts
-template <int FMT, bool LO>
-__device__ __forceinline__ void load_b(BSeg<FMT, LO> &bv, const char *row, size_t lo_bytes, int wo, int rb, int c) {
-  // bytes of the token row per byte of the weight row
-  constexpr int R = FMT == Q4 ? 4 : 1;
+// row: this lane's place in the segment's stretch of the token row (its first
+// byte plus lane_off); left: bytes of the weight row from the segment on.
+// CHECK: the segment may reach past the row's end.
+template <int FMT, bool LO, bool CHECK>
+__device__ __forceinline__ void load_b(BSeg<FMT, LO> &bv, const char *row, size_t lo_bytes, int left, int c) {
 #pragma unroll
   for (int q = 0; q < (FMT == Q4 ? 4 : 1); ++q) {
     // 4-bit: group q / 2 of the segment, elements 16 c + 8 (q % 2) ..
-    const int at = wo + (FMT == Q4 ? (q >> 1) * 32 + c * 8 + (q & 1) * 4 : c * 16);
-    const bool ok = row != nullptr && at < rb;
-    const char *a = row + (size_t)at * R;
+    constexpr int R = ratio_of<FMT>();
+    const int at = FMT == Q4 ? (q >> 1) * 32 + (q & 1) * 4 : 0;
+    const bool ok = !CHECK || at + c * (FMT == Q4 ? 8 : 16) < left;
 #pragma unroll
     for (int l = 0; l < (LO ? 2 : 1); ++l)
-      bv.v[q][l] = ok ? __ldcg(reinterpret_cast<const uint4 *>(a + (l ? lo_bytes : 0))) : make_uint4(0u, 0u, 0u, 0u);
+      bv.v[q][l] = ok ? __ldcg(reinterpret_cast<const uint4 *>(row + at * R + (l ? lo_bytes : 0)))
+                      : make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
+// Two accumulators per block of tokens, so that consecutive products do not
+// wait for one another
 template <int FMT, int NB>
 struct Acc {
-  float f[NB][4];
+  float f[NB][2][4];
 };
 template <int NB>
 struct Acc<I8, NB> {
-  int f[NB][4];
+  int f[NB][2][4];
 };
 
-// One 64-byte segment of the 16 rows (seg: its first byte in the stage, left:
-// valid bytes of the stage) times the tokens.  The first NBP blocks of eight
-// tokens have their operand in registers; a further one (4-bit weights, whose
-// operand is four times as long, and only for an expert that more than eight
-// tokens chose) fetches it here.
-template <int FMT, bool LO, int NB, int NBP>
-__device__ __forceinline__ void consume(Acc<FMT, NB> &acc, const BSeg<FMT, LO> (&bv)[NBP], const BSrc<NB> &src,
-                                        size_t lo_bytes, const uint8_t *tile, int seg, int left, int off, int rb, int rows,
-                                        int g, int c, const uint8_t *sc, int groups) {
-  constexpr int P = pitch_of(FMT);
+// One 64-byte segment of the 16 rows times the tokens.  lo_row / hi_row: this
+// lane's place in rows g and g + 8 (4-bit: without the lane's 8 c); left:
+// bytes of the rows from the segment on.  sc: 4-bit, the group's scales of
+// row g.  The first NBP blocks of eight tokens have their operand in
+// registers; a further one (4-bit weights, whose operand is four times as
+// long, and only for an expert that more than eight tokens chose) fetches it
+// here from `far`.
+template <int FMT, bool LO, int NB, int NBP, bool CHECK>
+__device__ __forceinline__ void consume(Acc<FMT, NB> &acc, const BSeg<FMT, LO> (&bv)[NBP], const char *far, int left,
+                                        const uint8_t *lo_row, const uint8_t *hi_row, bool second, int c,
+                                        const uint16_t *sc, int groups) {
   if constexpr (FMT != Q4) {
-    uint4 lo = lds128(tile + g * P + seg + c * 16), hi = lds128(tile + (g + 8) * P + seg + c * 16);
-    if (seg + c * 16 >= left) lo = hi = make_uint4(0u, 0u, 0u, 0u);
+    uint4 lo = lds128(lo_row), hi = lds128(hi_row);
+    if (CHECK && c * 16 >= left) lo = hi = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-      if (n > 0 && rows <= 8) break;
+      if (n > 0 && !second) break;
 #pragma unroll
       for (int l = 0; l < (LO ? 2 : 1); ++l) {
         const uint4 b = bv[n].v[0][l];
         if constexpr (FMT == BF16) {
-          mma_bf16(acc.f[n], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
-          mma_bf16(acc.f[n], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+          mma_bf16(acc.f[n][0], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+          mma_bf16(acc.f[n][1], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
         } else {
-          mma_s8(acc.f[n], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
-          mma_s8(acc.f[n], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+          mma_s8(acc.f[n][0], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+          mma_s8(acc.f[n][1], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
         }
       }
     }
   } else {
-    const uint16_t *t = reinterpret_cast<const uint16_t *>(sc);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const int go = seg + q * 32;
-      if (go >= left) break;
-      const uint2 lo = *reinterpret_cast<const uint2 *>(tile + g * P + go + c * 8);
-      const uint2 hi = *reinterpret_cast<const uint2 *>(tile + (g + 8) * P + go + c * 8);
-      // scale and bias of rows g and g + 8 for this group
-      const int gi = (off + go) / 32;
-      const float s_lo = bf16_to_f32(t[g * groups + gi]), b_lo = bf16_to_f32(t[(8 + g) * groups + gi]);
-      const float s_hi = bf16_to_f32(t[(16 + g) * groups + gi]), b_hi = bf16_to_f32(t[(24 + g) * groups + gi]);
+      if (CHECK && q * 32 >= left) break;
+      const uint2 lo = *reinterpret_cast<const uint2 *>(lo_row + q * 32);
+      const uint2 hi = *reinterpret_cast<const uint2 *>(hi_row + q * 32);
+      // scale and bias of rows g and g + 8 for this group.  The codes enter as
+      // 128 + q (an exact bf16 by its bits), so the bias takes 128 s off again
+      const float s_lo = bf16_to_f32(sc[q]), s_hi = bf16_to_f32(sc[16 * groups + q]);
+      const float b_lo = fmaf(-128.f, s_lo, bf16_to_f32(sc[8 * groups + q]));
+      const float b_hi = fmaf(-128.f, s_hi, bf16_to_f32(sc[24 * groups + q]));
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        if (n > 0 && rows <= 8) break;
+        if (n > 0 && !second) break;
         BSeg<FMT, LO> own;
-        if (n >= NBP) load_b<FMT, LO>(own, src.row[n], lo_bytes, off + seg, rb, c);
+        if (n >= NBP) load_b<FMT, LO, CHECK>(own, far, 0, left, c);
         float dq[4] = {0.f, 0.f, 0.f, 0.f}, dx[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const uint32_t wl = u ? lo.y : lo.x, wh = u ? hi.y : hi.x;
           constexpr uint32_t one = 0x3F803F80u;
-#pragma unroll
-          for (int l = 0; l < (LO ? 2 : 1); ++l) {
-            // elements (i, i + 4) of the token's 8, in the order of the nibble pairs
-            const uint4 b = n < NBP ? bv[n < NBP ? n : 0].v[2 * q + u][l] : own.v[2 * q + u][l];
-            const uint32_t p0 = __byte_perm(b.x, b.z, 0x5410), p1 = __byte_perm(b.x, b.z, 0x7632);
-            const uint32_t p2 = __byte_perm(b.y, b.w, 0x5410), p3 = __byte_perm(b.y, b.w, 0x7632);
-            mma_bf16(dq, code_pair(wl, 0), code_pair(wh, 0), code_pair(wl, 1), code_pair(wh, 1), p0, p1);
-            mma_bf16(dq, code_pair(wl, 2), code_pair(wh, 2), code_pair(wl, 3), code_pair(wh, 3), p2, p3);
-            mma_bf16(dx, one, one, one, one, p0, p1);
-            mma_bf16(dx, one, one, one, one, p2, p3);
-          }
+          // elements (i, i + 4) of the token's 8, in the order of the nibble pairs
+          const uint4 b = n < NBP ? bv[n < NBP ? n : 0].v[2 * q + u][0] : own.v[2 * q + u][0];
+          const uint32_t p0 = __byte_perm(b.x, b.z, 0x5410), p1 = __byte_perm(b.x, b.z, 0x7632);
+          const uint32_t p2 = __byte_perm(b.y, b.w, 0x5410), p3 = __byte_perm(b.y, b.w, 0x7632);
+          mma_bf16(dq, code_pair(wl, 0), code_pair(wh, 0), code_pair(wl, 1), code_pair(wh, 1), p0, p1);
+          mma_bf16(dx, one, one, one, one, p0, p1);
+          mma_bf16(dq, code_pair(wl, 2), code_pair(wh, 2), code_pair(wl, 3), code_pair(wh, 3), p2, p3);
+          mma_bf16(dx, one, one, one, one, p2, p3);
         }
-        acc.f[n][0] = fmaf(s_lo, dq[0], fmaf(b_lo, dx[0], acc.f[n][0]));
-        acc.f[n][1] = fmaf(s_lo, dq[1], fmaf(b_lo, dx[1], acc.f[n][1]));
-        acc.f[n][2] = fmaf(s_hi, dq[2], fmaf(b_hi, dx[2], acc.f[n][2]));
-        acc.f[n][3] = fmaf(s_hi, dq[3], fmaf(b_hi, dx[3], acc.f[n][3]));
+        float(&a)[4] = acc.f[n][q];
+        a[0] = fmaf(s_lo, dq[0], fmaf(b_lo, dx[0], a[0]));
+        a[1] = fmaf(s_lo, dq[1], fmaf(b_lo, dx[1], a[1]));
+        a[2] = fmaf(s_hi, dq[2], fmaf(b_hi, dx[2], a[2]));
+        a[3] = fmaf(s_hi, dq[3], fmaf(b_hi, dx[3], a[3]));
       }
     }
   }
@@ -480,113 +492,134 @@ __device__ __forceinline__ void place(const FewParams &p, const Shared *sh, cons
   }
 }
 
-template <int FMT, int PART, int NB>
-__device__ __forceinline__ BSrc<NB> b_src(const FewParams &p, const Cursor &cu, int g) {
-  BSrc<NB> s;
-#pragma unroll
-  for (int n = 0; n < NB; ++n) {
-    const int r = g + 8 * n;
-    s.row[n] = nullptr;
-    if (r < cu.rows) {
-      if (PART == S1 || PART == R1) {
-        const int t = PART == S1 ? r : nth_bit(cu.mask, r);
-        s.row[n] = FMT == I8 ? reinterpret_cast<const char *>(p.xq + (size_t)t * p.d)
-                             : reinterpret_cast<const char *>(p.x + (size_t)t * p.d);
-      } else if (PART == S2) {
-        s.row[n] = reinterpret_cast<const char *>(p.hs + (size_t)r * p.Fs);
-      } else {
-        s.row[n] = FMT == I8 ? reinterpret_cast<const char *>(p.hq + (size_t)(cu.row0 + r) * p.F)
-                             : reinterpret_cast<const char *>(p.h + (size_t)(cu.row0 + r) * p.F);
-      }
-    }
+// Row r of a task's token operand.  A row past the task's last repeats the
+// last: each token is a column of its own, and those columns are not stored.
+template <int FMT, int PART>
+__device__ __forceinline__ const char *b_row(const FewParams &p, const Cursor &cu, int r) {
+  r = min(r, cu.rows - 1);
+  if (PART == S1 || PART == R1) {
+    const int t = PART == S1 ? r : nth_bit(cu.mask, r);
+    return FMT == I8 ? reinterpret_cast<const char *>(p.xq + (size_t)t * p.d)
+                     : reinterpret_cast<const char *>(p.x + (size_t)t * p.d);
   }
-  return s;
+  if (PART == S2) return reinterpret_cast<const char *>(p.hs + (size_t)r * p.Fs);
+  return FMT == I8 ? reinterpret_cast<const char *>(p.hq + (size_t)(cu.row0 + r) * p.F)
+                   : reinterpret_cast<const char *>(p.h + (size_t)(cu.row0 + r) * p.F);
 }
 
-// The block's tasks of one part.  ITEMS: FMT of the weights read.
+// The block's tasks of one part.
 template <int FMT, int PART, int NB>
 __device__ __forceinline__ void consume_part(const FewParams &p, Ring &r, uint32_t &red_it) {
   Shared *sh = r.sh;
   constexpr bool PHASE2 = PART == S2 || PART == R2;
-  constexpr bool LO = PHASE2 && FMT != I8;
+  constexpr bool LO = PHASE2 && FMT == BF16;
+  constexpr int NBP = FMT == Q4 ? 1 : NB;   // blocks of eight tokens whose operand is fetched ahead
+  constexpr int R = ratio_of<FMT>();
   const Dims dm = part_dims(p, PART, sh->nact);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int K = !PHASE2 ? p.d : (PART == S2 ? p.Fs : p.F);
   const int rb = row_bytes<FMT>(K);
+  const int groups = K / 64;
   const size_t lo_bytes = 2 * (PART == S2 ? p.hs_lo : p.h_lo);
-  volatile int *abort_flag = &sh->abort_flag;
+  const int ch = p.ch;
+  const int w0 = warp * 64;                 // this warp's first segment of a stage
+  constexpr int STEP = CW * 64;             // and the distance to its next
+  const int lane_b = (w0 + c * (FMT == Q4 ? 8 : 16)) * R;
+  const uint32_t row_lo = g * (ch + pad_of(FMT)) + w0 + c * (FMT == Q4 ? 8 : 16);
+  const uint32_t row_hi = row_lo + 8 * (ch + pad_of(FMT));
   if (dm.first >= dm.count) return;
 
-  constexpr int NBP = FMT == Q4 ? 1 : NB;
-  const int groups = K / 64;
   Cursor cu;
   cu.task = dm.first;
   place<PART>(p, sh, dm, cu);
-  BSrc<NB> bs = b_src<FMT, PART, NB>(p, cu, g);
+  const char *bp[NB];                       // the stage's stretch of the token rows, at this lane
   BSeg<FMT, LO> bv[SEGS][NBP];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) bp[n] = b_row<FMT, PART>(p, cu, g + 8 * n) + lane_b;
 #pragma unroll
   for (int s = 0; s < SEGS; ++s)
 #pragma unroll
-    for (int n = 0; n < NBP; ++n) load_b<FMT, LO>(bv[s][n], bs.row[n], lo_bytes, (warp + CW * s) * 64, rb, c);
+    for (int n = 0; n < NBP; ++n)
+      load_b<FMT, LO, true>(bv[s][n], bp[n] + s * STEP * R, lo_bytes, min(ch, rb) - w0 - s * STEP, c);
 
   for (;;) {
     Acc<FMT, NB> acc;
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc.f[n][j] = 0;
+      for (int j = 0; j < 4; ++j) acc.f[n][0][j] = acc.f[n][1][j] = 0;
     Cursor nx = cu;
     nx.task += gridDim.x;
     const bool more = nx.task < dm.count;
-    const uint8_t *sc = nullptr;
+    const bool second = cu.rows > 8;
+    const uint16_t *sc = nullptr;
     if (FMT == Q4) {
-      const int slot = r.sc_it % p.sc_slots;
-      wait_bounded(&sh->sc_full[slot], (r.sc_it / p.sc_slots) & 1u, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns);
-      sc = r.sc + (size_t)slot * p.sc_slot;
+      wait_on(&sh->sc_full[r.sc_st], r.sc_ph, sh, p, kDevTimeoutEpilogue);
+      sc = reinterpret_cast<const uint16_t *>(r.sc + (size_t)r.sc_st * p.sc_slot) + g * groups + w0 / 32;
     }
-    for (int off = 0; off < rb; off += CH, ++r.it) {
+    for (int off = 0; off < rb; off += ch) {
       // where the next stage's token operand comes from: its loads take the
       // registers of each segment as soon as that has been used
-      const bool last = off + CH >= rb;
-      BSrc<NB> bn = bs;
-      if (last && more) {
-        place<PART>(p, sh, dm, nx);
-        bn = b_src<FMT, PART, NB>(p, nx, g);
+      const bool last = off + ch >= rb;
+      const char *bn[NB];
+      int next_left;                        // bytes of the weight rows in the next stage, none: 0
+      if (!last) {
+        next_left = min(ch, rb - off - ch);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) bn[n] = bp[n] + ch * R;
+      } else {
+        next_left = more ? min(ch, rb) : 0;
+        if (more) place<PART>(p, sh, dm, nx);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) bn[n] = more ? b_row<FMT, PART>(p, nx, g + 8 * n) + lane_b : bp[n];
       }
-      const int next_off = last ? 0 : off + CH;
-      const int st = r.it % p.stages;
-      const uint8_t *tile = r.tiles + (size_t)st * STAGE_BYTES;
-      const int left = min(CH, rb - off);
-      wait_bounded(&sh->full[st], (r.it / p.stages) & 1u, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns);
+      const uint8_t *tile = r.tiles + (size_t)r.st * p.stage_bytes;
+      const int left = min(ch, rb - off);
+      wait_on(&sh->full[r.st], r.ph, sh, p, kDevTimeoutEpilogue);
       __syncwarp();
+      if (left == MAX_CH && next_left == MAX_CH) {
 #pragma unroll
-      for (int s = 0; s < SEGS; ++s) {
-        const int seg = (warp + CW * s) * 64;
-        if (seg < left)
-          consume<FMT, LO, NB, NBP>(acc, bv[s], bs, lo_bytes, tile, seg, left, off, rb, cu.rows, g, c, sc, groups);
-        if (!last || more) {
+        for (int s = 0; s < SEGS; ++s) {
+          consume<FMT, LO, NB, NBP, false>(acc, bv[s], bp[NB - 1] + s * STEP * R, 64, tile + row_lo + s * STEP,
+                                           tile + row_hi + s * STEP, second, c, sc + (off + s * STEP) / 32, groups);
 #pragma unroll
-          for (int n = 0; n < NBP; ++n) load_b<FMT, LO>(bv[s][n], bn.row[n], lo_bytes, next_off + seg, rb, c);
+          for (int n = 0; n < NBP; ++n) load_b<FMT, LO, false>(bv[s][n], bn[n] + s * STEP * R, lo_bytes, 64, c);
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < SEGS; ++s) {
+          const int at = w0 + s * STEP;
+          if (at < left)
+            consume<FMT, LO, NB, NBP, true>(acc, bv[s], bp[NB - 1] + s * STEP * R, left - at, tile + row_lo + s * STEP,
+                                            tile + row_hi + s * STEP, second, c, sc + (off + s * STEP) / 32, groups);
+#pragma unroll
+          for (int n = 0; n < NBP; ++n) load_b<FMT, LO, true>(bv[s][n], bn[n] + s * STEP * R, lo_bytes, next_left - at, c);
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->empty[st]);
-      if (last) bs = bn;
+      if (lane == 0) mbar_arrive(&sh->empty[r.st]);
+      advance(r.st, r.ph, p.stages);
+#pragma unroll
+      for (int n = 0; n < NB; ++n) bp[n] = bn[n];
     }
     // the eight warps' partial results meet; two buffers in turn, so one
     // barrier per task keeps writers and readers apart
     uint32_t(*red)[2][32][4] = sh->red[red_it & 1u];
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
-      *reinterpret_cast<uint4 *>(red[warp][n][lane]) =
-          FMT == I8 ? make_uint4((uint32_t)acc.f[n][0], (uint32_t)acc.f[n][1], (uint32_t)acc.f[n][2],
-                                 (uint32_t)acc.f[n][3])
-                    : make_uint4(__float_as_uint((float)acc.f[n][0]), __float_as_uint((float)acc.f[n][1]),
-                                 __float_as_uint((float)acc.f[n][2]), __float_as_uint((float)acc.f[n][3]));
+    for (int n = 0; n < NB; ++n) {
+      uint32_t v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const auto sum = acc.f[n][0][j] + acc.f[n][1][j];
+        if constexpr (FMT == I8) v[j] = (uint32_t)sum;
+        else v[j] = __float_as_uint(sum);
+      }
+      *reinterpret_cast<uint4 *>(red[warp][n][lane]) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
     consumer_sync();
     if (FMT == Q4) {
-      if (threadIdx.x == 0) mbar_arrive(&sh->sc_empty[r.sc_it % p.sc_slots]);
-      ++r.sc_it;
+      if (threadIdx.x == 0) mbar_arrive(&sh->sc_empty[r.sc_st]);
+      advance(r.sc_st, r.sc_ph, p.sc_slots);
     }
     ++red_it;
     // value (row, token) of the task: accumulator j of lane 4 (row % 8) + (token % 8) / 2
@@ -635,7 +668,7 @@ __device__ __forceinline__ void consume_part(const FewParams &p, Ring &r, uint32
           const __nv_bfloat16 hi = __float2bfloat16_rn(v);
           uint16_t *h = PART == S1 ? p.hs + (size_t)tok * p.Fs + col : p.h + row * p.F + col;
           *h = *reinterpret_cast<const uint16_t *>(&hi);
-          if (FMT != I8) {
+          if (FMT == BF16) {
             const float rest = v - __bfloat162float(hi);
             const __nv_bfloat16 lo = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
             h[PART == S1 ? p.hs_lo : p.h_lo] = *reinterpret_cast<const uint16_t *>(&lo);
@@ -1024,9 +1057,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Ring r;
   r.tiles = smem_raw;
-  r.sc = smem_raw + (size_t)p.stages * STAGE_BYTES;
+  r.sc = smem_raw + (size_t)p.stages * p.stage_bytes;
   r.sh = reinterpret_cast<Shared *>(r.sc + (size_t)p.sc_slots * p.sc_slot);
-  r.it = r.sc_it = 0;
+  r.st = r.ph = r.sc_st = r.sc_ph = r.issued = r.sc_issued = 0;
   r.ok = true;
   Shared *sh = r.sh;
   const int warp = threadIdx.x >> 5;
@@ -1059,12 +1092,11 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     if (r.ok) produce_part<FMT>(p, r, R2, nact);
     if ((threadIdx.x & 31) == 0 && !r.ok) {
       // copies already issued land before the block goes away
-      const uint32_t first = r.it > (uint32_t)p.stages ? r.it - p.stages : 0u;
-      for (uint32_t i = first; i < r.it; ++i)
-        if (!wait_drain(&sh->full[i % p.stages], (i / p.stages) & 1u)) record_status(p.status, kDevTimeoutDrain);
-      if (FMT == Q4)
-        for (uint32_t i = r.sc_it > (uint32_t)p.sc_slots ? r.sc_it - p.sc_slots : 0u; i < r.sc_it; ++i)
-          if (!wait_drain(&sh->sc_full[i % p.sc_slots], (i / p.sc_slots) & 1u)) record_status(p.status, kDevTimeoutDrain);
+      const uint32_t n = p.stages, m = p.sc_slots;
+      for (uint32_t i = r.issued > n ? r.issued - n : 0u; i < r.issued; ++i)
+        if (!wait_drain(&sh->full[i % n], (i / n) & 1u)) record_status(p.status, kDevTimeoutDrain);
+      for (uint32_t i = r.sc_issued > m ? r.sc_issued - m : 0u; i < r.sc_issued; ++i)
+        if (!wait_drain(&sh->sc_full[i % m], (i / m) & 1u)) record_status(p.status, kDevTimeoutDrain);
     }
   } else {
     uint32_t red_it = 0;
@@ -1099,9 +1131,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
 template <int FMT, int TP>
 cudaError_t run(FewParams &p, cudaStream_t s) {
   const size_t fixed = sizeof(Shared) + (size_t)p.sc_slots * p.sc_slot;
-  int stages = (int)((SMEM_LIMIT - fixed) / STAGE_BYTES);
+  int stages = (int)((SMEM_LIMIT - fixed) / p.stage_bytes);
   p.stages = stages < MAX_STAGES ? stages : MAX_STAGES;
-  const size_t smem = fixed + (size_t)p.stages * STAGE_BYTES;
+  const size_t smem = fixed + (size_t)p.stages * p.stage_bytes;
   auto kern = few_kernel<FMT, TP>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
@@ -1164,6 +1196,19 @@ FewLayout few_layout(const moe_config &c) {
   return L;
 }
 
+// bytes of a row per stage: the longest row if that is short, so that short
+// rows get more stages
+int stage_ch(const moe_config &c) {
+  const long long K = c.hidden > c.intermediate ? c.hidden : c.intermediate;
+  long long b = c.weight_dtype == MOE_BF16 ? 2 * K : (c.weight_dtype == MOE_I8_CHANNEL ? K : K / 2);
+  if (c.shared_intermediate > 0) {
+    const long long s = 2LL * (c.hidden > c.shared_intermediate ? c.hidden : c.shared_intermediate);
+    b = b > s ? b : s;
+  }
+  b = (b + 127) / 128 * 128;
+  return (int)(b < MAX_CH ? b : MAX_CH);
+}
+
 int scale_slot(const moe_config &c) {
   // 16 rows of K/64 scales and biases, 2 bytes each
   const int K = c.hidden > c.intermediate ? c.hidden : c.intermediate;
@@ -1180,8 +1225,8 @@ int scale_slots(const moe_config &c) {
 
 bool few_supported(const moe_config &c) {
   if (c.num_tokens > kFewTokens || c.act_dtype != MOE_BF16) return false;
-  // at least four stages beside the scales
-  return sizeof(Shared) + (size_t)scale_slots(c) * scale_slot(c) + 4 * (size_t)STAGE_BYTES <= (size_t)SMEM_LIMIT;
+  // at least three stages beside the scales
+  return sizeof(Shared) + (size_t)scale_slots(c) * scale_slot(c) + 3 * (size_t)(ROWS * (MAX_CH + 64)) <= (size_t)SMEM_LIMIT;
 }
 
 size_t few_bytes(const moe_config &c) { return few_supported(c) ? few_layout(c).total : 0; }
@@ -1236,6 +1281,8 @@ cudaError_t launch_few(const FewArgs &a, cudaStream_t s) {
   p.rowmax = reinterpret_cast<unsigned *>(ws + L.rowmax);
   p.hq = reinterpret_cast<int8_t *>(ws + L.hq);
   p.y = reinterpret_cast<float *>(ws + L.y);
+  p.ch = stage_ch(c);
+  p.stage_bytes = ROWS * (p.ch + 64);
   p.sc_slot = scale_slot(c);
   p.sc_slots = scale_slots(c);
   switch (c.weight_dtype) {
