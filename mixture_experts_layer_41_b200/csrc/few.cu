@@ -61,8 +61,8 @@ constexpr int THREADS = CT + 32;
 constexpr int MAX_CH = 2048;                // most bytes of a row per stage
 constexpr int ROWS = 16;                    // weight rows per task
 constexpr int MAX_STAGES = 24;
-constexpr int MAX_SC = 12;                  // 4-bit: tasks whose scales and biases are held at once
-constexpr int SC_BYTES = 40 * 1024;         // and the shared memory they may take (two tasks at least)
+constexpr int MAX_SC = CW;                  // 4-bit: tasks whose scales and biases are held at once
+constexpr int SC_BYTES = 64 * 1024;         // and the shared memory they may take (two tasks at least)
 constexpr int MAX_T = kFewTokens;
 constexpr int MAX_SLOTS = MAX_T * kMaxTopK;
 constexpr int SMEM_LIMIT = 227 * 1024;
@@ -107,6 +107,7 @@ struct FewParams {
   float *y;                                 // [T*k + T][d] expert outputs, then the shared expert's
   int ch;                                   // bytes of a row per stage, a multiple of 128
   int stage_bytes, stages;
+  int solo;                                 // warps that take tasks by themselves where rows are short
   int sc_slot, sc_slots;                    // 4-bit: bytes of one task's scales and biases, and how many are held
 };
 
@@ -346,6 +347,14 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) {
   return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
 }
+// n arrivals at once
+__device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+// the larger magnitude, NaN above all
+__device__ __forceinline__ float abs_max(float a, float b) {
+  return __uint_as_float(max(__float_as_uint(a) & 0x7FFFFFFFu, __float_as_uint(b) & 0x7FFFFFFFu));
+}
 __device__ __forceinline__ uint4 lds128(const uint8_t *p) { return *reinterpret_cast<const uint4 *>(p); }
 
 // B operand of one 64-byte segment of weight rows.  bf16 and 8-bit: 16 bytes
@@ -356,7 +365,11 @@ struct BSeg {
   uint4 v[FMT == Q4 ? 4 : 1][LO ? 2 : 1];
 };
 
-constexpr int SEGS = MAX_CH / 64 / CW;      // segments per warp and stage
+// segments whose operand a warp holds at once (4-bit: four times the registers each)
+template <int FMT>
+__host__ __device__ constexpr int segs_of() {
+  return FMT == Q4 ? 2 : 4;
+}
 
 // bytes of the token row per byte of the weight row
 template <int FMT>
@@ -507,9 +520,58 @@ __device__ __forceinline__ const char *b_row(const FewParams &p, const Cursor &c
                    : reinterpret_cast<const char *>(p.h + (size_t)(cu.row0 + r) * p.F);
 }
 
-// The block's tasks of one part.
-template <int FMT, int PART, int NB>
-__device__ __forceinline__ void consume_part(const FewParams &p, Ring &r, uint32_t &red_it) {
+// What becomes of one finished value: row f of the task's `cols` (with its up
+// projection u where the task holds pairs), token tok.  Returns the magnitude
+// of the stored bf16 h (8-bit weights: the row maxima are taken from it).
+template <int FMT, int PART>
+__device__ __forceinline__ float emit(const FewParams &p, const Cursor &cu, int f, int tok, float v, float u) {
+  constexpr bool PHASE2 = PART == S2 || PART == R2;
+  const bool pairs = PART == S1 || (PART == R1 && p.swiglu);
+  const int col = cu.b * (pairs ? 8 : ROWS) + f;
+  const int N = PART == S1 ? p.Fs : (PART == R1 ? p.F : p.d);
+  if (tok >= cu.rows || col >= N) return 0.f;
+  const size_t row = (size_t)cu.row0 + tok;
+  if (FMT == I8) {
+    // row scale: of the token (phase 1), of the row of h (phase 2)
+    float xs;
+    if (PHASE2) {
+      const uint32_t top = __ldcg(p.rowmax + row);
+      xs = top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __fdiv_rn(__uint_as_float(top), 127.f);
+    } else {
+      xs = __ldcg(p.xs + nth_bit(cu.mask, tok));
+    }
+    const size_t r0 = (size_t)cu.e * (PHASE2 ? p.d : p.w_stride) + col;
+    v *= xs * __ldg(static_cast<const float *>(PHASE2 ? p.s3 : p.s1) + r0);
+    if (pairs) u *= xs * __ldg(static_cast<const float *>(p.s2) + r0);
+  }
+  if (PHASE2) {
+    p.y[(PART == S2 ? (size_t)p.T * p.k + tok : row) * p.d + col] = v;
+    return 0.f;
+  }
+  if (pairs) v = silu_f(v) * u;
+  else v = v < 0.f ? 0.f : v;               // a NaN stays one
+  const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+  uint16_t *h = PART == S1 ? p.hs + (size_t)tok * p.Fs + col : p.h + row * p.F + col;
+  *h = *reinterpret_cast<const uint16_t *>(&hi);
+  if (FMT == BF16) {
+    const float rest = v - __bfloat162float(hi);
+    const __nv_bfloat16 lo = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
+    h[PART == S1 ? p.hs_lo : p.h_lo] = *reinterpret_cast<const uint16_t *>(&lo);
+  }
+  return __bfloat162float(hi);
+}
+
+// The block's tasks of one part.  Long rows: the eight warps split each
+// stage's K, and their partial results meet in shared memory.  SOLO, rows that
+// fit one stage: each of p.solo warps takes every p.solo-th task by itself, so
+// nothing waits for the other warps (a short task's barrier and sum took
+// longer than its weights: 16 tokens over 4-bit experts, 83 of them at
+// d = 2048, F = 768, ran 261 us that way).  The number of stages (and of scale
+// slots) is a multiple of p.solo, so within a part a stage always serves the
+// same warp: a barrier's parity tells a warp only whether the use it waits
+// for is over if it has seen the one before.
+template <int FMT, int PART, int NB, bool SOLO>
+__device__ __noinline__ void consume_part(const FewParams &p, Ring &r, uint32_t &red_it) {
   Shared *sh = r.sh;
   constexpr bool PHASE2 = PART == S2 || PART == R2;
   constexpr bool LO = PHASE2 && FMT == BF16;
@@ -521,171 +583,211 @@ __device__ __forceinline__ void consume_part(const FewParams &p, Ring &r, uint32
   const int rb = row_bytes<FMT>(K);
   const int groups = K / 64;
   const size_t lo_bytes = 2 * (PART == S2 ? p.hs_lo : p.h_lo);
-  const int ch = p.ch;
-  const int w0 = warp * 64;                 // this warp's first segment of a stage
-  constexpr int STEP = CW * 64;             // and the distance to its next
+  const int w0 = SOLO ? 0 : warp * 64;      // this warp's first segment of a piece
+  constexpr int STEP = SOLO ? 64 : CW * 64; // and the distance to its next
+  constexpr int SEGS = segs_of<FMT>();
+  constexpr int FULL = SEGS * STEP;         // bytes of a row in a whole piece
+  const int start = min(min(FULL, p.ch), rb);   // and in a row's first
   const int lane_b = (w0 + c * (FMT == Q4 ? 8 : 16)) * R;
-  const uint32_t row_lo = g * (ch + pad_of(FMT)) + w0 + c * (FMT == Q4 ? 8 : 16);
-  const uint32_t row_hi = row_lo + 8 * (ch + pad_of(FMT));
+  const uint32_t row_lo = g * (p.ch + pad_of(FMT)) + w0 + c * (FMT == Q4 ? 8 : 16);
+  const uint32_t row_hi = row_lo + 8 * (p.ch + pad_of(FMT));
   if (dm.first >= dm.count) return;
+  const int mine = (dm.count - dm.first + (int)gridDim.x - 1) / (int)gridDim.x;   // tasks of this block
+  const int stride = SOLO ? p.solo * (int)gridDim.x : (int)gridDim.x;
+  uint32_t st = r.st, ph = r.ph, sc_st = r.sc_st, sc_ph = r.sc_ph;
+  const int skip = SOLO ? min(warp, mine) : 0;
+  for (int i = 0; i < skip; ++i) {
+    advance(st, ph, p.stages);
+    if (FMT == Q4) advance(sc_st, sc_ph, p.sc_slots);
+  }
 
   Cursor cu;
-  cu.task = dm.first;
-  place<PART>(p, sh, dm, cu);
-  const char *bp[NB];                       // the stage's stretch of the token rows, at this lane
-  BSeg<FMT, LO> bv[SEGS][NBP];
+  cu.task = dm.first + (SOLO ? warp : 0) * (int)gridDim.x;
+  if (cu.task < dm.count && (!SOLO || warp < p.solo)) {
+    place<PART>(p, sh, dm, cu);
+    const char *bp[NB];                     // the piece's stretch of the token rows, at this lane
+    BSeg<FMT, LO> bv[SEGS][NBP];
 #pragma unroll
-  for (int n = 0; n < NB; ++n) bp[n] = b_row<FMT, PART>(p, cu, g + 8 * n) + lane_b;
+    for (int n = 0; n < NB; ++n) bp[n] = b_row<FMT, PART>(p, cu, g + 8 * n) + lane_b;
 #pragma unroll
-  for (int s = 0; s < SEGS; ++s)
+    for (int s = 0; s < SEGS; ++s)
 #pragma unroll
-    for (int n = 0; n < NBP; ++n)
-      load_b<FMT, LO, true>(bv[s][n], bp[n] + s * STEP * R, lo_bytes, min(ch, rb) - w0 - s * STEP, c);
+      for (int n = 0; n < NBP; ++n)
+        load_b<FMT, LO, true>(bv[s][n], bp[n] + s * STEP * R, lo_bytes, start - w0 - s * STEP, c);
 
-  for (;;) {
-    Acc<FMT, NB> acc;
+    for (;;) {
+      Acc<FMT, NB> acc;
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
+      for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc.f[n][0][j] = acc.f[n][1][j] = 0;
-    Cursor nx = cu;
-    nx.task += gridDim.x;
-    const bool more = nx.task < dm.count;
-    const bool second = cu.rows > 8;
-    const uint16_t *sc = nullptr;
-    if (FMT == Q4) {
-      wait_on(&sh->sc_full[r.sc_st], r.sc_ph, sh, p, kDevTimeoutEpilogue);
-      sc = reinterpret_cast<const uint16_t *>(r.sc + (size_t)r.sc_st * p.sc_slot) + g * groups + w0 / 32;
-    }
-    for (int off = 0; off < rb; off += ch) {
-      // where the next stage's token operand comes from: its loads take the
-      // registers of each segment as soon as that has been used
-      const bool last = off + ch >= rb;
-      const char *bn[NB];
-      int next_left;                        // bytes of the weight rows in the next stage, none: 0
-      if (!last) {
-        next_left = min(ch, rb - off - ch);
-#pragma unroll
-        for (int n = 0; n < NB; ++n) bn[n] = bp[n] + ch * R;
-      } else {
-        next_left = more ? min(ch, rb) : 0;
-        if (more) place<PART>(p, sh, dm, nx);
-#pragma unroll
-        for (int n = 0; n < NB; ++n) bn[n] = more ? b_row<FMT, PART>(p, nx, g + 8 * n) + lane_b : bp[n];
+        for (int j = 0; j < 4; ++j) acc.f[n][0][j] = acc.f[n][1][j] = 0;
+      Cursor nx = cu;
+      nx.task += stride;
+      const bool more = nx.task < dm.count;
+      const bool second = cu.rows > 8;
+      const uint16_t *sc = nullptr;
+      if (FMT == Q4) {
+        wait_on(&sh->sc_full[sc_st], sc_ph, sh, p, kDevTimeoutEpilogue);
+        sc = reinterpret_cast<const uint16_t *>(r.sc + (size_t)sc_st * p.sc_slot) + g * groups + w0 / 32;
       }
-      const uint8_t *tile = r.tiles + (size_t)r.st * p.stage_bytes;
-      const int left = min(ch, rb - off);
-      wait_on(&sh->full[r.st], r.ph, sh, p, kDevTimeoutEpilogue);
-      __syncwarp();
-      if (left == MAX_CH && next_left == MAX_CH) {
+      int in = 0;                           // bytes of the rows before this piece in its stage
+      for (int off = 0, left; off < rb; off += left) {
+        left = min(min(FULL, p.ch - in), rb - off);
+        // where the next piece's token operand comes from: its loads take the
+        // registers of each segment as soon as that has been used
+        const bool last = off + left >= rb;
+        const bool ends = last || in + left == p.ch;        // of the stage
+        const char *bn[NB];
+        int next_left;                      // bytes of the weight rows in the next piece, none: 0
+        if (!last) {
+          next_left = min(min(FULL, ends ? p.ch : p.ch - in - left), rb - off - left);
 #pragma unroll
-        for (int s = 0; s < SEGS; ++s) {
-          consume<FMT, LO, NB, NBP, false>(acc, bv[s], bp[NB - 1] + s * STEP * R, 64, tile + row_lo + s * STEP,
-                                           tile + row_hi + s * STEP, second, c, sc + (off + s * STEP) / 32, groups);
-#pragma unroll
-          for (int n = 0; n < NBP; ++n) load_b<FMT, LO, false>(bv[s][n], bn[n] + s * STEP * R, lo_bytes, 64, c);
-        }
-      } else {
-#pragma unroll
-        for (int s = 0; s < SEGS; ++s) {
-          const int at = w0 + s * STEP;
-          if (at < left)
-            consume<FMT, LO, NB, NBP, true>(acc, bv[s], bp[NB - 1] + s * STEP * R, left - at, tile + row_lo + s * STEP,
-                                            tile + row_hi + s * STEP, second, c, sc + (off + s * STEP) / 32, groups);
-#pragma unroll
-          for (int n = 0; n < NBP; ++n) load_b<FMT, LO, true>(bv[s][n], bn[n] + s * STEP * R, lo_bytes, next_left - at, c);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->empty[r.st]);
-      advance(r.st, r.ph, p.stages);
-#pragma unroll
-      for (int n = 0; n < NB; ++n) bp[n] = bn[n];
-    }
-    // the eight warps' partial results meet; two buffers in turn, so one
-    // barrier per task keeps writers and readers apart
-    uint32_t(*red)[2][32][4] = sh->red[red_it & 1u];
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      uint32_t v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const auto sum = acc.f[n][0][j] + acc.f[n][1][j];
-        if constexpr (FMT == I8) v[j] = (uint32_t)sum;
-        else v[j] = __float_as_uint(sum);
-      }
-      *reinterpret_cast<uint4 *>(red[warp][n][lane]) = make_uint4(v[0], v[1], v[2], v[3]);
-    }
-    consumer_sync();
-    if (FMT == Q4) {
-      if (threadIdx.x == 0) mbar_arrive(&sh->sc_empty[r.sc_st]);
-      advance(r.sc_st, r.sc_ph, p.sc_slots);
-    }
-    ++red_it;
-    // value (row, token) of the task: accumulator j of lane 4 (row % 8) + (token % 8) / 2
-    auto total = [&](int row, int tok) {
-      const int ln = (row & 7) * 4 + ((tok & 7) >> 1), j = (tok & 1) + (row >> 3) * 2, n = tok >> 3;
-      if (FMT == I8) {
-        int v = 0;
-#pragma unroll
-        for (int w = 0; w < CW; ++w) v += (int)red[w][n][ln][j];
-        return (float)v;
-      }
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < CW; ++w) v += __uint_as_float(red[w][n][ln][j]);
-      return v;
-    };
-    const bool pairs = PART == S1 || (PART == R1 && p.swiglu);
-    const int cols = pairs ? 8 : ROWS;
-    const int N = PART == S1 ? p.Fs : (PART == R1 ? p.F : p.d);
-    for (int i = threadIdx.x; i < cols * 8 * NB; i += CT) {       // whole warps take part
-      const int tok = i / cols, f = i - tok * cols, col = cu.b * cols + f;
-      const bool live = tok < cu.rows && col < N;
-      const size_t row = (size_t)cu.row0 + tok;
-      float v = 0.f;
-      if (live) {
-        v = total(f, tok);
-        float xs = 1.f;
-        size_t r0 = 0;
-        if (FMT == I8) {
-          // row scale: of the token (phase 1), of the row of h (phase 2)
-          xs = PHASE2 ? __fdiv_rn(__uint_as_float(__ldcg(p.rowmax + row)), 127.f) : __ldcg(p.xs + nth_bit(cu.mask, tok));
-          if (PHASE2 && __ldcg(p.rowmax + row) >= 0x7F800000u) xs = __uint_as_float(0x7FC00000u);
-          r0 = (size_t)cu.e * (PHASE2 ? p.d : p.w_stride) + col;
-          v *= xs * __ldg(static_cast<const float *>(PHASE2 ? p.s3 : p.s1) + r0);
-        }
-        if (pairs) {
-          float u = total(f + 8, tok);
-          if (FMT == I8) u *= xs * __ldg(static_cast<const float *>(p.s2) + r0);
-          v = silu_f(v) * u;
-        } else if (PART == R1) {
-          v = v < 0.f ? 0.f : v;            // a NaN stays one
-        }
-        if (PHASE2) {
-          p.y[(PART == S2 ? (size_t)p.T * p.k + tok : row) * p.d + col] = v;
+          for (int n = 0; n < NB; ++n) bn[n] = bp[n] + left * R;
         } else {
-          const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-          uint16_t *h = PART == S1 ? p.hs + (size_t)tok * p.Fs + col : p.h + row * p.F + col;
-          *h = *reinterpret_cast<const uint16_t *>(&hi);
-          if (FMT == BF16) {
-            const float rest = v - __bfloat162float(hi);
-            const __nv_bfloat16 lo = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
-            h[PART == S1 ? p.hs_lo : p.h_lo] = *reinterpret_cast<const uint16_t *>(&lo);
+          next_left = more ? start : 0;
+          if (more) place<PART>(p, sh, dm, nx);
+#pragma unroll
+          for (int n = 0; n < NB; ++n) bn[n] = more ? b_row<FMT, PART>(p, nx, g + 8 * n) + lane_b : bp[n];
+        }
+        const uint8_t *tile = r.tiles + (size_t)st * p.stage_bytes + in;
+        if (in == 0) wait_on(&sh->full[st], ph, sh, p, kDevTimeoutEpilogue);
+        __syncwarp();
+        if (left == FULL && next_left == FULL) {
+#pragma unroll
+          for (int s = 0; s < SEGS; ++s) {
+            consume<FMT, LO, NB, NBP, false>(acc, bv[s], bp[NB - 1] + s * STEP * R, 64, tile + row_lo + s * STEP,
+                                             tile + row_hi + s * STEP, second, c, sc + (off + s * STEP) / 32, groups);
+#pragma unroll
+            for (int n = 0; n < NBP; ++n) load_b<FMT, LO, false>(bv[s][n], bn[n] + s * STEP * R, lo_bytes, 64, c);
           }
-          v = __bfloat162float(hi);
+        } else {
+#pragma unroll
+          for (int s = 0; s < SEGS; ++s) {
+            const int at = w0 + s * STEP;
+            if (at < left)
+              consume<FMT, LO, NB, NBP, true>(acc, bv[s], bp[NB - 1] + s * STEP * R, left - at,
+                                              tile + row_lo + s * STEP, tile + row_hi + s * STEP, second, c,
+                                              sc + (off + s * STEP) / 32, groups);
+#pragma unroll
+            for (int n = 0; n < NBP; ++n)
+              load_b<FMT, LO, true>(bv[s][n], bn[n] + s * STEP * R, lo_bytes, next_left - at, c);
+          }
+        }
+        if (ends) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive_n(&sh->empty[st], SOLO ? CW : 1);
+          if (!SOLO) advance(st, ph, p.stages);
+          in = 0;
+        } else {
+          in += left;
+        }
+#pragma unroll
+        for (int n = 0; n < NB; ++n) bp[n] = bn[n];
+      }
+      if (SOLO) {
+        if (FMT == Q4 && lane == 0) mbar_arrive(&sh->sc_empty[sc_st]);
+        for (int i = 0; i < p.solo; ++i) {
+          advance(st, ph, p.stages);
+          if (FMT == Q4) advance(sc_st, sc_ph, p.sc_slots);
+        }
+        // accumulators 0, 1: row g, tokens 2c, 2c + 1; 2, 3: row g + 8
+        const bool pairs = PART == S1 || (PART == R1 && p.swiglu);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          if (n > 0 && !second) break;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int tok = 8 * n + 2 * c + j;
+            const float a = (float)(acc.f[n][0][j] + acc.f[n][1][j]);
+            const float b = (float)(acc.f[n][0][j + 2] + acc.f[n][1][j + 2]);
+            float m = emit<FMT, PART>(p, cu, g, tok, a, b);
+            if (!pairs) m = abs_max(m, emit<FMT, PART>(p, cu, g + 8, tok, b, 0.f));
+            if (FMT == I8 && PART == R1) {
+              uint32_t top = __float_as_uint(m) & 0x7FFFFFFFu;
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+              if (g == 0 && tok < cu.rows) atomicMax(p.rowmax + cu.row0 + tok, top);
+            }
+          }
+        }
+      } else {
+        // the eight warps' partial results meet; two buffers in turn, so one
+        // barrier per task keeps writers and readers apart
+        uint32_t(*red)[2][32][4] = sh->red[red_it & 1u];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          uint32_t v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const auto sum = acc.f[n][0][j] + acc.f[n][1][j];
+            if constexpr (FMT == I8) v[j] = (uint32_t)sum;
+            else v[j] = __float_as_uint(sum);
+          }
+          *reinterpret_cast<uint4 *>(red[warp][n][lane]) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+        consumer_sync();
+        if (FMT == Q4) {
+          if (threadIdx.x == 0) mbar_arrive(&sh->sc_empty[sc_st]);
+          advance(sc_st, sc_ph, p.sc_slots);
+        }
+        ++red_it;
+        // value (row, token) of the task: accumulator j of lane 4 (row % 8) + (token % 8) / 2
+        auto total = [&](int row, int tok) {
+          const int ln = (row & 7) * 4 + ((tok & 7) >> 1), j = (tok & 1) + (row >> 3) * 2, n = tok >> 3;
+          if (FMT == I8) {
+            int v = 0;
+#pragma unroll
+            for (int w = 0; w < CW; ++w) v += (int)red[w][n][ln][j];
+            return (float)v;
+          }
+          float v = 0.f;
+#pragma unroll
+          for (int w = 0; w < CW; ++w) v += __uint_as_float(red[w][n][ln][j]);
+          return v;
+        };
+        const bool pairs = PART == S1 || (PART == R1 && p.swiglu);
+        const int cols = pairs ? 8 : ROWS;
+        const int most = cols * 8 * (second ? 2 : 1);
+        for (int i = threadIdx.x; i < most; i += CT) {            // whole warps take part
+          const int tok = i / cols, f = i - tok * cols;
+          const float m = tok < cu.rows ? emit<FMT, PART>(p, cu, f, tok, total(f, tok), pairs ? total(f + 8, tok) : 0.f) : 0.f;
+          if (FMT == I8 && PART == R1) {
+            // the row's largest |h|: over the task's columns (8 or 16 neighbouring lanes), then the grid
+            uint32_t top = __float_as_uint(m) & 0x7FFFFFFFu;
+            for (int o = 1; o < cols; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (f == 0 && tok < cu.rows) atomicMax(p.rowmax + cu.row0 + tok, top);
+          }
         }
       }
-      if (FMT == I8 && !PHASE2) {
-        // the row's largest |h|: over the task's columns (8 or 16 neighbouring lanes), then the grid
-        uint32_t m = __float_as_uint(v) & 0x7FFFFFFFu;
-        for (int o = 1; o < cols; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (f == 0 && tok < cu.rows) atomicMax(p.rowmax + row, m);
-      }
+      if (!more) break;
+      cu = nx;
     }
-    if (!more) break;
-    cu = nx;
   }
+  // every warp leaves the part at the same place of the ring, and together:
+  // the next part's uses follow ones that other warps waited for
+  if (SOLO) {
+    consumer_sync();
+    const uint32_t n = r.st + mine;
+    r.ph ^= n / p.stages & 1u;
+    r.st = n % p.stages;
+    if (FMT == Q4) {
+      const uint32_t m = r.sc_st + mine;
+      r.sc_ph ^= m / p.sc_slots & 1u;
+      r.sc_st = m % p.sc_slots;
+    }
+  } else {
+    r.st = st;
+    r.ph = ph;
+    r.sc_st = sc_st;
+    r.sc_ph = sc_ph;
+  }
+}
+
+template <int FMT, int PART, int NB>
+__device__ __forceinline__ void run_part(const FewParams &p, Ring &r, uint32_t &red_it) {
+  const int K = PART == S1 || PART == R1 ? p.d : (PART == S2 ? p.Fs : p.F);
+  if (row_bytes<FMT>(K) <= p.ch && p.solo >= CW / 2) consume_part<FMT, PART, NB, true>(p, r, red_it);
+  else consume_part<FMT, PART, NB, false>(p, r, red_it);
 }
 
 // ---------------------------------------------------------------- router
@@ -726,7 +828,7 @@ __device__ __forceinline__ void route_partials(const FewParams &p) {
 #pragma unroll
     for (int t = 0; t < TP; ++t) acc[t] = 0.0;
     const float *w = p.w_router + (size_t)e * p.d;
-#pragma unroll 2
+#pragma unroll (TP > 4 ? 1 : 4)
     for (int k = k0 + lane * 8; k < k1; k += 256) {
       const float4 wa = __ldg(reinterpret_cast<const float4 *>(w + k));
       const float4 wb = __ldg(reinterpret_cast<const float4 *>(w + k + 4));
@@ -746,13 +848,27 @@ __device__ __forceinline__ void route_partials(const FewParams &p) {
         }
       }
     }
+    // halving exchanges: each step keeps half of the tokens' sums on each half of the lanes
+    int have = TP;
 #pragma unroll
-    for (int t = 0; t < TP; ++t) {
-      if (t < p.T) {
-        const double s = warp_sum(acc[t]);
-        if (lane == 0) p.part[((size_t)sl * p.T + t) * p.E + e] = s;
+    for (int o = 16; o > 0; o >>= 1) {
+      if (have > 1) {
+        have >>= 1;
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < TP / 2; ++i)
+          if (i < have) {
+            const double give = up ? acc[i] : acc[i + have];
+            acc[i] = (up ? acc[i + have] : acc[i]) + __shfl_xor_sync(0xffffffffu, give, o);
+          }
+      } else {
+        acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
       }
     }
+    // the lane's token: its bits from 16 down chose the halves
+    constexpr int LOG = TP == 16 ? 4 : (TP == 8 ? 3 : (TP == 4 ? 2 : 0));
+    const int t = lane >> (5 - LOG);
+    if ((lane & ((32 >> LOG) - 1)) == 0 && t < p.T) p.part[((size_t)sl * p.T + t) * p.E + e] = acc[0];
   }
 }
 
@@ -770,8 +886,15 @@ __device__ __forceinline__ void choose(const FewParams &p, Shared *sh, int t, do
     prob[j] = 0.0;
     score[j] = -INFINITY;
     if (32 * j < E && e < E) {
+      // eight slices' loads in flight at a time
       double l = 0.0;
-      for (int s = 0; s < p.ks; ++s) l += __ldcg(p.part + ((size_t)s * p.T + t) * E + e);
+      for (int s0 = 0; s0 < p.ks; s0 += 8) {
+        double v[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) v[s] = s0 + s < p.ks ? __ldcg(p.part + ((size_t)(s0 + s) * p.T + t) * E + e) : 0.0;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) l += v[s];
+      }
       prob[j] = l;
     }
   }
@@ -1108,19 +1231,19 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.dropped = 0;
     route_partials<TP>(p);
     grid_arrive(p.bar);
-    if (p.Fs) consume_part<BF16, S1, NB>(p, r, red_it);
+    if (p.Fs) run_part<BF16, S1, NB>(p, r, red_it);
     grid_wait(p.bar, abort_flag, p);
     make_plan(p, sh);
-    consume_part<FMT, R1, NB>(p, r, red_it);
+    run_part<FMT, R1, NB>(p, r, red_it);
     grid_arrive(p.bar + 8);
     grid_wait(p.bar + 8, abort_flag, p);
     if (FMT == I8) {
       quantize_h(p, sh);
       grid_arrive(p.bar + 16);
     }
-    if (p.Fs) consume_part<BF16, S2, NB>(p, r, red_it);
+    if (p.Fs) run_part<BF16, S2, NB>(p, r, red_it);
     if (FMT == I8) grid_wait(p.bar + 16, abort_flag, p);
-    consume_part<FMT, R2, NB>(p, r, red_it);
+    run_part<FMT, R2, NB>(p, r, red_it);
     grid_arrive(p.bar + 24);
     grid_wait(p.bar + 24, abort_flag, p);
     combine(p, sh);
@@ -1132,7 +1255,11 @@ template <int FMT, int TP>
 cudaError_t run(FewParams &p, cudaStream_t s) {
   const size_t fixed = sizeof(Shared) + (size_t)p.sc_slots * p.sc_slot;
   int stages = (int)((SMEM_LIMIT - fixed) / p.stage_bytes);
-  p.stages = stages < MAX_STAGES ? stages : MAX_STAGES;
+  stages = stages < MAX_STAGES ? stages : MAX_STAGES;
+  p.solo = p.sc_slots && p.sc_slots < CW ? p.sc_slots : CW;
+  p.solo = stages < p.solo ? stages : p.solo;
+  if (p.sc_slots) p.sc_slots -= p.sc_slots % p.solo;
+  p.stages = stages - stages % p.solo;
   const size_t smem = fixed + (size_t)p.stages * p.stage_bytes;
   auto kern = few_kernel<FMT, TP>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
