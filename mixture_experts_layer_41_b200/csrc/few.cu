@@ -7,7 +7,8 @@
 // through shared memory without a pause, from the first product to the last.
 //
 //   router    each warp dots one expert's slice of the hidden dimension with
-//             every token (fp32 products over runs of 8, float64 sums);
+//             every token (fp32 products over runs of 8, float64 sums); the
+//             shared expert's first product runs before anyone waits for it;
 //   choice    after a grid barrier every block selects for all tokens from
 //             the same partial sums (float64, ties to the lower expert) and
 //             builds the same plan: per expert a 16-bit mask of its tokens in
@@ -111,6 +112,8 @@ struct FewParams {
   int sc_slot, sc_slots;                    // 4-bit: bytes of one task's scales and biases, and how many are held
 };
 
+__host__ __device__ constexpr size_t scratch_bytes(int T, int E) { return ((size_t)T * E * 8 + 127) / 128 * 128; }
+
 struct Shared {
   uint64_t full[MAX_STAGES];
   uint64_t empty[MAX_STAGES];
@@ -124,10 +127,10 @@ struct Shared {
   int sel_id[MAX_SLOTS];
   float sel_w[MAX_SLOTS];
   int16_t slot_row[MAX_SLOTS];
-  // partial results of the consumer warps, two tasks in turn; scratch of the choice
+  int warp_n[CW], warp_rows[CW];            // per 32 experts: how many have rows, and the rows
+  // partial results of the consumer warps, two tasks in turn
   __align__(16) uint32_t red[2][CW][2][32][4];
 };
-static_assert(sizeof(((Shared *)0)->red) >= CW * kMaxExperts * sizeof(double), "selection scratch");
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(CT) : "memory"); }
 
@@ -168,10 +171,11 @@ __device__ __forceinline__ void grid_wait(unsigned *ctr, volatile int *abort_fla
 
 // ---------------------------------------------------------------- tasks
 // One task: 16 weight rows.  The order of a block's tasks is the same for the
-// producer and the consumers: shared phase 1, routed phase 1, shared phase 2,
+// producer and the consumers: shared phase 1, shared phase 2, routed phase 1,
 // routed phase 2, each strided over the blocks, the stride running on from
-// one part to the next.
-enum Part { S1 = 0, R1 = 1, S2 = 2, R2 = 3 };
+// one part to the next.  The shared expert needs no choice, so its weights
+// stream while the router, the first barrier and the plan take their time.
+enum Part { S1 = 0, S2 = 1, R1 = 2, R2 = 3 };
 
 struct Dims {
   int nb;        // row blocks per expert
@@ -182,8 +186,8 @@ struct Dims {
 __device__ __forceinline__ Dims part_dims(const FewParams &p, int part, int nact) {
   const int nbs1 = p.Fs / 8, nbs2 = p.Fs ? (p.d + ROWS - 1) / ROWS : 0;
   const int nb1 = p.swiglu ? p.F / 8 : (p.F + ROWS - 1) / ROWS, nb2 = (p.d + ROWS - 1) / ROWS;
-  const int counts[4] = {nbs1, nact * nb1, nbs2, nact * nb2};
-  const int nbs[4] = {nbs1, nb1, nbs2, nb2};
+  const int counts[4] = {nbs1, nbs2, nact * nb1, nact * nb2};
+  const int nbs[4] = {nbs1, nbs2, nb1, nb2};
   long long before = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -248,6 +252,7 @@ struct Ring {
   Shared *sh;
   uint8_t *tiles;
   uint8_t *sc;                              // 4-bit: the slots of scales and biases
+  uint8_t *scratch;                         // [T][E] doubles: the tokens' probabilities
   uint32_t st, ph;                          // next stage and the parity of its use
   uint32_t sc_st, sc_ph;                    // likewise the next scale slot
   uint32_t issued, sc_issued;               // producer: copies' stages and slots so far
@@ -815,6 +820,10 @@ __device__ __forceinline__ void warp_argmax(double &v, int &i) {
   v = __longlong_as_double((long long)((mk >> 63) ? (mk & 0x7FFFFFFFFFFFFFFFull) : ~mk));
 }
 
+// steps of 256 elements in a router slice, for tokens padded to TP
+__host__ __device__ constexpr int route_steps(int TP) { return TP <= 4 ? 8 : (TP <= 8 ? 4 : 2); }
+__host__ __device__ constexpr int pad_tokens(int T) { return T <= 1 ? 1 : (T <= 4 ? 4 : (T <= 8 ? 8 : 16)); }
+
 // Partial logits: unit (expert, slice of the hidden dimension) per warp.
 template <int TP>
 __device__ __forceinline__ void route_partials(const FewParams &p) {
@@ -828,23 +837,37 @@ __device__ __forceinline__ void route_partials(const FewParams &p) {
 #pragma unroll
     for (int t = 0; t < TP; ++t) acc[t] = 0.0;
     const float *w = p.w_router + (size_t)e * p.d;
-#pragma unroll (TP > 4 ? 1 : 4)
-    for (int k = k0 + lane * 8; k < k1; k += 256) {
-      const float4 wa = __ldg(reinterpret_cast<const float4 *>(w + k));
-      const float4 wb = __ldg(reinterpret_cast<const float4 *>(w + k + 4));
+    // the slice's weights are all in flight before the first is used
+    constexpr int IT = route_steps(TP);
+    float4 wv[IT][2];
 #pragma unroll
-      for (int t = 0; t < TP; ++t) {
-        if (t < p.T) {
-          const uint4 xv = __ldg(reinterpret_cast<const uint4 *>(p.x + (size_t)t * p.d + k));
-          float run = __uint_as_float(xv.x << 16) * wa.x;
-          run = fmaf(__uint_as_float(xv.x & 0xffff0000u), wa.y, run);
-          run = fmaf(__uint_as_float(xv.y << 16), wa.z, run);
-          run = fmaf(__uint_as_float(xv.y & 0xffff0000u), wa.w, run);
-          run = fmaf(__uint_as_float(xv.z << 16), wb.x, run);
-          run = fmaf(__uint_as_float(xv.z & 0xffff0000u), wb.y, run);
-          run = fmaf(__uint_as_float(xv.w << 16), wb.z, run);
-          run = fmaf(__uint_as_float(xv.w & 0xffff0000u), wb.w, run);
-          acc[t] += (double)run;
+    for (int i = 0; i < IT; ++i) {
+      const int k = k0 + (lane + 32 * i) * 8;
+      wv[i][0] = wv[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k < k1) {
+        wv[i][0] = __ldg(reinterpret_cast<const float4 *>(w + k));
+        wv[i][1] = __ldg(reinterpret_cast<const float4 *>(w + k + 4));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int k = k0 + (lane + 32 * i) * 8;
+      if (k < k1) {
+        const float4 wa = wv[i][0], wb = wv[i][1];
+#pragma unroll
+        for (int t = 0; t < TP; ++t) {
+          if (t < p.T) {
+            const uint4 xv = __ldg(reinterpret_cast<const uint4 *>(p.x + (size_t)t * p.d + k));
+            float run = __uint_as_float(xv.x << 16) * wa.x;
+            run = fmaf(__uint_as_float(xv.x & 0xffff0000u), wa.y, run);
+            run = fmaf(__uint_as_float(xv.y << 16), wa.z, run);
+            run = fmaf(__uint_as_float(xv.y & 0xffff0000u), wa.w, run);
+            run = fmaf(__uint_as_float(xv.z << 16), wb.x, run);
+            run = fmaf(__uint_as_float(xv.z & 0xffff0000u), wb.y, run);
+            run = fmaf(__uint_as_float(xv.w << 16), wb.z, run);
+            run = fmaf(__uint_as_float(xv.w & 0xffff0000u), wb.w, run);
+            acc[t] += (double)run;
+          }
         }
       }
     }
@@ -874,76 +897,53 @@ __device__ __forceinline__ void route_partials(const FewParams &p) {
 
 constexpr int EPL = kMaxExperts / 32;
 
-// One token's choice: ids and weights to shared memory, probabilities added
-// to psum (expert lane + 32 j).
-__device__ __forceinline__ void choose(const FewParams &p, Shared *sh, int t, double (&psum)[EPL], double *wscr,
-                                       int lane) {
+// One token's choice from its row of `prob` (softmax: shifted logits, made
+// probabilities here; sigmoid: probabilities); ids and weights to shared
+// memory.  A warp; expert lane + 32 j.
+__device__ __forceinline__ void choose(const FewParams &p, Shared *sh, int t, double *prob, int lane) {
   const int E = p.E;
-  double prob[EPL], score[EPL];
+  double score[EPL];
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    const int e = lane + 32 * j;
-    prob[j] = 0.0;
-    score[j] = -INFINITY;
-    if (32 * j < E && e < E) {
-      // eight slices' loads in flight at a time
-      double l = 0.0;
-      for (int s0 = 0; s0 < p.ks; s0 += 8) {
-        double v[8];
+  for (int j = 0; j < EPL; ++j) score[j] = lane + 32 * j < E ? prob[lane + 32 * j] : -INFINITY;
+  bool number = false;
 #pragma unroll
-        for (int s = 0; s < 8; ++s) v[s] = s0 + s < p.ks ? __ldcg(p.part + ((size_t)(s0 + s) * p.T + t) * E + e) : 0.0;
-#pragma unroll
-        for (int s = 0; s < 8; ++s) l += v[s];
-      }
-      prob[j] = l;
-    }
-  }
+  for (int j = 0; j < EPL; ++j) number |= lane + 32 * j < E && score[j] == score[j];
+  // a token without a single number among its scores chooses nothing
+  const bool none = !__any_sync(0xffffffffu, number);
   if (p.router == MOE_ROUTER_SOFTMAX_TOPK) {
     double m = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (lane + 32 * j < E) {
-        if (p.bias) prob[j] += (double)__ldg(p.bias + lane + 32 * j);
-        m = fmax(m, prob[j]);
-      }
+    for (int j = 0; j < EPL; ++j) m = fmax(m, score[j]);
     m = warp_max(m);
     double s = 0.0;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (lane + 32 * j < E) {
-        prob[j] = exp(prob[j] - m);
-        s += prob[j];
-      }
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32) {
+      const double v = exp(prob[e] - m);
+      prob[e] = v;
+      s += v;
+    }
     s = warp_sum(s);
-#pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (lane + 32 * j < E) {
-        prob[j] = prob[j] / s;
-        score[j] = prob[j];
-      }
-  } else {
-#pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (lane + 32 * j < E) {
-        const int e = lane + 32 * j;
-        prob[j] = 1.0 / (1.0 + exp(-prob[j]));
-        score[j] = prob[j] + (p.bias ? (double)__ldg(p.bias + e) : 0.0);
-        wscr[e] = score[j];
-      }
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32) prob[e] = prob[e] / s;
     __syncwarp();
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) score[j] = lane + 32 * j < E ? prob[lane + 32 * j] : -INFINITY;
+  } else {
     // group score = sum of the two largest selection scores in the group
     const int G = E / p.n_group;
     double gs = -INFINITY;
     if (lane < p.n_group) {
       double b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll 4
       for (int q = 0; q < G; ++q) {
-        const double v = wscr[lane * G + q];
+        const double v = prob[lane * G + q] + (p.bias ? (double)__ldg(p.bias + lane * G + q) : 0.0);
         if (v > b1) { b2 = b1; b1 = v; } else if (v > b2) { b2 = v; }
       }
       gs = b1 + b2;
     }
     __syncwarp();
     uint32_t keep = 0;
+#pragma unroll 1
     for (int r = 0; r < p.topk_group; ++r) {
       const bool open = lane < p.n_group && !((keep >> lane) & 1u);
       double v = open ? gs : -INFINITY;
@@ -952,21 +952,18 @@ __device__ __forceinline__ void choose(const FewParams &p, Shared *sh, int t, do
       keep |= 1u << (gi & 31);
     }
 #pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (lane + 32 * j < E && !((keep >> ((lane + 32 * j) / G)) & 1u)) score[j] = -INFINITY;
+    for (int j = 0; j < EPL; ++j) {
+      const int e = lane + 32 * j;
+      if (e < E) {
+        if (p.bias) score[j] += (double)__ldg(p.bias + e);
+        if (!((keep >> (e / G)) & 1u)) score[j] = -INFINITY;
+      }
+    }
   }
-  // a token without a single number among its scores chooses nothing
-  bool number = false;
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    psum[j] += prob[j];
-    number |= lane + 32 * j < E && prob[j] == prob[j];
-  }
-  const bool none = !__any_sync(0xffffffffu, number);
 
   uint32_t taken = 0;
   int my_e = -1;
-  double my_w = 0.0;
+#pragma unroll 1
   for (int r = 0; r < p.k; ++r) {
     double bv = -INFINITY;
     int bi = 0x7fffffff;
@@ -979,99 +976,118 @@ __device__ __forceinline__ void choose(const FewParams &p, Shared *sh, int t, do
       }
     }
     warp_argmax(bv, bi);
-    double wv = 0.0;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (lane + 32 * j == bi && bi < E) {
-        wv = prob[j];
-        taken |= 1u << j;
-      }
-    wv = __shfl_sync(0xffffffffu, wv, bi & 31);
-    if (lane == r) { my_e = bi; my_w = wv; }
+    if ((bi & 31) == lane && bi < E) taken |= 1u << (bi >> 5);
+    if (lane == r) my_e = bi;
   }
-  const double tot = warp_sum(lane < p.k ? my_w : 0.0);
+  const bool bad = none || my_e < 0 || my_e >= E;
+  const double my_w = lane < p.k && my_e >= 0 && my_e < E ? prob[my_e] : 0.0;
+  const double tot = warp_sum(my_w);
   double wout;
   if (p.router == MOE_ROUTER_SOFTMAX_TOPK) wout = p.norm ? my_w / fmax(tot, 1e-12) : my_w;
   else wout = (p.norm ? my_w / (tot + 1e-20) : my_w) * p.scaling;
   if (lane < p.k) {
-    const bool bad = none || my_e < 0 || my_e >= E;
     if (bad && blockIdx.x == 0) record_status(p.status, kDevBadExpertId);
     sh->sel_id[t * p.k + lane] = bad ? -1 : my_e;
     sh->sel_w[t * p.k + lane] = (float)wout;
   }
 }
 
-// Choice for every token and the plan, the same in every block.
-__device__ __forceinline__ void make_plan(const FewParams &p, Shared *sh) {
+// Choice for every token and the plan, the same in every block.  The loops
+// that run once per expert stay rolled: a block runs this code once per
+// launch, and fetching its instructions is much of its time.
+__device__ __noinline__ void make_plan(const FewParams &p, Shared *sh, double *prob) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  double *scratch = reinterpret_cast<double *>(sh->red);
-  double psum[EPL];
+  sh->mask[tid] = 0u;
+  static_assert(CT == kMaxExperts, "a thread per expert");
+  // logits (softmax: with the bias) or sigmoid scores, a thread per (token, expert)
+#pragma unroll 1
+  for (int i = tid; i < p.T * p.E; i += CT) {
+    double l = 0.0;
+#pragma unroll 1
+    for (int s0 = 0; s0 < p.ks; s0 += 8) {             // eight slices' loads in flight at a time
+      double v[8];
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) psum[j] = 0.0;
-  for (int e = tid; e < kMaxExperts; e += CT) sh->mask[e] = 0u;
-  for (int t = warp; t < p.T; t += CW) choose(p, sh, t, psum, scratch + warp * kMaxExperts, lane);
-  consumer_sync();
-  const int slots = p.T * p.k;
-  for (int i = tid; i < slots; i += CT)
-    if (sh->sel_id[i] >= 0) atomicOr(&sh->mask[sh->sel_id[i]], 1u << (i / p.k));
-  if (blockIdx.x == 0) {
+      for (int s = 0; s < 8; ++s) v[s] = s0 + s < p.ks ? __ldcg(p.part + (size_t)(s0 + s) * p.T * p.E + i) : 0.0;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) scratch[warp * kMaxExperts + lane + 32 * j] = psum[j];
+      for (int s = 0; s < 8; ++s) l += v[s];
+    }
+    if (p.router == MOE_ROUTER_SOFTMAX_TOPK) {
+      if (p.bias) l += (double)__ldg(p.bias + i % p.E);
+    } else {
+      l = 1.0 / (1.0 + exp(-l));
+    }
+    prob[i] = l;
   }
   consumer_sync();
-  if (blockIdx.x == 0)
+#pragma unroll 1
+  for (int t = warp; t < p.T; t += CW) choose(p, sh, t, prob + (size_t)t * p.E, lane);
+  consumer_sync();
+  const int slots = p.T * p.k;
+#pragma unroll 1
+  for (int i = tid; i < slots; i += CT) {
+    const int e = sh->sel_id[i];
+    if (e >= 0) atomicOr(&sh->mask[e], 1u << (i / p.k));
+  }
+  consumer_sync();
+  // thread e: expert e.  In-order dropping: the first `cap` tokens stay
+  uint32_t m = sh->mask[tid];
+  const int raw = __popc(m);
+  if (p.cap >= 0)
+    while (__popc(m) > p.cap) m &= ~(0x80000000u >> __clz(m));
+  const int cnt = __popc(m);
+  const unsigned live = __ballot_sync(0xffffffffu, cnt > 0);
+  int pre = cnt;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, pre, o);
+    if (lane >= o) pre += v;
+  }
+  if (lane == 31) {
+    sh->warp_n[warp] = __popc(live);
+    sh->warp_rows[warp] = pre;
+  }
+  sh->mask[tid] = m;
+  consumer_sync();
+  int n = 0, rows = 0, all_n = 0, all_rows = 0;
+#pragma unroll
+  for (int w = 0; w < CW; ++w) {
+    if (w == warp) {
+      n = all_n;
+      rows = all_rows;
+    }
+    all_n += sh->warp_n[w];
+    all_rows += sh->warp_rows[w];
+  }
+  if (cnt > 0) {
+    const int at = n + __popc(live & ((1u << lane) - 1u));
+    sh->act[at] = (int16_t)tid;
+    sh->row0[at] = (int16_t)(rows + pre - cnt);
+  }
+  if (tid == 0) {
+    sh->nact = all_n;
+    sh->row0[all_n] = (int16_t)all_rows;
+  }
+  consumer_sync();
+  if (tid == 0) mbar_arrive(&sh->plan);
+  if (blockIdx.x == 0) {
     for (int i = tid; i < slots; i += CT) {
       p.ids[i] = sh->sel_id[i];
       p.wts[i] = sh->sel_w[i];
     }
-  int lost = 0;
-  for (int e = tid; e < p.E; e += CT) {
-    uint32_t m = sh->mask[e];
-    const int raw = __popc(m);
-    // in-order dropping: the first `cap` tokens stay
-    if (p.cap >= 0)
-      while (__popc(m) > p.cap) m &= ~(0x80000000u >> __clz(m));
-    sh->mask[e] = m;
-    lost += raw - __popc(m);
-    if (blockIdx.x == 0) {
+    if (tid < p.E) {
       double s = 0.0;
-      for (int w = 0; w < CW; ++w) s += scratch[w * kMaxExperts + e];
-      p.prob_sum[e] = (float)s;
-      p.raw_counts[e] = raw;
-      p.kept_counts[e] = __popc(m);
+      for (int t = 0; t < p.T; ++t) s += prob[(size_t)t * p.E + tid];
+      p.prob_sum[tid] = (float)s;
+      p.raw_counts[tid] = raw;
+      p.kept_counts[tid] = cnt;
+      if (raw > cnt) atomicAdd(p.dropped, raw - cnt);
     }
   }
-  if (blockIdx.x == 0 && lost) atomicAdd(p.dropped, lost);
-  consumer_sync();
-  if (warp == 0) {
-    int n = 0, rows = 0;
-    for (int base = 0; base < p.E; base += 32) {
-      const int e = base + lane;
-      const int cnt = e < p.E ? __popc(sh->mask[e]) : 0;
-      const unsigned live = __ballot_sync(0xffffffffu, cnt > 0);
-      int pre = cnt;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, pre, o);
-        if (lane >= o) pre += v;
-      }
-      if (cnt > 0) {
-        const int at = n + __popc(live & ((1u << lane) - 1u));
-        sh->act[at] = (int16_t)e;
-        sh->row0[at] = (int16_t)(rows + pre - cnt);
-      }
-      n += __popc(live);
-      rows += __shfl_sync(0xffffffffu, pre, 31);
-    }
-    if (lane == 0) {
-      sh->nact = n;
-      sh->row0[n] = (int16_t)rows;
-    }
-  }
-  consumer_sync();
-  if (tid == 0) mbar_arrive(&sh->plan);
-  // row of every slot (only the combine needs it)
-  for (int i = tid; i < slots; i += CT) {
+}
+
+// Row of every slot, for the combine
+__device__ __forceinline__ void slot_rows(const FewParams &p, Shared *sh) {
+  for (int i = threadIdx.x; i < p.T * p.k; i += CT) {
     const int e = sh->sel_id[i], t = i / p.k;
     int row = -1;
     if (e >= 0 && (sh->mask[e] >> t & 1u)) {
@@ -1084,7 +1100,6 @@ __device__ __forceinline__ void make_plan(const FewParams &p, Shared *sh) {
     }
     sh->slot_row[i] = (int16_t)row;
   }
-  consumer_sync();
 }
 
 // ---------------------------------------------------------------- 8-bit codes
@@ -1181,7 +1196,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
   Ring r;
   r.tiles = smem_raw;
   r.sc = smem_raw + (size_t)p.stages * p.stage_bytes;
-  r.sh = reinterpret_cast<Shared *>(r.sc + (size_t)p.sc_slots * p.sc_slot);
+  r.scratch = r.sc + (size_t)p.sc_slots * p.sc_slot;
+  r.sh = reinterpret_cast<Shared *>(r.scratch + scratch_bytes(p.T, p.E));
   r.st = r.ph = r.sc_st = r.sc_ph = r.issued = r.sc_issued = 0;
   r.ok = true;
   Shared *sh = r.sh;
@@ -1206,12 +1222,12 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
 
   if (warp == CW) {
     if (p.Fs) produce_part<BF16>(p, r, S1, 0);
+    if (p.Fs && r.ok) produce_part<BF16>(p, r, S2, 0);
     if (r.ok)
       r.ok = wait_bounded(&sh->plan, 0u, abort_flag, p.status, kDevTimeoutProducer, p.timeout_ns);
     r.ok = __all_sync(0xffffffffu, r.ok);
     const int nact = r.ok ? sh->nact : 0;
     if (r.ok) produce_part<FMT>(p, r, R1, nact);
-    if (r.ok && p.Fs) produce_part<BF16>(p, r, S2, nact);
     if (r.ok) produce_part<FMT>(p, r, R2, nact);
     if ((threadIdx.x & 31) == 0 && !r.ok) {
       // copies already issued land before the block goes away
@@ -1230,21 +1246,22 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.dropped = 0;
     route_partials<TP>(p);
-    grid_arrive(p.bar);
     if (p.Fs) run_part<BF16, S1, NB>(p, r, red_it);
+    grid_arrive(p.bar);
     grid_wait(p.bar, abort_flag, p);
-    make_plan(p, sh);
+    make_plan(p, sh, reinterpret_cast<double *>(r.scratch));
+    if (p.Fs) run_part<BF16, S2, NB>(p, r, red_it);
     run_part<FMT, R1, NB>(p, r, red_it);
     grid_arrive(p.bar + 8);
     grid_wait(p.bar + 8, abort_flag, p);
     if (FMT == I8) {
       quantize_h(p, sh);
       grid_arrive(p.bar + 16);
+      grid_wait(p.bar + 16, abort_flag, p);
     }
-    if (p.Fs) run_part<BF16, S2, NB>(p, r, red_it);
-    if (FMT == I8) grid_wait(p.bar + 16, abort_flag, p);
     run_part<FMT, R2, NB>(p, r, red_it);
     grid_arrive(p.bar + 24);
+    slot_rows(p, sh);
     grid_wait(p.bar + 24, abort_flag, p);
     combine(p, sh);
   }
@@ -1253,7 +1270,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
 
 template <int FMT, int TP>
 cudaError_t run(FewParams &p, cudaStream_t s) {
-  const size_t fixed = sizeof(Shared) + (size_t)p.sc_slots * p.sc_slot;
+  const size_t fixed = sizeof(Shared) + scratch_bytes(p.T, p.E) + (size_t)p.sc_slots * p.sc_slot;
   int stages = (int)((SMEM_LIMIT - fixed) / p.stage_bytes);
   stages = stages < MAX_STAGES ? stages : MAX_STAGES;
   p.solo = p.sc_slots && p.sc_slots < CW ? p.sc_slots : CW;
@@ -1288,10 +1305,13 @@ cudaError_t run_t(FewParams &p, cudaStream_t s) {
 
 int route_slices(const moe_config &c) {
   // a warp per (expert, slice) on all SMs, slices of at least 256 elements
+  // and at most what a warp loads at once
   const int want = (148 * CW) / c.num_experts;
   const int most = (c.hidden + 255) / 256;
+  const int step = 256 * route_steps(pad_tokens(c.num_tokens));
+  const int least = (c.hidden + step - 1) / step;
   const int n = want < most ? want : most;
-  return n < 1 ? 1 : n;
+  return n < least ? least : n;
 }
 
 struct FewLayout {
@@ -1353,7 +1373,7 @@ int scale_slots(const moe_config &c) {
 bool few_supported(const moe_config &c) {
   if (c.num_tokens > kFewTokens || c.act_dtype != MOE_BF16) return false;
   // at least three stages beside the scales
-  return sizeof(Shared) + (size_t)scale_slots(c) * scale_slot(c) + 3 * (size_t)(ROWS * (MAX_CH + 64)) <= (size_t)SMEM_LIMIT;
+  return sizeof(Shared) + scratch_bytes(c.num_tokens, c.num_experts) + (size_t)scale_slots(c) * scale_slot(c) + 3 * (size_t)(ROWS * (MAX_CH + 64)) <= (size_t)SMEM_LIMIT;
 }
 
 size_t few_bytes(const moe_config &c) { return few_supported(c) ? few_layout(c).total : 0; }
@@ -1398,7 +1418,7 @@ cudaError_t launch_few(const FewArgs &a, cudaStream_t s) {
   char *ws = static_cast<char *>(a.ws);
   p.part = reinterpret_cast<double *>(ws + L.part);
   p.ks = route_slices(c);
-  p.kslice = ((c.hidden + p.ks - 1) / p.ks + 7) / 8 * 8;
+  p.kslice = ((c.hidden + p.ks - 1) / p.ks + 7) / 8 * 8;   // at most 256 * route_steps: d and the step are multiples of 8
   p.xq = reinterpret_cast<int8_t *>(ws + L.xq);
   p.xs = reinterpret_cast<float *>(ws + L.xs);
   p.h = reinterpret_cast<uint16_t *>(ws + L.h);
