@@ -95,8 +95,7 @@ struct FewParams {
   // workspace
   int *status;
   unsigned *bar;                            // grid barrier counters, zeroed before the launch
-  double *part;                             // [ks][T][E] partial logits
-  int ks, kslice;
+  double *logits;                           // [T][E]
   int8_t *xq;                               // 8-bit: [T][d] codes and scales of x
   float *xs;
   uint16_t *h;                              // [T*k][F], the low parts h_lo elements further
@@ -172,15 +171,16 @@ __device__ __forceinline__ void grid_wait(unsigned *ctr, volatile int *abort_fla
 // ---------------------------------------------------------------- tasks
 // One task: 16 weight rows.  The order of a block's tasks is the same for the
 // producer and the consumers: shared phase 1, shared phase 2, routed phase 1,
-// routed phase 2, each strided over the blocks, the stride running on from
-// one part to the next.  The shared expert needs no choice, so its weights
+// routed phase 2.  Of each part a block takes a run of consecutive tasks, so
+// most of them are one expert's and its tokens' rows stay in L1 (with tasks
+// strided over the blocks every operand came from L2, and short rows waited for
+// it); the blocks with one task more are others from part to part.  The shared expert needs no choice, so its weights
 // stream while the router, the first barrier and the plan take their time.
 enum Part { S1 = 0, S2 = 1, R1 = 2, R2 = 3 };
 
 struct Dims {
   int nb;        // row blocks per expert
-  int count;     // tasks of the part
-  int first;     // this block's first
+  int first, n;  // this block's tasks: first .. first + n - 1
 };
 
 __device__ __forceinline__ Dims part_dims(const FewParams &p, int part, int nact) {
@@ -188,15 +188,17 @@ __device__ __forceinline__ Dims part_dims(const FewParams &p, int part, int nact
   const int nb1 = p.swiglu ? p.F / 8 : (p.F + ROWS - 1) / ROWS, nb2 = (p.d + ROWS - 1) / ROWS;
   const int counts[4] = {nbs1, nbs2, nact * nb1, nact * nb2};
   const int nbs[4] = {nbs1, nbs2, nb1, nb2};
-  long long before = 0;
+  const int G = (int)gridDim.x;
+  int skip = 0;                              // blocks that already hold one task more
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (i < part) before += counts[i];
+    if (i < part) skip += counts[i] % G;
+  const int b = ((int)blockIdx.x - skip % G + G) % G;
+  const int q = counts[part] / G, rest = counts[part] % G;
   Dims r;
   r.nb = nbs[part];
-  r.count = counts[part];
-  const int skip = (int)(before % gridDim.x);
-  r.first = ((int)blockIdx.x - skip + (int)gridDim.x) % (int)gridDim.x;
+  r.n = q + (b < rest ? 1 : 0);
+  r.first = b * q + min(b, rest);
   return r;
 }
 
@@ -282,7 +284,7 @@ __device__ __forceinline__ void produce_part(const FewParams &p, Ring &r, int pa
   volatile int *abort_flag = &r.sh->abort_flag;
   const int K = part == S1 || part == R1 ? p.d : (part == S2 ? p.Fs : p.F);
   const int rb = row_bytes<FMT>(K);
-  for (int task = dm.first; task < dm.count && r.ok; task += gridDim.x) {
+  for (int task = dm.first; task < dm.first + dm.n && r.ok; ++task) {
     const int i = task / dm.nb, b = task - i * dm.nb;
     const Src s = task_src<FMT>(p, part, part == R1 || part == R2 ? r.sh->act[i] : 0, b);
     const bool mine = lane < 8 ? lane < s.n0 : (lane < ROWS && lane - 8 < s.n1);
@@ -352,6 +354,14 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) {
   return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
 }
+// 16 bytes of a token's row, kept in L1.  The rows that this kernel writes
+// (codes of x, h) are read after a grid barrier, whose acquire keeps older
+// copies out of L1.
+__device__ __forceinline__ uint4 ld_l1(const char *p) {
+  uint4 v;
+  asm volatile("ld.global.ca.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
 // n arrivals at once
 __device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
@@ -395,8 +405,7 @@ __device__ __forceinline__ void load_b(BSeg<FMT, LO> &bv, const char *row, size_
     const bool ok = !CHECK || at + c * (FMT == Q4 ? 8 : 16) < left;
 #pragma unroll
     for (int l = 0; l < (LO ? 2 : 1); ++l)
-      bv.v[q][l] = ok ? __ldcg(reinterpret_cast<const uint4 *>(row + at * R + (l ? lo_bytes : 0)))
-                      : make_uint4(0u, 0u, 0u, 0u);
+      bv.v[q][l] = ok ? ld_l1(row + at * R + (l ? lo_bytes : 0)) : make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
@@ -596,9 +605,9 @@ __device__ __noinline__ void consume_part(const FewParams &p, Ring &r, uint32_t 
   const int lane_b = (w0 + c * (FMT == Q4 ? 8 : 16)) * R;
   const uint32_t row_lo = g * (p.ch + pad_of(FMT)) + w0 + c * (FMT == Q4 ? 8 : 16);
   const uint32_t row_hi = row_lo + 8 * (p.ch + pad_of(FMT));
-  if (dm.first >= dm.count) return;
-  const int mine = (dm.count - dm.first + (int)gridDim.x - 1) / (int)gridDim.x;   // tasks of this block
-  const int stride = SOLO ? p.solo * (int)gridDim.x : (int)gridDim.x;
+  const int mine = dm.n, end = dm.first + dm.n;       // tasks of this block
+  if (mine == 0) return;
+  const int stride = SOLO ? p.solo : 1;
   uint32_t st = r.st, ph = r.ph, sc_st = r.sc_st, sc_ph = r.sc_ph;
   const int skip = SOLO ? min(warp, mine) : 0;
   for (int i = 0; i < skip; ++i) {
@@ -607,8 +616,8 @@ __device__ __noinline__ void consume_part(const FewParams &p, Ring &r, uint32_t 
   }
 
   Cursor cu;
-  cu.task = dm.first + (SOLO ? warp : 0) * (int)gridDim.x;
-  if (cu.task < dm.count && (!SOLO || warp < p.solo)) {
+  cu.task = dm.first + (SOLO ? warp : 0);
+  if (cu.task < end && (!SOLO || warp < p.solo)) {
     place<PART>(p, sh, dm, cu);
     const char *bp[NB];                     // the piece's stretch of the token rows, at this lane
     BSeg<FMT, LO> bv[SEGS][NBP];
@@ -628,7 +637,7 @@ __device__ __noinline__ void consume_part(const FewParams &p, Ring &r, uint32_t 
         for (int j = 0; j < 4; ++j) acc.f[n][0][j] = acc.f[n][1][j] = 0;
       Cursor nx = cu;
       nx.task += stride;
-      const bool more = nx.task < dm.count;
+      const bool more = nx.task < end;
       const bool second = cu.rows > 8;
       const uint16_t *sc = nullptr;
       if (FMT == Q4) {
@@ -806,67 +815,74 @@ __device__ __forceinline__ double warp_max(double v) {
   for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
-// Warp arg-max of (v, i), ties to the lower index (i >= 0): three warp
-// reductions on the order-preserving 64-bit image of v.
-__device__ __forceinline__ void warp_argmax(double &v, int &i) {
+// The order-preserving 64-bit image of a float64 (-0 as +0, NaN below all),
+// and back.  Comparing images costs integer instructions; a float64
+// comparison is several times slower here.
+__device__ __forceinline__ unsigned long long key_of(double v) {
+  const unsigned long long u = (unsigned long long)__double_as_longlong(v + 0.0);
+  return v == v ? ((u >> 63) ? ~u : (u | 0x8000000000000000ull)) : 0ull;
+}
+__device__ __forceinline__ double of_key(unsigned long long k) {
+  return __longlong_as_double((long long)((k >> 63) ? (k & 0x7FFFFFFFFFFFFFFFull) : ~k));
+}
+// Warp arg-max of (key, i), ties to the lower i; returns i
+__device__ __forceinline__ int warp_argmax(unsigned long long key, int i) {
   const unsigned full = 0xffffffffu;
-  const unsigned long long u = (unsigned long long)__double_as_longlong(v + 0.0);   // -0 as +0
-  const unsigned long long key = (u >> 63) ? ~u : (u | 0x8000000000000000ull);
   const uint32_t hi = (uint32_t)(key >> 32), lo = (uint32_t)key;
-  const uint32_t mhi = __reduce_max_sync(full, hi);
-  const uint32_t mlo = __reduce_max_sync(full, hi == mhi ? lo : 0u);
-  i = (int)__reduce_min_sync(full, hi == mhi && lo == mlo ? (uint32_t)i : 0xFFFFFFFFu);
-  const unsigned long long mk = ((unsigned long long)mhi << 32) | mlo;
-  v = __longlong_as_double((long long)((mk >> 63) ? (mk & 0x7FFFFFFFFFFFFFFFull) : ~mk));
+  const bool top = hi == __reduce_max_sync(full, hi);
+  const unsigned who = __ballot_sync(full, top);
+  if (__popc(who) == 1) return __shfl_sync(full, i, __ffs(who) - 1);
+  const uint32_t mlo = __reduce_max_sync(full, top ? lo : 0u);
+  return (int)__reduce_min_sync(full, top && lo == mlo ? (uint32_t)i : 0xFFFFFFFFu);
 }
 
-// steps of 256 elements in a router slice, for tokens padded to TP
-__host__ __device__ constexpr int route_steps(int TP) { return TP <= 4 ? 8 : (TP <= 8 ? 4 : 2); }
-__host__ __device__ constexpr int pad_tokens(int T) { return T <= 1 ? 1 : (T <= 4 ? 4 : (T <= 8 ? 8 : 16)); }
-
-// Partial logits: unit (expert, slice of the hidden dimension) per warp.
+// Logits: `per` warps of a block share an expert, each a slice of the hidden
+// dimension; their sums meet in shared memory, in slice order.
 template <int TP>
-__device__ __forceinline__ void route_partials(const FewParams &p) {
+__device__ __forceinline__ void route_logits(const FewParams &p, Shared *sh) {
+  constexpr int IT = TP <= 4 ? 8 : (TP <= 8 ? 4 : 2);   // steps of 256 elements whose weights are in flight at once
+  double(*sums)[MAX_T] = reinterpret_cast<double(*)[MAX_T]>(sh->red);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int units = p.E * p.ks;
-  // consecutive units go to different blocks
-  for (int u = blockIdx.x + gridDim.x * warp; u < units; u += gridDim.x * CW) {
-    const int e = u % p.E, sl = u / p.E;
-    const int k0 = sl * p.kslice, k1 = min(p.d, k0 + p.kslice);
+  const int per = p.E <= (int)gridDim.x ? CW : CW / 2, at_once = CW / per;
+  const int slice = ((p.d + per - 1) / per + 7) / 8 * 8;
+  for (int e0 = blockIdx.x * at_once; e0 < p.E; e0 += gridDim.x * at_once) {
+    const int e = e0 + warp / per;
     double acc[TP];
 #pragma unroll
     for (int t = 0; t < TP; ++t) acc[t] = 0.0;
-    const float *w = p.w_router + (size_t)e * p.d;
-    // the slice's weights are all in flight before the first is used
-    constexpr int IT = route_steps(TP);
-    float4 wv[IT][2];
+    const int k1 = e < p.E ? min(p.d, (warp % per + 1) * slice) : 0;
+    const float *w = p.w_router + (size_t)min(e, p.E - 1) * p.d;
+#pragma unroll 1
+    for (int k0 = (warp % per) * slice; k0 < k1; k0 += 256 * IT) {
+      float4 wv[IT][2];
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int k = k0 + (lane + 32 * i) * 8;
-      wv[i][0] = wv[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (k < k1) {
-        wv[i][0] = __ldg(reinterpret_cast<const float4 *>(w + k));
-        wv[i][1] = __ldg(reinterpret_cast<const float4 *>(w + k + 4));
+      for (int i = 0; i < IT; ++i) {
+        const int k = k0 + (lane + 32 * i) * 8;
+        wv[i][0] = wv[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < k1) {
+          wv[i][0] = __ldg(reinterpret_cast<const float4 *>(w + k));
+          wv[i][1] = __ldg(reinterpret_cast<const float4 *>(w + k + 4));
+        }
       }
-    }
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int k = k0 + (lane + 32 * i) * 8;
-      if (k < k1) {
-        const float4 wa = wv[i][0], wb = wv[i][1];
+      for (int i = 0; i < IT; ++i) {
+        const int k = k0 + (lane + 32 * i) * 8;
+        if (k < k1) {
+          const float4 wa = wv[i][0], wb = wv[i][1];
 #pragma unroll
-        for (int t = 0; t < TP; ++t) {
-          if (t < p.T) {
-            const uint4 xv = __ldg(reinterpret_cast<const uint4 *>(p.x + (size_t)t * p.d + k));
-            float run = __uint_as_float(xv.x << 16) * wa.x;
-            run = fmaf(__uint_as_float(xv.x & 0xffff0000u), wa.y, run);
-            run = fmaf(__uint_as_float(xv.y << 16), wa.z, run);
-            run = fmaf(__uint_as_float(xv.y & 0xffff0000u), wa.w, run);
-            run = fmaf(__uint_as_float(xv.z << 16), wb.x, run);
-            run = fmaf(__uint_as_float(xv.z & 0xffff0000u), wb.y, run);
-            run = fmaf(__uint_as_float(xv.w << 16), wb.z, run);
-            run = fmaf(__uint_as_float(xv.w & 0xffff0000u), wb.w, run);
-            acc[t] += (double)run;
+          for (int t = 0; t < TP; ++t) {
+            if (t < p.T) {
+              const uint4 xv = __ldg(reinterpret_cast<const uint4 *>(p.x + (size_t)t * p.d + k));
+              float run = __uint_as_float(xv.x << 16) * wa.x;
+              run = fmaf(__uint_as_float(xv.x & 0xffff0000u), wa.y, run);
+              run = fmaf(__uint_as_float(xv.y << 16), wa.z, run);
+              run = fmaf(__uint_as_float(xv.y & 0xffff0000u), wa.w, run);
+              run = fmaf(__uint_as_float(xv.z << 16), wb.x, run);
+              run = fmaf(__uint_as_float(xv.z & 0xffff0000u), wb.y, run);
+              run = fmaf(__uint_as_float(xv.w << 16), wb.z, run);
+              run = fmaf(__uint_as_float(xv.w & 0xffff0000u), wb.w, run);
+              acc[t] += (double)run;
+            }
           }
         }
       }
@@ -890,8 +906,15 @@ __device__ __forceinline__ void route_partials(const FewParams &p) {
     }
     // the lane's token: its bits from 16 down chose the halves
     constexpr int LOG = TP == 16 ? 4 : (TP == 8 ? 3 : (TP == 4 ? 2 : 0));
-    const int t = lane >> (5 - LOG);
-    if ((lane & ((32 >> LOG) - 1)) == 0 && t < p.T) p.part[((size_t)sl * p.T + t) * p.E + e] = acc[0];
+    if ((lane & ((32 >> LOG) - 1)) == 0) sums[warp][lane >> (5 - LOG)] = acc[0];
+    consumer_sync();
+    for (int i = threadIdx.x; i < at_once * p.T; i += CT) {
+      const int t = i / at_once, q = i - t * at_once;
+      double s = 0.0;
+      for (int j = 0; j < per; ++j) s += sums[q * per + j][t];
+      if (e0 + q < p.E) p.logits[(size_t)t * p.E + e0 + q] = s;
+    }
+    consumer_sync();
   }
 }
 
@@ -899,22 +922,21 @@ constexpr int EPL = kMaxExperts / 32;
 
 // One token's choice from its row of `prob` (softmax: shifted logits, made
 // probabilities here; sigmoid: probabilities); ids and weights to shared
-// memory.  A warp; expert lane + 32 j.
-__device__ __forceinline__ void choose(const FewParams &p, Shared *sh, int t, double *prob, int lane) {
+// memory.  A warp; expert lane + 32 j.  keys: this warp's scratch.
+__device__ __forceinline__ void choose(const FewParams &p, Shared *sh, int t, double *prob, unsigned long long *keys,
+                                       int lane) {
   const int E = p.E;
-  double score[EPL];
+  constexpr unsigned long long LOWEST = 0x000FFFFFFFFFFFFFull;   // key of -infinity
+  unsigned long long key[EPL];
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) score[j] = lane + 32 * j < E ? prob[lane + 32 * j] : -INFINITY;
-  bool number = false;
+  for (int j = 0; j < EPL; ++j) key[j] = lane + 32 * j < E ? key_of(prob[lane + 32 * j]) : 0ull;
+  unsigned long long best = 0;
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) number |= lane + 32 * j < E && score[j] == score[j];
+  for (int j = 0; j < EPL; ++j) best = max(best, key[j]);
   // a token without a single number among its scores chooses nothing
-  const bool none = !__any_sync(0xffffffffu, number);
+  const bool none = !__any_sync(0xffffffffu, best != 0ull);
   if (p.router == MOE_ROUTER_SOFTMAX_TOPK) {
-    double m = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) m = fmax(m, score[j]);
-    m = warp_max(m);
+    const double m = warp_max(best ? of_key(best) : -INFINITY);
     double s = 0.0;
 #pragma unroll 1
     for (int e = lane; e < E; e += 32) {
@@ -922,65 +944,71 @@ __device__ __forceinline__ void choose(const FewParams &p, Shared *sh, int t, do
       prob[e] = v;
       s += v;
     }
-    s = warp_sum(s);
-#pragma unroll 1
-    for (int e = lane; e < E; e += 32) prob[e] = prob[e] / s;
-    __syncwarp();
+    const double inv = 1.0 / warp_sum(s);
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) score[j] = lane + 32 * j < E ? prob[lane + 32 * j] : -INFINITY;
-  } else {
-    // group score = sum of the two largest selection scores in the group
-    const int G = E / p.n_group;
-    double gs = -INFINITY;
-    if (lane < p.n_group) {
-      double b1 = -INFINITY, b2 = -INFINITY;
-#pragma unroll 4
-      for (int q = 0; q < G; ++q) {
-        const double v = prob[lane * G + q] + (p.bias ? (double)__ldg(p.bias + lane * G + q) : 0.0);
-        if (v > b1) { b2 = b1; b1 = v; } else if (v > b2) { b2 = v; }
+    for (int j = 0; j < EPL; ++j)
+      if (lane + 32 * j < E) {
+        const double v = prob[lane + 32 * j] * inv;
+        prob[lane + 32 * j] = v;
+        key[j] = key_of(v);
       }
-      gs = b1 + b2;
+    __syncwarp();
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      const int e = lane + 32 * j;
+      if (e < E) {
+        if (p.bias) key[j] = key_of(prob[e] + (double)__ldg(p.bias + e));
+        keys[e] = key[j];
+      }
     }
     __syncwarp();
+    // group score = sum of the two largest selection scores in the group
+    const int G = E / p.n_group;
+    unsigned long long gkey = 0;
+    if (lane < p.n_group) {
+      unsigned long long b1 = 0, b2 = 0;
+#pragma unroll 4
+      for (int q = 0; q < G; ++q) {
+        const unsigned long long v = keys[lane * G + q];
+        b2 = max(b2, min(b1, v));
+        b1 = max(b1, v);
+      }
+      gkey = key_of((b1 ? of_key(b1) : -INFINITY) + (b2 ? of_key(b2) : -INFINITY));
+    }
     uint32_t keep = 0;
 #pragma unroll 1
     for (int r = 0; r < p.topk_group; ++r) {
       const bool open = lane < p.n_group && !((keep >> lane) & 1u);
-      double v = open ? gs : -INFINITY;
-      int gi = open ? lane : 0x7fffffff;
-      warp_argmax(v, gi);
+      const int gi = warp_argmax(open ? gkey : 0ull, open ? lane : 0x7fffffff);
       keep |= 1u << (gi & 31);
     }
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
       const int e = lane + 32 * j;
-      if (e < E) {
-        if (p.bias) score[j] += (double)__ldg(p.bias + e);
-        if (!((keep >> (e / G)) & 1u)) score[j] = -INFINITY;
-      }
+      if (e < E && !((keep >> (e / G)) & 1u)) key[j] = min(key[j], LOWEST);
     }
   }
 
-  uint32_t taken = 0;
-  int my_e = -1;
+  int my_e = 0x7fffffff;
 #pragma unroll 1
   for (int r = 0; r < p.k; ++r) {
-    double bv = -INFINITY;
+    unsigned long long bk = 0;
     int bi = 0x7fffffff;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      const int e = lane + 32 * j;
-      if (e < E && !((taken >> j) & 1u) && (score[j] > bv || (score[j] == bv && e < bi))) {
-        bv = score[j];
-        bi = e;
+    for (int j = EPL - 1; j >= 0; --j)                 // ties: the lower expert
+      if (key[j] >= bk && key[j] != 0ull) {
+        bk = key[j];
+        bi = lane + 32 * j;
       }
-    }
-    warp_argmax(bv, bi);
-    if ((bi & 31) == lane && bi < E) taken |= 1u << (bi >> 5);
+    bi = warp_argmax(bk, bi);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (bi == lane + 32 * j) key[j] = 0ull;          // taken
     if (lane == r) my_e = bi;
   }
   const bool bad = none || my_e < 0 || my_e >= E;
-  const double my_w = lane < p.k && my_e >= 0 && my_e < E ? prob[my_e] : 0.0;
+  const double my_w = lane < p.k && !bad ? prob[my_e] : 0.0;
   const double tot = warp_sum(my_w);
   double wout;
   if (p.router == MOE_ROUTER_SOFTMAX_TOPK) wout = p.norm ? my_w / fmax(tot, 1e-12) : my_w;
@@ -997,20 +1025,24 @@ __device__ __forceinline__ void choose(const FewParams &p, Shared *sh, int t, do
 // launch, and fetching its instructions is much of its time.
 __device__ __noinline__ void make_plan(const FewParams &p, Shared *sh, double *prob) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  static_assert(sizeof(((Shared *)0)->red) >= CW * kMaxExperts * 8, "selection scratch");
+  unsigned long long *keys = reinterpret_cast<unsigned long long *>(sh->red) + warp * kMaxExperts;
   sh->mask[tid] = 0u;
   static_assert(CT == kMaxExperts, "a thread per expert");
   // logits (softmax: with the bias) or sigmoid scores, a thread per (token, expert)
+  const int n_logits = p.T * p.E;
+#pragma unroll 1
+  for (int i0 = tid; i0 < n_logits; i0 += 8 * CT) {    // eight loads in flight at a time
+    double v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = i0 + u * CT < n_logits ? __ldcg(p.logits + i0 + u * CT) : 0.0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (i0 + u * CT < n_logits) prob[i0 + u * CT] = v[u];
+  }
 #pragma unroll 1
   for (int i = tid; i < p.T * p.E; i += CT) {
-    double l = 0.0;
-#pragma unroll 1
-    for (int s0 = 0; s0 < p.ks; s0 += 8) {             // eight slices' loads in flight at a time
-      double v[8];
-#pragma unroll
-      for (int s = 0; s < 8; ++s) v[s] = s0 + s < p.ks ? __ldcg(p.part + (size_t)(s0 + s) * p.T * p.E + i) : 0.0;
-#pragma unroll
-      for (int s = 0; s < 8; ++s) l += v[s];
-    }
+    double l = prob[i];
     if (p.router == MOE_ROUTER_SOFTMAX_TOPK) {
       if (p.bias) l += (double)__ldg(p.bias + i % p.E);
     } else {
@@ -1020,7 +1052,7 @@ __device__ __noinline__ void make_plan(const FewParams &p, Shared *sh, double *p
   }
   consumer_sync();
 #pragma unroll 1
-  for (int t = warp; t < p.T; t += CW) choose(p, sh, t, prob + (size_t)t * p.E, lane);
+  for (int t = warp; t < p.T; t += CW) choose(p, sh, t, prob + (size_t)t * p.E, keys, lane);
   consumer_sync();
   const int slots = p.T * p.k;
 #pragma unroll 1
@@ -1149,6 +1181,7 @@ __device__ __forceinline__ void quantize_x(const FewParams &p, Shared *sh) {
       reinterpret_cast<uint2 *>(p.xq + (size_t)t * p.d)[i] = codes8(__ldg(row + i), m);
     if (threadIdx.x == 0)
       p.xs[t] = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __fdiv_rn(__uint_as_float(m), 127.f);
+    consumer_sync();                        // the scratch has been read
   }
 }
 
@@ -1245,7 +1278,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         for (int i = threadIdx.x; i < p.T * p.k; i += CT) p.rowmax[i] = 0u;
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.dropped = 0;
-    route_partials<TP>(p);
+    route_logits<TP>(p, sh);
     if (p.Fs) run_part<BF16, S1, NB>(p, r, red_it);
     grid_arrive(p.bar);
     grid_wait(p.bar, abort_flag, p);
@@ -1303,19 +1336,8 @@ cudaError_t run_t(FewParams &p, cudaStream_t s) {
   return run<FMT, 16>(p, s);
 }
 
-int route_slices(const moe_config &c) {
-  // a warp per (expert, slice) on all SMs, slices of at least 256 elements
-  // and at most what a warp loads at once
-  const int want = (148 * CW) / c.num_experts;
-  const int most = (c.hidden + 255) / 256;
-  const int step = 256 * route_steps(pad_tokens(c.num_tokens));
-  const int least = (c.hidden + step - 1) / step;
-  const int n = want < most ? want : most;
-  return n < least ? least : n;
-}
-
 struct FewLayout {
-  size_t part, xq, xs, h, h_lo, hs, hs_lo, rowmax, hq, y, total;
+  size_t logits, xq, xs, h, h_lo, hs, hs_lo, rowmax, hq, y, total;
 };
 
 FewLayout few_layout(const moe_config &c) {
@@ -1329,7 +1351,7 @@ FewLayout few_layout(const moe_config &c) {
   const size_t T = c.num_tokens, S = T * c.top_k, d = c.hidden, F = c.intermediate;
   const size_t Fs = c.shared_intermediate > 0 ? c.shared_intermediate : 0;
   const bool i8 = c.weight_dtype == MOE_I8_CHANNEL;
-  L.part = take(sizeof(double) * route_slices(c) * T * c.num_experts);
+  L.logits = take(sizeof(double) * T * c.num_experts);
   L.xq = take(i8 ? T * d : 0);
   L.xs = take(i8 ? sizeof(float) * T : 0);
   L.h = take(2 * S * F);
@@ -1416,9 +1438,7 @@ cudaError_t launch_few(const FewArgs &a, cudaStream_t s) {
   p.status = a.status;
   p.bar = reinterpret_cast<unsigned *>(a.status) + 16;
   char *ws = static_cast<char *>(a.ws);
-  p.part = reinterpret_cast<double *>(ws + L.part);
-  p.ks = route_slices(c);
-  p.kslice = ((c.hidden + p.ks - 1) / p.ks + 7) / 8 * 8;   // at most 256 * route_steps: d and the step are multiples of 8
+  p.logits = reinterpret_cast<double *>(ws + L.logits);
   p.xq = reinterpret_cast<int8_t *>(ws + L.xq);
   p.xs = reinterpret_cast<float *>(ws + L.xs);
   p.h = reinterpret_cast<uint16_t *>(ws + L.h);
