@@ -4,74 +4,82 @@
 // nearly all of its time is reading the chosen experts' weights once.  The
 // staged layer spends 9-10 launches on it and gives each weight tile a
 // 128-row operand; here one persistent block per SM streams weight rows
-// through shared memory without a pause, from the first product to the last.
+// through shared memory from the first product to the last.
 //
-//   router    each warp dots one expert's slice of the hidden dimension with
-//             every token (fp32 products over runs of 8, float64 sums); the
-//             shared expert's first product runs before anyone waits for it;
+//   router    the warps of a block share an expert, each a slice of the hidden
+//             dimension, times every token (fp32 products over runs of 8,
+//             float64 sums);
 //   choice    after a grid barrier every block selects for all tokens from
-//             the same partial sums (float64, ties to the lower expert) and
-//             builds the same plan: per expert a 16-bit mask of its tokens in
-//             token order, cut to the capacity;
+//             the same logits (float64, ties to the lower expert) and builds
+//             the same plan: per expert a 16-bit mask of its tokens in token
+//             order, cut to the capacity;
 //   phase 1   tasks of 16 weight rows: 8 gate rows and the 8 up rows of the
 //             same features (ReLU: 16 rows), times the expert's tokens;
 //   phase 2   tasks of 16 rows of the down projection, times h;
 //   combine   after a last grid barrier: out = sum_j w_j y_j (+ shared).
+// The shared expert needs no choice: its phase 1 runs beside the router, its
+// phase 2 before the routed experts'.
 //
-// A block is one producer warp and eight consumer warps.  The producer copies
-// rows, up to 2048 bytes of each of a task's 16 at a time, into a ring of stages
-// (cp.async.bulk, one mbarrier per stage) and runs ahead of the consumers
-// across tasks, phases and grid barriers: the ring is full of the next
-// phase's weights when a barrier opens, and of the shared expert's while the
-// router runs.  The row pitch in shared memory is 64 bytes more than a
-// multiple of 128 (32 for 4-bit codes), so a warp reads its matrix fragments
-// straight from the copied rows without bank conflicts.
-// The consumers split a stage's K into 64-byte segments; per segment a thread
-// takes 16 bytes of weight rows g and g + 8 and of token g's row, which is
-// one A and one B operand of mma.sync m16n8 for a permuted order of K (a sum
-// over K has no order).  mma.sync is the right unit here: 8 tokens are its N,
-// and at a row of weights per 23 bytes a clock it is idle most of the time.
-// The eight partial 16 x 8 results meet in shared memory.
+// How the weights move.  Each of a block's eight warps walks its own units, 16
+// rows x 256 bytes, and each lane fetches with cp.async the 16-byte pieces
+// that it will multiply itself, DEPTH units ahead, into slots of its own: there
+// is nobody to hand over to, so the stream has no barriers, and it runs on
+// across tasks, phases and grid barriers (the slots are full of the next
+// phase's weights when a barrier opens).  Measured on 466 MB of 16-row tasks:
+// 6.49 TB/s four units deep; one bulk copy per row piece, with a producer
+// warp, cost 55 ns each whatever its size (5.1 TB/s at 2 KB, 1.3 at 512 B).
+// A block takes a run of consecutive tasks, so most are one expert's and its
+// tokens' rows stay in L1.
+//
+// The product.  mma.sync m16n8: 16 weight rows times 8 tokens.  A thread's
+// 16 bytes of rows g and g + 8 and of token g's row are one A and one B
+// operand for a permuted order of K (a sum over K has no order), so nothing is
+// transposed or shuffled.  At 23 bytes of weights per clock and SM the legacy
+// unit (2 clocks a product) is mostly idle.
+//   long rows   the warps split a task's K; their partial 16 x 8 results meet
+//               in shared memory, one barrier per task;
+//   short rows  (solo) each warp takes whole tasks.
 //
 // Precision: bf16 weights take h as the sum of two bf16 (16 bits); with 4-bit
-// ones, whose products already keep the tensor pipe busy for most of the
-// time a group of codes takes to arrive, h is one bf16, as in the staged
+// ones, whose unpacking is what bounds them, h is one bf16, as in the staged
 // layer.  4-bit codes are multiplied as exact small integers and scaled per
 // group of 64 in fp32 (w = s q + b: s sum(q x) + b sum(x)).  Expert outputs
-// stay fp32 until the combine.  8-bit weights follow
-// the 8-bit layer's definition (rows of x and of the bf16 h quantised).
+// stay fp32 until the combine.  8-bit weights follow the 8-bit layer's
+// definition (rows of x and of the bf16 h quantised).
 //
 // Results do not depend on timing: every sum has a fixed order, and the row
 // maxima behind the 8-bit codes of h are integer maxima.
-// Bound by HBM.  All waits are bounded (moe_set_wait_timeout_ns): one that runs
-// out records a status and turns every later wait of its block into a
-// no-op, so the block runs through its (in-bounds) work, meets every barrier
-// and ends.
+// The only waits are the grid barriers, bounded by moe_set_wait_timeout_ns: one
+// that runs out records a status and turns every later wait of its block into
+// a no-op, so the block runs through its (in-bounds) work and ends.
 #include "tc_ptx.cuh"
 
 #include <math.h>
+
+#include <type_traits>
 
 namespace moe {
 namespace {
 
 using namespace ptx;
 
-constexpr int CW = 8;                       // consumer warps
+constexpr int CW = 8;                       // warps
 constexpr int CT = 32 * CW;
-constexpr int THREADS = CT + 32;
-constexpr int MAX_CH = 2048;                // most bytes of a row per stage
 constexpr int ROWS = 16;                    // weight rows per task
-constexpr int MAX_STAGES = 24;
-constexpr int MAX_SC = CW;                  // 4-bit: tasks whose scales and biases are held at once
-constexpr int SC_BYTES = 64 * 1024;         // and the shared memory they may take (two tasks at least)
+constexpr int UNIT = 256;                   // bytes of a row per unit
+constexpr int SEG = 64;                     // and per product step: 16 bytes for each lane of a quad
+constexpr int SEGS = UNIT / SEG;
+constexpr int DEPTH = 4;                    // units in flight per warp
+constexpr int SOLO_BYTES = 2048;            // rows of at most that many bytes go one task to a warp
+constexpr int MAX_KSPLIT = 4;               // parts of K a down-projection task may be cut into
 constexpr int MAX_T = kFewTokens;
 constexpr int MAX_SLOTS = MAX_T * kMaxTopK;
 constexpr int SMEM_LIMIT = 227 * 1024;
 
 enum Fmt { BF16 = 0, I8 = 1, Q4 = 2 };
 
-// row pitch in a stage beyond its ch bytes (a multiple of 128)
-__host__ __device__ constexpr int pad_of(int fmt) { return fmt == Q4 ? 32 : 64; }
+// shared memory of one unit: the lanes' pieces, and 32 bytes of scales and biases per lane
+__host__ __device__ constexpr int unit_bytes(int fmt) { return ROWS * UNIT + (fmt == Q4 ? 32 * 32 : 0); }
 
 struct FewParams {
   uint64_t timeout_ns;
@@ -104,20 +112,14 @@ struct FewParams {
   size_t hs_lo;
   unsigned *rowmax;                         // 8-bit: [T*k] largest |h| of a row, as fp32 bits
   int8_t *hq;                               // 8-bit: [T*k][F]
-  float *y;                                 // [T*k + T][d] expert outputs, then the shared expert's
-  int ch;                                   // bytes of a row per stage, a multiple of 128
-  int stage_bytes, stages;
-  int solo;                                 // warps that take tasks by themselves where rows are short
-  int sc_slot, sc_slots;                    // 4-bit: bytes of one task's scales and biases, and how many are held
+  float *y;                                 // [ksplit][T*k][d] expert outputs, then [T][d] of the shared expert
+  int y_rows;                               // T*k
+  int ksplit;                               // most parts of K that y has room for
 };
 
 __host__ __device__ constexpr size_t scratch_bytes(int T, int E) { return ((size_t)T * E * 8 + 127) / 128 * 128; }
 
 struct Shared {
-  uint64_t full[MAX_STAGES];
-  uint64_t empty[MAX_STAGES];
-  uint64_t sc_full[MAX_SC], sc_empty[MAX_SC];
-  uint64_t plan;
   int abort_flag;
   int nact;                                 // experts with rows
   uint32_t mask[kMaxExperts];               // tokens an expert keeps
@@ -126,24 +128,18 @@ struct Shared {
   int sel_id[MAX_SLOTS];
   float sel_w[MAX_SLOTS];
   int16_t slot_row[MAX_SLOTS];
+  float bias[kMaxExperts];                  // the router's, zeros without one
+  uint8_t raw[kMaxExperts];                 // tokens that chose an expert
   int warp_n[CW], warp_rows[CW];            // per 32 experts: how many have rows, and the rows
-  // partial results of the consumer warps, two tasks in turn
+  // partial results of the warps, two tasks in turn; scratch of the router and the choice
   __align__(16) uint32_t red[2][CW][2][32][4];
 };
 
-__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(CT) : "memory"); }
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
-
 // ---------------------------------------------------------------- grid barrier
 // Arrival and wait are apart, so work that does not depend on the other blocks
-// can run between them.  Both are called by all consumer threads.
+// can run between them.  Both are called by all threads.
 __device__ __forceinline__ void grid_arrive(unsigned *ctr) {
-  consumer_sync();
+  __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
     asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(ctr) : "memory");
@@ -165,61 +161,100 @@ __device__ __forceinline__ void grid_wait(unsigned *ctr, volatile int *abort_fla
     }
     __threadfence();
   }
-  consumer_sync();
+  __syncthreads();
 }
 
 // ---------------------------------------------------------------- tasks
-// One task: 16 weight rows.  The order of a block's tasks is the same for the
-// producer and the consumers: shared phase 1, shared phase 2, routed phase 1,
-// routed phase 2.  Of each part a block takes a run of consecutive tasks, so
-// most of them are one expert's and its tokens' rows stay in L1 (with tasks
-// strided over the blocks every operand came from L2, and short rows waited for
-// it); the blocks with one task more are others from part to part.  The shared expert needs no choice, so its weights
-// stream while the router, the first barrier and the plan take their time.
-enum Part { S1 = 0, S2 = 1, R1 = 2, R2 = 3 };
-
-struct Dims {
-  int nb;        // row blocks per expert
-  int first, n;  // this block's tasks: first .. first + n - 1
-};
-
-__device__ __forceinline__ Dims part_dims(const FewParams &p, int part, int nact) {
-  const int nbs1 = p.Fs / 8, nbs2 = p.Fs ? (p.d + ROWS - 1) / ROWS : 0;
-  const int nb1 = p.swiglu ? p.F / 8 : (p.F + ROWS - 1) / ROWS, nb2 = (p.d + ROWS - 1) / ROWS;
-  const int counts[4] = {nbs1, nbs2, nact * nb1, nact * nb2};
-  const int nbs[4] = {nbs1, nbs2, nb1, nb2};
-  const int G = (int)gridDim.x;
-  int skip = 0;                              // blocks that already hold one task more
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < part) skip += counts[i] % G;
-  const int b = ((int)blockIdx.x - skip % G + G) % G;
-  const int q = counts[part] / G, rest = counts[part] % G;
-  Dims r;
-  r.nb = nbs[part];
-  r.n = q + (b < rest ? 1 : 0);
-  r.first = b * q + min(b, rest);
-  return r;
-}
+// One task: 16 weight rows.  A block's tasks come in this order: shared phase
+// 1, shared phase 2, routed phase 1, routed phase 2; of each part a block
+// takes a run of consecutive ones, and the blocks with one task more are
+// others from part to part.
+enum Part { S1 = 0, S2 = 1, R1 = 2, R2 = 3, END = 4 };
 
 template <int FMT>
 __device__ __forceinline__ int row_bytes(int K) {
   return FMT == BF16 ? 2 * K : (FMT == I8 ? K : K / 2);
 }
 
-// Weight rows of a task: rows 0-7 from w0, 8-15 from w1, both `bytes` long
+struct Geo {
+  int nb;        // row blocks per expert and part of K
+  int first, n;  // this block's tasks: first .. first + n - 1
+  int rb, ns;    // bytes of a weight row, and its segments
+  int ks;        // parts of K
+  bool solo;     // one task to a warp
+};
+
+// Tasks of the routed down projection are cut along K while a block has few
+// of them: 512 tasks of 28 KB rows on 148 blocks are three or four each, and
+// the blocks with three would wait for the others for a quarter of the phase.
+__device__ __forceinline__ int k_parts(const FewParams &p, int nact, int rb) {
+  int ks = 1;
+  while (2 * ks <= p.ksplit && rb >= 2 * SOLO_BYTES * 2 * ks &&
+         (long long)nact * ((p.d + ROWS - 1) / ROWS) * ks < 10LL * (int)gridDim.x)
+    ks *= 2;
+  return ks;
+}
+
+template <int FMT>
+__device__ __forceinline__ Geo part_geo(const FewParams &p, int part, int nact) {
+  const int nbs1 = p.Fs / 8, nbs2 = p.Fs ? (p.d + ROWS - 1) / ROWS : 0;
+  const int nb1 = p.swiglu ? p.F / 8 : (p.F + ROWS - 1) / ROWS, nb2 = (p.d + ROWS - 1) / ROWS;
+  Geo r;
+  r.rb = row_bytes<FMT>(part == S1 || part == R1 ? p.d : (part == S2 ? p.Fs : p.F));
+  r.ns = (r.rb + SEG - 1) / SEG;
+  r.ks = part == R2 ? k_parts(p, nact, r.rb) : 1;
+  r.solo = r.rb <= SOLO_BYTES;
+  r.nb = part == S1 ? nbs1 : (part == S2 ? nbs2 : (part == R1 ? nb1 : nb2));
+  const int counts[4] = {nbs1, nbs2, nact * nb1, nact * nb2 * r.ks};
+  const int G = (int)gridDim.x;
+  int skip = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < part) skip += counts[i] % G;
+  const int count = part == S1 ? counts[0] : (part == S2 ? counts[1] : (part == R1 ? counts[2] : counts[3]));
+  const int b = ((int)blockIdx.x - skip % G + G) % G;
+  const int q = count / G, rest = count % G;
+  r.n = q + (b < rest ? 1 : 0);
+  r.first = b * q + min(b, rest);
+  return r;
+}
+
+// A task in full: row block b of active expert i, part kp of K
+struct Task {
+  int i, kp, b;
+};
+__device__ __forceinline__ Task task_of(const Geo &g, int task) {
+  Task t;
+  const int blocks = g.nb * g.ks;
+  t.i = task / blocks;
+  const int w = task - t.i * blocks;
+  t.kp = w / g.nb;
+  t.b = w - t.kp * g.nb;
+  return t;
+}
+
+// Segments of the row that this warp takes of a task
+struct Span {
+  int first, n;
+};
+__device__ __forceinline__ Span warp_span(const Geo &g, int kp, int warp) {
+  const int a = g.ks == 1 ? 0 : kp * g.ns / g.ks, b = g.ks == 1 ? g.ns : (kp + 1) * g.ns / g.ks;
+  if (g.solo) return {a, b - a};
+  const int c = a + warp * (b - a) / CW;
+  return {c, a + (warp + 1) * (b - a) / CW - c};
+}
+
+// Weight rows of a task: rows 0-7 from w0, 8-15 from w1
 struct Src {
   const char *w0, *w1;
   int n0, n1;                               // valid rows of each half
   size_t r0, r1;                            // row index of each half's first (channel scales)
 };
 
-template <int FMT>
-__device__ __forceinline__ Src task_src(const FewParams &p, int part, int e, int b) {
+__device__ __forceinline__ Src task_src(const FewParams &p, int part, int e, int b, int rb) {
   Src s;
   if (part == S1 || part == R1) {
     const size_t base = part == S1 ? 0 : (size_t)e * p.w_stride;
-    const size_t rb = row_bytes<FMT>(p.d);
     const char *g = static_cast<const char *>(part == S1 ? (const void *)p.sw1 : p.w1);
     const char *u = static_cast<const char *>(part == S1 ? (const void *)p.sw2 : p.w2);
     if (part == S1 || p.swiglu) {
@@ -237,7 +272,6 @@ __device__ __forceinline__ Src task_src(const FewParams &p, int part, int e, int
     }
   } else {
     const size_t base = part == S2 ? 0 : (size_t)e * p.d;
-    const size_t rb = row_bytes<FMT>(part == S2 ? p.Fs : p.F);
     const char *w = static_cast<const char *>(part == S2 ? (const void *)p.sw3 : p.w3);
     s.r0 = base + (size_t)b * ROWS;
     s.r1 = s.r0 + 8;
@@ -249,103 +283,169 @@ __device__ __forceinline__ Src task_src(const FewParams &p, int part, int e, int
   return s;
 }
 
-// ---------------------------------------------------------------- producer
-struct Ring {
-  Shared *sh;
-  uint8_t *tiles;
-  uint8_t *sc;                              // 4-bit: the slots of scales and biases
-  uint8_t *scratch;                         // [T][E] doubles: the tokens' probabilities
-  uint32_t st, ph;                          // next stage and the parity of its use
-  uint32_t sc_st, sc_ph;                    // likewise the next scale slot
-  uint32_t issued, sc_issued;               // producer: copies' stages and slots so far
-  bool ok;
-};
-__device__ __forceinline__ void advance(uint32_t &st, uint32_t &ph, uint32_t n) {
-  if (++st == n) {
-    st = 0;
-    ph ^= 1u;
-  }
+// ---------------------------------------------------------------- the weight stream
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The slow half of a barrier wait, out of line
-__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status, int code,
-                                       uint64_t limit_ns) {
-  return wait_bounded(bar, parity, abort_flag, status, code, limit_ns);
-}
-__device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, Shared *sh, const FewParams &p, int code) {
-  if (mbar_try_wait(bar, parity)) return true;
-  return wait_slow(bar, parity, &sh->abort_flag, p.status, code, p.timeout_ns);
-}
+// The fetching end of a warp's stream: the next unit to fetch, DEPTH units
+// before the one in use.  Every fetch, and every step at which there is
+// nothing to fetch yet, closes a cp.async group, so the unit in use is always
+// at least DEPTH groups old.
+struct Feed {
+  int part, limit;                          // part fetched from, and the first that is not known yet
+  Geo g;
+  int j;                                    // task, from the block's first
+  int u, nu;                                // unit of the task, and how many it has here
+  int nseg;                                 // segments of the task here
+  int tail;                                 // valid bytes of this lane's piece of the row's last segment: 16 or 0
+  bool ends;                                // the span reaches the row's end
+  const char *lo, *hi;                      // this lane's place in rows g and g + 8; null: no such row
+  const char *sc[4];                        // 4-bit: its place in s and b of row g, s and b of row g + 8
+  int groups;                               // 4-bit: groups of the row from that place on
+  uint32_t issued, used;                    // units so far
+};
 
 template <int FMT>
-__device__ __forceinline__ void produce_part(const FewParams &p, Ring &r, int part, int nact) {
-  const Dims dm = part_dims(p, part, nact);
-  const int lane = threadIdx.x & 31;
-  volatile int *abort_flag = &r.sh->abort_flag;
-  const int K = part == S1 || part == R1 ? p.d : (part == S2 ? p.Fs : p.F);
-  const int rb = row_bytes<FMT>(K);
-  for (int task = dm.first; task < dm.first + dm.n && r.ok; ++task) {
-    const int i = task / dm.nb, b = task - i * dm.nb;
-    const Src s = task_src<FMT>(p, part, part == R1 || part == R2 ? r.sh->act[i] : 0, b);
-    const bool mine = lane < 8 ? lane < s.n0 : (lane < ROWS && lane - 8 < s.n1);
-    const char *row = lane < 8 ? s.w0 + (size_t)lane * rb : s.w1 + (size_t)(lane - 8) * rb;
-    if (FMT == Q4) {
-      // scales and biases of the task's two blocks of 8 rows, each contiguous
-      int good = 1;
-      if (lane == 0)
-        good = wait_on(&r.sh->sc_empty[r.sc_st], r.sc_ph ^ 1u, r.sh, p, kDevTimeoutProducer) && !*abort_flag;
-      if (!__shfl_sync(0xffffffffu, good, 0)) {
-        r.ok = false;
-        break;
-      }
-      const int blk = K / 64 * 2 * 8;       // bytes: a multiple of 16
-      if (lane == 0) mbar_expect_tx(&r.sh->sc_full[r.sc_st], 4 * blk);
-      __syncwarp();
-      if (lane < 4) {
-        const char *base = static_cast<const char *>(
-            part == R2 ? (lane & 1 ? p.b3 : p.s3)
-                       : (lane < 2 ? (lane & 1 ? p.b1 : p.s1) : (lane & 1 ? p.b2 : p.s2)));
-        const size_t row_i = lane < 2 ? s.r0 : s.r1;
-        bulk_load(smem_u32(r.sc + (size_t)r.sc_st * p.sc_slot + lane * blk), base + row_i * (size_t)(K / 64 * 2), blk,
-                  smem_u32(&r.sh->sc_full[r.sc_st]));
-      }
-      ++r.sc_issued;
-      advance(r.sc_st, r.sc_ph, p.sc_slots);
-    }
-    const uint32_t dst_row = smem_u32(r.tiles) + lane * (p.ch + pad_of(FMT));
-    for (int off = 0; off < rb; off += p.ch) {
-      int good = 1;
-      if (lane == 0) {
-        // a consumer that gave up releases stages it did not wait for, having
-        // raised the flag first: nothing may be copied into them
-        good = wait_on(&r.sh->empty[r.st], r.ph ^ 1u, r.sh, p, kDevTimeoutProducer) && !*abort_flag;
-        if (good) mbar_expect_tx(&r.sh->full[r.st], min(p.ch, rb - off) * (s.n0 + s.n1));
-      }
-      if (!__shfl_sync(0xffffffffu, good, 0)) {
-        r.ok = false;
-        break;
-      }
-      if (mine)
-        bulk_load(dst_row + r.st * p.stage_bytes, row + off, min(p.ch, rb - off), smem_u32(&r.sh->full[r.st]));
-      ++r.issued;
-      advance(r.st, r.ph, p.stages);
-    }
+__device__ __forceinline__ void feed_task(const FewParams &p, const Shared *sh, Feed &f) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const Task t = task_of(f.g, f.g.first + f.j);
+  const Span w = warp_span(f.g, t.kp, warp);
+  const Src s = task_src(p, f.part, f.part >= R1 ? sh->act[t.i] : 0, t.b, f.g.rb);
+  f.u = 0;
+  f.nseg = w.n;
+  f.nu = (w.n + SEGS - 1) / SEGS;
+  f.ends = w.first + w.n == f.g.ns;
+  f.tail = f.g.rb - (f.g.ns - 1) * SEG - c * 16;
+  const size_t off = (size_t)w.first * SEG + c * 16;
+  f.lo = g < s.n0 ? s.w0 + (size_t)g * f.g.rb + off : nullptr;
+  f.hi = g < s.n1 ? s.w1 + (size_t)g * f.g.rb + off : nullptr;
+  if (FMT == Q4) {
+    // groups 2c, 2c + 1 of the unit's eight; words of two groups, from the
+    // word that holds the first (a row of an odd number of groups may start
+    // in the middle of one)
+    const int KG = f.g.rb / 32, g0 = w.first * 2 + 2 * c;
+    f.groups = KG - g0;
+    const size_t i0 = (s.r0 + g) * (size_t)KG + g0, i1 = (s.r1 + g) * (size_t)KG + g0;
+    const char *const base[4] = {
+        static_cast<const char *>(f.part == R2 ? p.s3 : p.s1), static_cast<const char *>(f.part == R2 ? p.b3 : p.b1),
+        static_cast<const char *>(f.part == R2 ? p.s3 : p.s2), static_cast<const char *>(f.part == R2 ? p.b3 : p.b2)};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) f.sc[q] = base[q] + ((q < 2 ? i0 : i1) & ~(size_t)1) * 2;
   }
 }
 
-// ---------------------------------------------------------------- consumers
+// The stream at the first part from `part` on in which this warp has a task.
+// (By value: a reference would keep the caller's copy in memory.)
+template <int FMT>
+__device__ __noinline__ Feed feed_part(const FewParams &p, const Shared *sh, Feed f, int part) {
+  const int warp = threadIdx.x >> 5;
+  for (; part < f.limit; ++part) {
+    f.g = part < R1 ? part_geo<BF16>(p, part, sh->nact) : part_geo<FMT>(p, part, sh->nact);
+    f.j = f.g.solo ? warp : 0;
+    if (f.j < f.g.n) break;
+  }
+  f.part = part;
+  if (part < f.limit) {
+    if (part < R1) feed_task<BF16>(p, sh, f);
+    else feed_task<FMT>(p, sh, f);
+  }
+  return f;
+}
+
+// 4-bit pieces: lane (g, c) keeps its 16 bytes so that the eight bytes that
+// the lanes of four rows read at once lie in different banks
+__device__ __forceinline__ uint32_t piece_at(bool q4) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  return q4 ? g * 64 + ((c ^ (g & 2)) << 4) : lane * 16;
+}
+
+// Fetches the next unit (if there is one yet) and closes its group.
+template <int FMT>
+__device__ __forceinline__ void feed_step(const FewParams &p, const Shared *sh, Feed &f, uint32_t ring) {
+  if (f.part < f.limit) {
+    const int lane = threadIdx.x & 31;
+    const bool q4 = FMT == Q4 && f.part >= R1;
+    const uint32_t slot = ring + (f.issued % DEPTH) * unit_bytes(FMT);
+    const uint32_t dst = slot + piece_at(q4);
+    const int n = min(SEGS, f.nseg - f.u * SEGS);
+    // (the row's last segment may be short of this lane's piece)
+    const int whole = f.ends && f.u + 1 == f.nu && f.tail <= 0 ? n - 1 : n;
+#pragma unroll
+    for (int s = 0; s < SEGS; ++s)
+      if (s < whole) {
+        if (f.lo) cp_async16(dst + s * 1024, f.lo + s * SEG);
+        if (f.hi) cp_async16(dst + s * 1024 + 512, f.hi + s * SEG);
+      }
+    if (f.lo) f.lo += UNIT;
+    if (f.hi) f.hi += UNIT;
+    if (q4) {
+      const int KG = f.g.rb / 32;
+      const int left = f.groups - f.u * 8;  // groups of the row from this lane's first on
+      const bool odd = (KG & 1) && ((lane >> 2) & 1);     // the first group is the high half of its word
+      const uint32_t d = slot + ROWS * UNIT + lane * 32;
+      if (left > 0) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          cp_async4(d + q * 4, f.sc[q] + f.u * 16);
+          if (odd && left > 1) cp_async4(d + 16 + q * 4, f.sc[q] + f.u * 16 + 4);
+        }
+      }
+    }
+    ++f.issued;
+    if (++f.u == f.nu) {
+      f.j += f.g.solo ? CW : 1;
+      if (f.j < f.g.n) {
+        if (f.part < R1) feed_task<BF16>(p, sh, f);
+        else feed_task<FMT>(p, sh, f);
+      } else {
+        f = feed_part<FMT>(p, sh, f, f.part + 1);
+      }
+    }
+  }
+  cp_async_commit();
+}
+
+// Lets the stream go on into parts before `limit`, and fills it up.
+template <int FMT>
+__device__ __noinline__ void feed_open(const FewParams &p, const Shared *sh, Feed &feed, uint32_t ring, int limit) {
+  Feed f = feed;
+  const int from = f.part;
+  const bool stopped = f.part >= f.limit;
+  f.limit = limit;
+  if (stopped) f = feed_part<FMT>(p, sh, f, from);
+  __syncwarp();
+  for (uint32_t i = f.issued - f.used; i < DEPTH; ++i) feed_step<FMT>(p, sh, f, ring);
+  feed = f;
+}
+
+// ---------------------------------------------------------------- products
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// with a zero accumulator
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -362,39 +462,34 @@ __device__ __forceinline__ uint4 ld_l1(const char *p) {
   asm volatile("ld.global.ca.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
-// n arrivals at once
-__device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
-}
 // the larger magnitude, NaN above all
 __device__ __forceinline__ float abs_max(float a, float b) {
   return __uint_as_float(max(__float_as_uint(a) & 0x7FFFFFFFu, __float_as_uint(b) & 0x7FFFFFFFu));
 }
-__device__ __forceinline__ uint4 lds128(const uint8_t *p) { return *reinterpret_cast<const uint4 *>(p); }
-
-// B operand of one 64-byte segment of weight rows.  bf16 and 8-bit: 16 bytes
-// of the token row (and of its low part).  4-bit: a segment is two groups of
-// 64 codes; 16 elements of the token row per group.
-template <int FMT, bool LO>
-struct BSeg {
-  uint4 v[FMT == Q4 ? 4 : 1][LO ? 2 : 1];
-};
-
-// segments whose operand a warp holds at once (4-bit: four times the registers each)
-template <int FMT>
-__host__ __device__ constexpr int segs_of() {
-  return FMT == Q4 ? 2 : 4;
-}
+__device__ __forceinline__ float silu_f(float g) { return g / (1.f + expf(-g)); }
 
 // bytes of the token row per byte of the weight row
 template <int FMT>
 __host__ __device__ constexpr int ratio_of() {
   return FMT == Q4 ? 4 : 1;
 }
+// segments whose token operand a warp holds at once (4-bit: four times the registers each)
+template <int FMT>
+__host__ __device__ constexpr int held_of() {
+  return FMT == Q4 ? 2 : 4;
+}
 
-// row: this lane's place in the segment's stretch of the token row (its first
-// byte plus lane_off); left: bytes of the weight row from the segment on.
-// CHECK: the segment may reach past the row's end.
+// B operand of one segment.  bf16 and 8-bit: 16 bytes of the token row (and of
+// its low part).  4-bit: a segment is two groups of 64 codes; 16 elements of
+// the token row per group.
+template <int FMT, bool LO>
+struct BSeg {
+  uint4 v[FMT == Q4 ? 4 : 1][LO ? 2 : 1];
+};
+
+// row: this lane's place in the segment's stretch of the token row; left:
+// bytes of the weight row from the segment on.  CHECK: the segment may reach
+// past the row's end.
 template <int FMT, bool LO, bool CHECK>
 __device__ __forceinline__ void load_b(BSeg<FMT, LO> &bv, const char *row, size_t lo_bytes, int left, int c) {
 #pragma unroll
@@ -420,19 +515,18 @@ struct Acc<I8, NB> {
   int f[NB][2][4];
 };
 
-// One 64-byte segment of the 16 rows times the tokens.  lo_row / hi_row: this
-// lane's place in rows g and g + 8 (4-bit: without the lane's 8 c); left:
-// bytes of the rows from the segment on.  sc: 4-bit, the group's scales of
-// row g.  The first NBP blocks of eight tokens have their operand in
-// registers; a further one (4-bit weights, whose operand is four times as
-// long, and only for an expert that more than eight tokens chose) fetches it
-// here from `far`.
+// One segment of the 16 rows times the tokens.  a: this lane's place in the
+// segment's slots (4-bit: row g's); left: bytes of the rows from the segment
+// on.  sw: 4-bit, the lane's scale words of the segment (s and b of row g, of
+// row g + 8, two groups each).  The first NBP blocks of eight tokens have
+// their operand in registers; a further one (4-bit weights, whose operand is
+// four times as long, and only for an expert that more than eight tokens
+// chose) fetches it here from `far`.
 template <int FMT, bool LO, int NB, int NBP, bool CHECK>
 __device__ __forceinline__ void consume(Acc<FMT, NB> &acc, const BSeg<FMT, LO> (&bv)[NBP], const char *far, int left,
-                                        const uint8_t *lo_row, const uint8_t *hi_row, bool second, int c,
-                                        const uint16_t *sc, int groups) {
+                                        const uint8_t *a, bool second, int g, int c, const uint32_t (&sw)[4]) {
   if constexpr (FMT != Q4) {
-    uint4 lo = lds128(lo_row), hi = lds128(hi_row);
+    uint4 lo = *reinterpret_cast<const uint4 *>(a), hi = *reinterpret_cast<const uint4 *>(a + 512);
     if (CHECK && c * 16 >= left) lo = hi = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
@@ -453,19 +547,21 @@ __device__ __forceinline__ void consume(Acc<FMT, NB> &acc, const BSeg<FMT, LO> (
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       if (CHECK && q * 32 >= left) break;
-      const uint2 lo = *reinterpret_cast<const uint2 *>(lo_row + q * 32);
-      const uint2 hi = *reinterpret_cast<const uint2 *>(hi_row + q * 32);
+      const int half = (q ^ ((g >> 1) & 1)) * 32 + c * 8;
+      const uint2 lo = *reinterpret_cast<const uint2 *>(a + half);
+      const uint2 hi = *reinterpret_cast<const uint2 *>(a + 512 + half);
       // scale and bias of rows g and g + 8 for this group.  The codes enter as
       // 128 + q (an exact bf16 by its bits), so the bias takes 128 s off again
-      const float s_lo = bf16_to_f32(sc[q]), s_hi = bf16_to_f32(sc[16 * groups + q]);
-      const float b_lo = fmaf(-128.f, s_lo, bf16_to_f32(sc[8 * groups + q]));
-      const float b_hi = fmaf(-128.f, s_hi, bf16_to_f32(sc[24 * groups + q]));
+      const float s_lo = __uint_as_float(q ? sw[0] & 0xFFFF0000u : sw[0] << 16);
+      const float s_hi = __uint_as_float(q ? sw[2] & 0xFFFF0000u : sw[2] << 16);
+      const float b_lo = fmaf(-128.f, s_lo, __uint_as_float(q ? sw[1] & 0xFFFF0000u : sw[1] << 16));
+      const float b_hi = fmaf(-128.f, s_hi, __uint_as_float(q ? sw[3] & 0xFFFF0000u : sw[3] << 16));
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
         if (n > 0 && !second) break;
         BSeg<FMT, LO> own;
         if (n >= NBP) load_b<FMT, LO, CHECK>(own, far, 0, left, c);
-        float dq[4] = {0.f, 0.f, 0.f, 0.f}, dx[4] = {0.f, 0.f, 0.f, 0.f};
+        float dq[4], dx[4];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const uint32_t wl = u ? lo.y : lo.x, wh = u ? hi.y : hi.x;
@@ -474,22 +570,25 @@ __device__ __forceinline__ void consume(Acc<FMT, NB> &acc, const BSeg<FMT, LO> (
           const uint4 b = n < NBP ? bv[n < NBP ? n : 0].v[2 * q + u][0] : own.v[2 * q + u][0];
           const uint32_t p0 = __byte_perm(b.x, b.z, 0x5410), p1 = __byte_perm(b.x, b.z, 0x7632);
           const uint32_t p2 = __byte_perm(b.y, b.w, 0x5410), p3 = __byte_perm(b.y, b.w, 0x7632);
-          mma_bf16(dq, code_pair(wl, 0), code_pair(wh, 0), code_pair(wl, 1), code_pair(wh, 1), p0, p1);
-          mma_bf16(dx, one, one, one, one, p0, p1);
+          if (u == 0) {
+            mma_bf16_first(dq, code_pair(wl, 0), code_pair(wh, 0), code_pair(wl, 1), code_pair(wh, 1), p0, p1);
+            mma_bf16_first(dx, one, one, one, one, p0, p1);
+          } else {
+            mma_bf16(dq, code_pair(wl, 0), code_pair(wh, 0), code_pair(wl, 1), code_pair(wh, 1), p0, p1);
+            mma_bf16(dx, one, one, one, one, p0, p1);
+          }
           mma_bf16(dq, code_pair(wl, 2), code_pair(wh, 2), code_pair(wl, 3), code_pair(wh, 3), p2, p3);
           mma_bf16(dx, one, one, one, one, p2, p3);
         }
-        float(&a)[4] = acc.f[n][q];
-        a[0] = fmaf(s_lo, dq[0], fmaf(b_lo, dx[0], a[0]));
-        a[1] = fmaf(s_lo, dq[1], fmaf(b_lo, dx[1], a[1]));
-        a[2] = fmaf(s_hi, dq[2], fmaf(b_hi, dx[2], a[2]));
-        a[3] = fmaf(s_hi, dq[3], fmaf(b_hi, dx[3], a[3]));
+        float(&t)[4] = acc.f[n][q];
+        t[0] = fmaf(s_lo, dq[0], fmaf(b_lo, dx[0], t[0]));
+        t[1] = fmaf(s_lo, dq[1], fmaf(b_lo, dx[1], t[1]));
+        t[2] = fmaf(s_hi, dq[2], fmaf(b_hi, dx[2], t[2]));
+        t[3] = fmaf(s_hi, dq[3], fmaf(b_hi, dx[3], t[3]));
       }
     }
   }
 }
-
-__device__ __forceinline__ float silu_f(float g) { return g / (1.f + expf(-g)); }
 
 // n-th set bit of a mask (the mask has more than n)
 __device__ __forceinline__ int nth_bit(uint32_t m, int n) {
@@ -498,25 +597,28 @@ __device__ __forceinline__ int nth_bit(uint32_t m, int n) {
 }
 
 struct Cursor {
-  int task, e, rows, row0, b;               // row0: first row of h / y
+  int e, rows, row0, b, kp;                 // row0: first row of h / y; b: row block; kp: part of K
   uint32_t mask;
 };
 
 template <int PART>
-__device__ __forceinline__ void place(const FewParams &p, const Shared *sh, const Dims &dm, Cursor &cu) {
-  const int i = cu.task / dm.nb;
-  cu.b = cu.task - i * dm.nb;
+__device__ __forceinline__ Cursor cursor_of(const FewParams &p, const Shared *sh, const Geo &g, int task) {
+  Cursor cu;
+  const Task t = task_of(g, task);
+  cu.kp = t.kp;
+  cu.b = t.b;
   if (PART == S1 || PART == S2) {
     cu.e = 0;
     cu.mask = (1u << p.T) - 1u;
     cu.row0 = 0;
     cu.rows = p.T;
   } else {
-    cu.e = sh->act[i];
+    cu.e = sh->act[t.i];
     cu.mask = sh->mask[cu.e];
-    cu.row0 = sh->row0[i];
-    cu.rows = sh->row0[i + 1] - cu.row0;
+    cu.row0 = sh->row0[t.i];
+    cu.rows = sh->row0[t.i + 1] - cu.row0;
   }
+  return cu;
 }
 
 // Row r of a task's token operand.  A row past the task's last repeats the
@@ -559,7 +661,7 @@ __device__ __forceinline__ float emit(const FewParams &p, const Cursor &cu, int 
     if (pairs) u *= xs * __ldg(static_cast<const float *>(p.s2) + r0);
   }
   if (PHASE2) {
-    p.y[(PART == S2 ? (size_t)p.T * p.k + tok : row) * p.d + col] = v;
+    p.y[(PART == S2 ? (size_t)p.ksplit * p.y_rows + tok : (size_t)cu.kp * p.y_rows + row) * p.d + col] = v;
     return 0.f;
   }
   if (pairs) v = silu_f(v) * u;
@@ -575,152 +677,133 @@ __device__ __forceinline__ float emit(const FewParams &p, const Cursor &cu, int 
   return __bfloat162float(hi);
 }
 
-// The block's tasks of one part.  Long rows: the eight warps split each
-// stage's K, and their partial results meet in shared memory.  SOLO, rows that
-// fit one stage: each of p.solo warps takes every p.solo-th task by itself, so
-// nothing waits for the other warps (a short task's barrier and sum took
-// longer than its weights: 16 tokens over 4-bit experts, 83 of them at
-// d = 2048, F = 768, ran 261 us that way).  The number of stages (and of scale
-// slots) is a multiple of p.solo, so within a part a stage always serves the
-// same warp: a barrier's parity tells a warp only whether the use it waits
-// for is over if it has seen the one before.
-template <int FMT, int PART, int NB, bool SOLO>
-__device__ __noinline__ void consume_part(const FewParams &p, Ring &r, uint32_t &red_it) {
-  Shared *sh = r.sh;
+// The block's tasks of one part.  RFMT: the routed experts' format, which the
+// stream may go on to.
+template <int FMT, int RFMT, int PART, int NB, bool SOLO>
+__device__ __noinline__ void consume_part(const FewParams &p, Shared *sh, uint8_t *ring_ptr, Feed &feed, uint32_t &red_it,
+                                          const Geo &geo) {
   constexpr bool PHASE2 = PART == S2 || PART == R2;
   constexpr bool LO = PHASE2 && FMT == BF16;
   constexpr int NBP = FMT == Q4 ? 1 : NB;   // blocks of eight tokens whose operand is fetched ahead
   constexpr int R = ratio_of<FMT>();
-  const Dims dm = part_dims(p, PART, sh->nact);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int K = !PHASE2 ? p.d : (PART == S2 ? p.Fs : p.F);
-  const int rb = row_bytes<FMT>(K);
-  const int groups = K / 64;
+  constexpr int HELD = held_of<FMT>();
+  const Geo g = geo;
+  Feed f = feed;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, c = lane & 3;
+  const uint32_t ring = smem_u32(ring_ptr);
   const size_t lo_bytes = 2 * (PART == S2 ? p.hs_lo : p.h_lo);
-  const int w0 = SOLO ? 0 : warp * 64;      // this warp's first segment of a piece
-  constexpr int STEP = SOLO ? 64 : CW * 64; // and the distance to its next
-  constexpr int SEGS = segs_of<FMT>();
-  constexpr int FULL = SEGS * STEP;         // bytes of a row in a whole piece
-  const int start = min(min(FULL, p.ch), rb);   // and in a row's first
-  const int lane_b = (w0 + c * (FMT == Q4 ? 8 : 16)) * R;
-  const uint32_t row_lo = g * (p.ch + pad_of(FMT)) + w0 + c * (FMT == Q4 ? 8 : 16);
-  const uint32_t row_hi = row_lo + 8 * (p.ch + pad_of(FMT));
-  const int mine = dm.n, end = dm.first + dm.n;       // tasks of this block
-  if (mine == 0) return;
-  const int stride = SOLO ? p.solo : 1;
-  uint32_t st = r.st, ph = r.ph, sc_st = r.sc_st, sc_ph = r.sc_ph;
-  const int skip = SOLO ? min(warp, mine) : 0;
-  for (int i = 0; i < skip; ++i) {
-    advance(st, ph, p.stages);
-    if (FMT == Q4) advance(sc_st, sc_ph, p.sc_slots);
-  }
+  const bool even = g.rb % SEG == 0;        // whole segments only
+  const bool odd_groups = FMT == Q4 && (g.rb / 32 & 1) && (lg & 1);
+  const bool pairs = PART == S1 || (PART == R1 && p.swiglu);
+  const int stride = SOLO ? CW : 1;
+  const int lane_b = c * (FMT == Q4 ? 8 : 16) * R;
 
-  Cursor cu;
-  cu.task = dm.first + (SOLO ? warp : 0);
-  if (cu.task < end && (!SOLO || warp < p.solo)) {
-    place<PART>(p, sh, dm, cu);
-    const char *bp[NB];                     // the piece's stretch of the token rows, at this lane
-    BSeg<FMT, LO> bv[SEGS][NBP];
+  // a task's token rows at this lane and the warp's place in them
+  auto enter = [&](int j, Cursor &cu, Span &w, const char *(&rp)[NB]) {
+    cu = cursor_of<PART>(p, sh, g, g.first + j);
+    w = warp_span(g, cu.kp, warp);
 #pragma unroll
-    for (int n = 0; n < NB; ++n) bp[n] = b_row<FMT, PART>(p, cu, g + 8 * n) + lane_b;
+    for (int n = 0; n < NB; ++n) rp[n] = b_row<FMT, PART>(p, cu, lg + 8 * n) + lane_b + (size_t)w.first * SEG * R;
+  };
+
+  int j = SOLO ? warp : 0;
+  if (j < g.n) {
+    Cursor cu;
+    Span w;
+    const char *rowp[NB];
+    enter(j, cu, w, rowp);
+    BSeg<FMT, LO> bv[HELD][NBP];
 #pragma unroll
-    for (int s = 0; s < SEGS; ++s)
+    for (int s = 0; s < HELD; ++s)
 #pragma unroll
       for (int n = 0; n < NBP; ++n)
-        load_b<FMT, LO, true>(bv[s][n], bp[n] + s * STEP * R, lo_bytes, start - w0 - s * STEP, c);
-
+        load_b<FMT, LO, true>(bv[s][n], rowp[n] + s * SEG * R, lo_bytes, g.rb - (w.first + s) * SEG, c);
     for (;;) {
       Acc<FMT, NB> acc;
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc.f[n][0][j] = acc.f[n][1][j] = 0;
-      Cursor nx = cu;
-      nx.task += stride;
-      const bool more = nx.task < end;
+        for (int i = 0; i < 4; ++i) acc.f[n][0][i] = acc.f[n][1][i] = 0;
       const bool second = cu.rows > 8;
-      const uint16_t *sc = nullptr;
-      if (FMT == Q4) {
-        wait_on(&sh->sc_full[sc_st], sc_ph, sh, p, kDevTimeoutEpilogue);
-        sc = reinterpret_cast<const uint16_t *>(r.sc + (size_t)sc_st * p.sc_slot) + g * groups + w0 / 32;
-      }
-      int in = 0;                           // bytes of the rows before this piece in its stage
-      for (int off = 0, left; off < rb; off += left) {
-        left = min(min(FULL, p.ch - in), rb - off);
-        // where the next piece's token operand comes from: its loads take the
-        // registers of each segment as soon as that has been used
-        const bool last = off + left >= rb;
-        const bool ends = last || in + left == p.ch;        // of the stage
-        const char *bn[NB];
-        int next_left;                      // bytes of the weight rows in the next piece, none: 0
-        if (!last) {
-          next_left = min(min(FULL, ends ? p.ch : p.ch - in - left), rb - off - left);
+      const bool more = j + stride < g.n;
+      // the next task, whose first token operand is fetched during this one's last unit
+      Cursor nc = cu;
+      Span nw{0, 0};
+      const char *nrow[NB];
 #pragma unroll
-          for (int n = 0; n < NB; ++n) bn[n] = bp[n] + left * R;
-        } else {
-          next_left = more ? start : 0;
-          if (more) place<PART>(p, sh, dm, nx);
-#pragma unroll
-          for (int n = 0; n < NB; ++n) bn[n] = more ? b_row<FMT, PART>(p, nx, g + 8 * n) + lane_b : bp[n];
-        }
-        const uint8_t *tile = r.tiles + (size_t)st * p.stage_bytes + in;
-        if (in == 0) wait_on(&sh->full[st], ph, sh, p, kDevTimeoutEpilogue);
-        __syncwarp();
-        if (left == FULL && next_left == FULL) {
+      for (int n = 0; n < NB; ++n) nrow[n] = rowp[n];
+      const int nu = (w.n + SEGS - 1) / SEGS;
+      for (int u = 0; u < nu; ++u) {
+        const bool last = u + 1 == nu;
+        if (last && more) enter(j + stride, nc, nw, nrow);
+        const int n_seg = min(SEGS, w.n - u * SEGS);
+        const int row_left = g.rb - (w.first + u * SEGS) * SEG;          // bytes of the row from here on
+        // the unit after this one: its segments, their token rows, and what is left of the row there
+        const int next_seg = last ? min(SEGS, nw.n) : min(SEGS, w.n - (u + 1) * SEGS);
+        const int next_left = last ? g.rb - nw.first * SEG : row_left - UNIT;
+        const int here = u * UNIT * R, there = last ? 0 : here + UNIT * R;
+        const uint8_t *slot = ring_ptr + (f.used % DEPTH) * unit_bytes(RFMT);
+        cp_async_wait<DEPTH - 1>();
+        if (FMT == Q4) __syncwarp();
+        const uint8_t *a = FMT == Q4 ? slot + lg * 64 : slot + lane * 16;
+        uint32_t sw[4] = {0u, 0u, 0u, 0u};
+        auto step = [&](auto check) {
+          constexpr bool CHECK = decltype(check)::value;
 #pragma unroll
           for (int s = 0; s < SEGS; ++s) {
-            consume<FMT, LO, NB, NBP, false>(acc, bv[s], bp[NB - 1] + s * STEP * R, 64, tile + row_lo + s * STEP,
-                                             tile + row_hi + s * STEP, second, c, sc + (off + s * STEP) / 32, groups);
+            if (s < n_seg) {
+              if constexpr (FMT == Q4) {
+                const uint4 *t = reinterpret_cast<const uint4 *>(slot + ROWS * UNIT + (lg * 4 + s) * 32);
+                const uint4 x = t[0];
+                sw[0] = x.x; sw[1] = x.y; sw[2] = x.z; sw[3] = x.w;
+                if (odd_groups) {
+                  const uint4 y = t[1];
+                  sw[0] = __funnelshift_r(x.x, y.x, 16); sw[1] = __funnelshift_r(x.y, y.y, 16);
+                  sw[2] = __funnelshift_r(x.z, y.z, 16); sw[3] = __funnelshift_r(x.w, y.w, 16);
+                }
+              }
+              consume<FMT, LO, NB, NBP, CHECK>(acc, bv[s % HELD], rowp[NB - 1] + here + s * SEG * R, row_left - s * SEG,
+                                               a + s * 1024, second, lg, c, sw);
+            }
+            // the operand of the segment HELD further on takes its registers
+            const int t = s + HELD;
+            if (t < SEGS) {
+              if (t < n_seg) {
 #pragma unroll
-            for (int n = 0; n < NBP; ++n) load_b<FMT, LO, false>(bv[s][n], bn[n] + s * STEP * R, lo_bytes, 64, c);
+                for (int n = 0; n < NBP; ++n)
+                  load_b<FMT, LO, CHECK>(bv[s % HELD][n], rowp[n] + here + t * SEG * R, lo_bytes, row_left - t * SEG, c);
+              }
+            } else if (t - SEGS < next_seg) {
+#pragma unroll
+              for (int n = 0; n < NBP; ++n)
+                load_b<FMT, LO, CHECK>(bv[s % HELD][n], (last ? nrow[n] : rowp[n]) + there + (t - SEGS) * SEG * R, lo_bytes,
+                                       next_left - (t - SEGS) * SEG, c);
+            }
           }
-        } else {
-#pragma unroll
-          for (int s = 0; s < SEGS; ++s) {
-            const int at = w0 + s * STEP;
-            if (at < left)
-              consume<FMT, LO, NB, NBP, true>(acc, bv[s], bp[NB - 1] + s * STEP * R, left - at,
-                                              tile + row_lo + s * STEP, tile + row_hi + s * STEP, second, c,
-                                              sc + (off + s * STEP) / 32, groups);
-#pragma unroll
-            for (int n = 0; n < NBP; ++n)
-              load_b<FMT, LO, true>(bv[s][n], bn[n] + s * STEP * R, lo_bytes, next_left - at, c);
-          }
-        }
-        if (ends) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive_n(&sh->empty[st], SOLO ? CW : 1);
-          if (!SOLO) advance(st, ph, p.stages);
-          in = 0;
-        } else {
-          in += left;
-        }
-#pragma unroll
-        for (int n = 0; n < NB; ++n) bp[n] = bn[n];
+        };
+        if (even) step(std::false_type{});
+        else step(std::true_type{});
+        if (FMT == Q4) __syncwarp();
+        ++f.used;
+        feed_step<RFMT>(p, sh, f, ring);
       }
       if (SOLO) {
-        if (FMT == Q4 && lane == 0) mbar_arrive(&sh->sc_empty[sc_st]);
-        for (int i = 0; i < p.solo; ++i) {
-          advance(st, ph, p.stages);
-          if (FMT == Q4) advance(sc_st, sc_ph, p.sc_slots);
-        }
         // accumulators 0, 1: row g, tokens 2c, 2c + 1; 2, 3: row g + 8
-        const bool pairs = PART == S1 || (PART == R1 && p.swiglu);
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
           if (n > 0 && !second) break;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int tok = 8 * n + 2 * c + j;
-            const float a = (float)(acc.f[n][0][j] + acc.f[n][1][j]);
-            const float b = (float)(acc.f[n][0][j + 2] + acc.f[n][1][j + 2]);
-            float m = emit<FMT, PART>(p, cu, g, tok, a, b);
-            if (!pairs) m = abs_max(m, emit<FMT, PART>(p, cu, g + 8, tok, b, 0.f));
+          for (int i = 0; i < 2; ++i) {
+            const int tok = 8 * n + 2 * c + i;
+            const float v0 = (float)(acc.f[n][0][i] + acc.f[n][1][i]);
+            const float v1 = (float)(acc.f[n][0][i + 2] + acc.f[n][1][i + 2]);
+            float m = emit<FMT, PART>(p, cu, lg, tok, v0, v1);
+            if (!pairs) m = abs_max(m, emit<FMT, PART>(p, cu, lg + 8, tok, v1, 0.f));
             if (FMT == I8 && PART == R1) {
               uint32_t top = __float_as_uint(m) & 0x7FFFFFFFu;
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-              if (g == 0 && tok < cu.rows) atomicMax(p.rowmax + cu.row0 + tok, top);
+              if (lg == 0 && tok < cu.rows) atomicMax(p.rowmax + cu.row0 + tok, top);
             }
           }
         }
@@ -732,76 +815,60 @@ __device__ __noinline__ void consume_part(const FewParams &p, Ring &r, uint32_t 
         for (int n = 0; n < NB; ++n) {
           uint32_t v[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const auto sum = acc.f[n][0][j] + acc.f[n][1][j];
-            if constexpr (FMT == I8) v[j] = (uint32_t)sum;
-            else v[j] = __float_as_uint(sum);
+          for (int i = 0; i < 4; ++i) {
+            const auto sum = acc.f[n][0][i] + acc.f[n][1][i];
+            if constexpr (FMT == I8) v[i] = (uint32_t)sum;
+            else v[i] = __float_as_uint(sum);
           }
           *reinterpret_cast<uint4 *>(red[warp][n][lane]) = make_uint4(v[0], v[1], v[2], v[3]);
         }
-        consumer_sync();
-        if (FMT == Q4) {
-          if (threadIdx.x == 0) mbar_arrive(&sh->sc_empty[sc_st]);
-          advance(sc_st, sc_ph, p.sc_slots);
-        }
+        __syncthreads();
         ++red_it;
-        // value (row, token) of the task: accumulator j of lane 4 (row % 8) + (token % 8) / 2
+        // value (row, token) of the task: accumulator i of lane 4 (row % 8) + (token % 8) / 2
         auto total = [&](int row, int tok) {
-          const int ln = (row & 7) * 4 + ((tok & 7) >> 1), j = (tok & 1) + (row >> 3) * 2, n = tok >> 3;
+          const int ln = (row & 7) * 4 + ((tok & 7) >> 1), i = (tok & 1) + (row >> 3) * 2, n = tok >> 3;
           if (FMT == I8) {
             int v = 0;
 #pragma unroll
-            for (int w = 0; w < CW; ++w) v += (int)red[w][n][ln][j];
+            for (int q = 0; q < CW; ++q) v += (int)red[q][n][ln][i];
             return (float)v;
           }
           float v = 0.f;
 #pragma unroll
-          for (int w = 0; w < CW; ++w) v += __uint_as_float(red[w][n][ln][j]);
+          for (int q = 0; q < CW; ++q) v += __uint_as_float(red[q][n][ln][i]);
           return v;
         };
-        const bool pairs = PART == S1 || (PART == R1 && p.swiglu);
         const int cols = pairs ? 8 : ROWS;
         const int most = cols * 8 * (second ? 2 : 1);
-        for (int i = threadIdx.x; i < most; i += CT) {            // whole warps take part
-          const int tok = i / cols, f = i - tok * cols;
-          const float m = tok < cu.rows ? emit<FMT, PART>(p, cu, f, tok, total(f, tok), pairs ? total(f + 8, tok) : 0.f) : 0.f;
+        // (whole warps, other ones from task to task: the scales they fetch are not waited for by all)
+        for (int i = (threadIdx.x + 64 * red_it) % CT; i < most; i += CT) {
+          const int tok = i / cols, q = i - tok * cols;
+          const float m =
+              tok < cu.rows ? emit<FMT, PART>(p, cu, q, tok, total(q, tok), pairs ? total(q + 8, tok) : 0.f) : 0.f;
           if (FMT == I8 && PART == R1) {
             // the row's largest |h|: over the task's columns (8 or 16 neighbouring lanes), then the grid
             uint32_t top = __float_as_uint(m) & 0x7FFFFFFFu;
             for (int o = 1; o < cols; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            if (f == 0 && tok < cu.rows) atomicMax(p.rowmax + cu.row0 + tok, top);
+            if (q == 0 && tok < cu.rows) atomicMax(p.rowmax + cu.row0 + tok, top);
           }
         }
       }
       if (!more) break;
-      cu = nx;
+      j += stride;
+      cu = nc;
+      w = nw;
+#pragma unroll
+      for (int n = 0; n < NB; ++n) rowp[n] = nrow[n];
     }
   }
-  // every warp leaves the part at the same place of the ring, and together:
-  // the next part's uses follow ones that other warps waited for
-  if (SOLO) {
-    consumer_sync();
-    const uint32_t n = r.st + mine;
-    r.ph ^= n / p.stages & 1u;
-    r.st = n % p.stages;
-    if (FMT == Q4) {
-      const uint32_t m = r.sc_st + mine;
-      r.sc_ph ^= m / p.sc_slots & 1u;
-      r.sc_st = m % p.sc_slots;
-    }
-  } else {
-    r.st = st;
-    r.ph = ph;
-    r.sc_st = sc_st;
-    r.sc_ph = sc_ph;
-  }
+  feed = f;
 }
 
-template <int FMT, int PART, int NB>
-__device__ __forceinline__ void run_part(const FewParams &p, Ring &r, uint32_t &red_it) {
-  const int K = PART == S1 || PART == R1 ? p.d : (PART == S2 ? p.Fs : p.F);
-  if (row_bytes<FMT>(K) <= p.ch && p.solo >= CW / 2) consume_part<FMT, PART, NB, true>(p, r, red_it);
-  else consume_part<FMT, PART, NB, false>(p, r, red_it);
+template <int FMT, int RFMT, int PART, int NB>
+__device__ __forceinline__ void run_part(const FewParams &p, Shared *sh, uint8_t *ring, Feed &feed, uint32_t &red_it) {
+  const Geo g = part_geo<FMT>(p, PART, sh->nact);
+  if (g.solo) consume_part<FMT, RFMT, PART, NB, true>(p, sh, ring, feed, red_it, g);
+  else consume_part<FMT, RFMT, PART, NB, false>(p, sh, ring, feed, red_it, g);
 }
 
 // ---------------------------------------------------------------- router
@@ -907,14 +974,14 @@ __device__ __forceinline__ void route_logits(const FewParams &p, Shared *sh) {
     // the lane's token: its bits from 16 down chose the halves
     constexpr int LOG = TP == 16 ? 4 : (TP == 8 ? 3 : (TP == 4 ? 2 : 0));
     if ((lane & ((32 >> LOG) - 1)) == 0) sums[warp][lane >> (5 - LOG)] = acc[0];
-    consumer_sync();
+    __syncthreads();
     for (int i = threadIdx.x; i < at_once * p.T; i += CT) {
       const int t = i / at_once, q = i - t * at_once;
       double s = 0.0;
       for (int j = 0; j < per; ++j) s += sums[q * per + j][t];
       if (e0 + q < p.E) p.logits[(size_t)t * p.E + e0 + q] = s;
     }
-    consumer_sync();
+    __syncthreads();
   }
 }
 
@@ -958,7 +1025,7 @@ __device__ __forceinline__ void choose(const FewParams &p, Shared *sh, int t, do
     for (int j = 0; j < EPL; ++j) {
       const int e = lane + 32 * j;
       if (e < E) {
-        if (p.bias) key[j] = key_of(prob[e] + (double)__ldg(p.bias + e));
+        key[j] = key_of(prob[e] + (double)sh->bias[e]);
         keys[e] = key[j];
       }
     }
@@ -983,28 +1050,47 @@ __device__ __forceinline__ void choose(const FewParams &p, Shared *sh, int t, do
       const int gi = warp_argmax(open ? gkey : 0ull, open ? lane : 0x7fffffff);
       keep |= 1u << (gi & 31);
     }
+    const int inv = (65536 + G - 1) / G;               // e / G = e inv >> 16 for every e < E <= 256
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
       const int e = lane + 32 * j;
-      if (e < E && !((keep >> (e / G)) & 1u)) key[j] = min(key[j], LOWEST);
+      if (e < E && !((keep >> (e * inv >> 16)) & 1u)) key[j] = min(key[j], LOWEST);
+    }
+  }
+  // the lane's experts in order (Batcher's network of 19 exchanges, mostly
+  // side by side), so that a round looks at each lane's first only
+  int at[EPL];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) at[j] = lane + 32 * j;
+  if (E > 32) {
+    constexpr int net[19][2] = {{0, 1}, {2, 3}, {4, 5}, {6, 7}, {0, 2}, {1, 3}, {4, 6}, {5, 7}, {1, 2}, {5, 6},
+                                {0, 4}, {1, 5}, {2, 6}, {3, 7}, {2, 4}, {3, 5}, {1, 2}, {3, 4}, {5, 6}};
+    static_assert(EPL == 8, "the network sorts eight");
+#pragma unroll
+    for (int q = 0; q < 19; ++q) {
+      const int a = net[q][0], b = net[q][1];
+      const bool swap = key[b] > key[a] || (key[b] == key[a] && at[b] < at[a]);
+      const unsigned long long ka = key[a];
+      const int ia = at[a];
+      key[a] = swap ? key[b] : ka;
+      at[a] = swap ? at[b] : ia;
+      key[b] = swap ? ka : key[b];
+      at[b] = swap ? ia : at[b];
     }
   }
 
   int my_e = 0x7fffffff;
 #pragma unroll 1
   for (int r = 0; r < p.k; ++r) {
-    unsigned long long bk = 0;
-    int bi = 0x7fffffff;
+    const int bi = warp_argmax(key[0], key[0] ? at[0] : 0x7fffffff);
+    if (bi == at[0]) {                                 // taken: the lane's next moves up
 #pragma unroll
-    for (int j = EPL - 1; j >= 0; --j)                 // ties: the lower expert
-      if (key[j] >= bk && key[j] != 0ull) {
-        bk = key[j];
-        bi = lane + 32 * j;
+      for (int j = 0; j + 1 < EPL; ++j) {
+        key[j] = key[j + 1];
+        at[j] = at[j + 1];
       }
-    bi = warp_argmax(bk, bi);
-#pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (bi == lane + 32 * j) key[j] = 0ull;          // taken
+      key[EPL - 1] = 0ull;
+    }
     if (lane == r) my_e = bi;
   }
   const bool bad = none || my_e < 0 || my_e >= E;
@@ -1044,26 +1130,26 @@ __device__ __noinline__ void make_plan(const FewParams &p, Shared *sh, double *p
   for (int i = tid; i < p.T * p.E; i += CT) {
     double l = prob[i];
     if (p.router == MOE_ROUTER_SOFTMAX_TOPK) {
-      if (p.bias) l += (double)__ldg(p.bias + i % p.E);
+      if (p.bias) l += (double)sh->bias[i % p.E];
     } else {
       l = 1.0 / (1.0 + exp(-l));
     }
     prob[i] = l;
   }
-  consumer_sync();
+  __syncthreads();
 #pragma unroll 1
   for (int t = warp; t < p.T; t += CW) choose(p, sh, t, prob + (size_t)t * p.E, keys, lane);
-  consumer_sync();
+  __syncthreads();
   const int slots = p.T * p.k;
 #pragma unroll 1
   for (int i = tid; i < slots; i += CT) {
     const int e = sh->sel_id[i];
     if (e >= 0) atomicOr(&sh->mask[e], 1u << (i / p.k));
   }
-  consumer_sync();
+  __syncthreads();
   // thread e: expert e.  In-order dropping: the first `cap` tokens stay
   uint32_t m = sh->mask[tid];
-  const int raw = __popc(m);
+  sh->raw[tid] = (uint8_t)__popc(m);
   if (p.cap >= 0)
     while (__popc(m) > p.cap) m &= ~(0x80000000u >> __clz(m));
   const int cnt = __popc(m);
@@ -1079,7 +1165,7 @@ __device__ __noinline__ void make_plan(const FewParams &p, Shared *sh, double *p
     sh->warp_rows[warp] = pre;
   }
   sh->mask[tid] = m;
-  consumer_sync();
+  __syncthreads();
   int n = 0, rows = 0, all_n = 0, all_rows = 0;
 #pragma unroll
   for (int w = 0; w < CW; ++w) {
@@ -1099,21 +1185,24 @@ __device__ __noinline__ void make_plan(const FewParams &p, Shared *sh, double *p
     sh->nact = all_n;
     sh->row0[all_n] = (int16_t)all_rows;
   }
-  consumer_sync();
-  if (tid == 0) mbar_arrive(&sh->plan);
-  if (blockIdx.x == 0) {
-    for (int i = tid; i < slots; i += CT) {
-      p.ids[i] = sh->sel_id[i];
-      p.wts[i] = sh->sel_w[i];
-    }
-    if (tid < p.E) {
-      double s = 0.0;
-      for (int t = 0; t < p.T; ++t) s += prob[(size_t)t * p.E + tid];
-      p.prob_sum[tid] = (float)s;
-      p.raw_counts[tid] = raw;
-      p.kept_counts[tid] = cnt;
-      if (raw > cnt) atomicAdd(p.dropped, raw - cnt);
-    }
+  __syncthreads();
+}
+
+// What the call returns beside the output; one block, while it waits
+__device__ __forceinline__ void write_choice(const FewParams &p, const Shared *sh, const double *prob) {
+  const int e = threadIdx.x;
+  for (int i = e; i < p.T * p.k; i += CT) {
+    p.ids[i] = sh->sel_id[i];
+    p.wts[i] = sh->sel_w[i];
+  }
+  if (e < p.E) {
+    double s = 0.0;
+    for (int t = 0; t < p.T; ++t) s += prob[(size_t)t * p.E + e];
+    const int raw = sh->raw[e], kept = __popc(sh->mask[e]);
+    p.prob_sum[e] = (float)s;
+    p.raw_counts[e] = raw;
+    p.kept_counts[e] = kept;
+    if (raw > kept) atomicAdd(p.dropped, raw - kept);
   }
 }
 
@@ -1173,15 +1262,15 @@ __device__ __forceinline__ void quantize_x(const FewParams &p, Shared *sh) {
       m = abs_max2(v.x, abs_max2(v.y, abs_max2(v.z, abs_max2(v.w, m))));
     }
     m = __reduce_max_sync(0xffffffffu, m);
-    consumer_sync();
+    __syncthreads();
     if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = m;
-    consumer_sync();
+    __syncthreads();
     for (int w = 0; w < CW; ++w) m = max(m, scratch[w]);
     for (int i = threadIdx.x; i < p.d / 8; i += CT)
       reinterpret_cast<uint2 *>(p.xq + (size_t)t * p.d)[i] = codes8(__ldg(row + i), m);
     if (threadIdx.x == 0)
       p.xs[t] = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __fdiv_rn(__uint_as_float(m), 127.f);
-    consumer_sync();                        // the scratch has been read
+    __syncthreads();                        // the scratch has been read
   }
 }
 
@@ -1196,7 +1285,7 @@ __device__ __forceinline__ void quantize_h(const FewParams &p, const Shared *sh)
 }
 
 // out[t] = sum_j w_j y[slot_row] in slot order (+ the shared expert's row), 4 columns per thread
-__device__ __forceinline__ void combine(const FewParams &p, const Shared *sh) {
+__device__ __forceinline__ void combine(const FewParams &p, const Shared *sh, int ks) {
   const int nv = p.d / 4;
   for (int i = blockIdx.x * CT + threadIdx.x; i < p.T * nv; i += gridDim.x * CT) {
     const int t = i / nv, c = i - t * nv;
@@ -1205,14 +1294,18 @@ __device__ __forceinline__ void combine(const FewParams &p, const Shared *sh) {
       const int row = sh->slot_row[t * p.k + j];
       if (row < 0) continue;
       const float w = sh->sel_w[t * p.k + j];
-      const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.y + (size_t)row * p.d) + c);
+      float4 v = __ldcg(reinterpret_cast<const float4 *>(p.y + (size_t)row * p.d) + c);
+      for (int q = 1; q < ks; ++q) {
+        const float4 u = __ldcg(reinterpret_cast<const float4 *>(p.y + ((size_t)q * p.y_rows + row) * p.d) + c);
+        v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+      }
       a[0] = fmaf(w, v.x, a[0]);
       a[1] = fmaf(w, v.y, a[1]);
       a[2] = fmaf(w, v.z, a[2]);
       a[3] = fmaf(w, v.w, a[3]);
     }
     if (p.Fs) {
-      const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.y + (size_t)(p.T * p.k + t) * p.d) + c);
+      const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.y + ((size_t)p.ksplit * p.y_rows + t) * p.d) + c);
       a[0] += v.x;
       a[1] += v.y;
       a[2] += v.z;
@@ -1223,94 +1316,57 @@ __device__ __forceinline__ void combine(const FewParams &p, const Shared *sh) {
 }
 
 template <int FMT, int TP>
-__global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__ FewParams p) {
+__global__ void __launch_bounds__(CT, 1) few_kernel(const __grid_constant__ FewParams p) {
   constexpr int NB = TP > 8 ? 2 : 1;
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  Ring r;
-  r.tiles = smem_raw;
-  r.sc = smem_raw + (size_t)p.stages * p.stage_bytes;
-  r.scratch = r.sc + (size_t)p.sc_slots * p.sc_slot;
-  r.sh = reinterpret_cast<Shared *>(r.scratch + scratch_bytes(p.T, p.E));
-  r.st = r.ph = r.sc_st = r.sc_ph = r.issued = r.sc_issued = 0;
-  r.ok = true;
-  Shared *sh = r.sh;
-  const int warp = threadIdx.x >> 5;
+  uint8_t *ring_ptr = smem_raw + (threadIdx.x >> 5) * DEPTH * unit_bytes(FMT);      // this warp's
+  const uint32_t ring = smem_u32(ring_ptr);
+  double *prob = reinterpret_cast<double *>(smem_raw + CW * DEPTH * unit_bytes(FMT));
+  Shared *sh = reinterpret_cast<Shared *>(reinterpret_cast<uint8_t *>(prob) + scratch_bytes(p.T, p.E));
+  volatile int *abort_flag = &sh->abort_flag;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
-      mbar_init(&sh->full[s], 1);
-      mbar_init(&sh->empty[s], CW);
-    }
-    for (int s = 0; s < MAX_SC; ++s) {
-      mbar_init(&sh->sc_full[s], 1);
-      mbar_init(&sh->sc_empty[s], 1);
-    }
-    mbar_init(&sh->plan, 1);
     sh->abort_flag = 0;
     sh->nact = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    if (blockIdx.x == 0) *p.dropped = 0;
   }
+  sh->bias[threadIdx.x] = p.bias && threadIdx.x < p.E ? __ldg(p.bias + threadIdx.x) : 0.f;
   __syncthreads();
-  volatile int *abort_flag = &sh->abort_flag;
-
-  if (warp == CW) {
-    if (p.Fs) produce_part<BF16>(p, r, S1, 0);
-    if (p.Fs && r.ok) produce_part<BF16>(p, r, S2, 0);
-    if (r.ok)
-      r.ok = wait_bounded(&sh->plan, 0u, abort_flag, p.status, kDevTimeoutProducer, p.timeout_ns);
-    r.ok = __all_sync(0xffffffffu, r.ok);
-    const int nact = r.ok ? sh->nact : 0;
-    if (r.ok) produce_part<FMT>(p, r, R1, nact);
-    if (r.ok) produce_part<FMT>(p, r, R2, nact);
-    if ((threadIdx.x & 31) == 0 && !r.ok) {
-      // copies already issued land before the block goes away
-      const uint32_t n = p.stages, m = p.sc_slots;
-      for (uint32_t i = r.issued > n ? r.issued - n : 0u; i < r.issued; ++i)
-        if (!wait_drain(&sh->full[i % n], (i / n) & 1u)) record_status(p.status, kDevTimeoutDrain);
-      for (uint32_t i = r.sc_issued > m ? r.sc_issued - m : 0u; i < r.sc_issued; ++i)
-        if (!wait_drain(&sh->sc_full[i % m], (i / m) & 1u)) record_status(p.status, kDevTimeoutDrain);
-    }
-  } else {
-    uint32_t red_it = 0;
-    if (FMT == I8) {
-      quantize_x(p, sh);
-      if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < p.T * p.k; i += CT) p.rowmax[i] = 0u;
-    }
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.dropped = 0;
-    route_logits<TP>(p, sh);
-    if (p.Fs) run_part<BF16, S1, NB>(p, r, red_it);
-    grid_arrive(p.bar);
-    grid_wait(p.bar, abort_flag, p);
-    make_plan(p, sh, reinterpret_cast<double *>(r.scratch));
-    if (p.Fs) run_part<BF16, S2, NB>(p, r, red_it);
-    run_part<FMT, R1, NB>(p, r, red_it);
-    grid_arrive(p.bar + 8);
-    grid_wait(p.bar + 8, abort_flag, p);
-    if (FMT == I8) {
-      quantize_h(p, sh);
-      grid_arrive(p.bar + 16);
-      grid_wait(p.bar + 16, abort_flag, p);
-    }
-    run_part<FMT, R2, NB>(p, r, red_it);
-    grid_arrive(p.bar + 24);
-    slot_rows(p, sh);
-    grid_wait(p.bar + 24, abort_flag, p);
-    combine(p, sh);
+  Feed feed{};
+  uint32_t red_it = 0;
+  if (p.Fs) feed_open<FMT>(p, sh, feed, ring, R1);
+  else feed.part = feed.limit = R1;
+  if (FMT == I8) {
+    quantize_x(p, sh);
+    if (blockIdx.x == 0)
+      for (int i = threadIdx.x; i < p.T * p.k; i += CT) p.rowmax[i] = 0u;
   }
-  __syncthreads();
+  route_logits<TP>(p, sh);
+  if (p.Fs) run_part<BF16, FMT, S1, NB>(p, sh, ring_ptr, feed, red_it);
+  grid_arrive(p.bar);
+  grid_wait(p.bar, abort_flag, p);
+  make_plan(p, sh, prob);
+  feed_open<FMT>(p, sh, feed, ring, END);
+  if (p.Fs) run_part<BF16, FMT, S2, NB>(p, sh, ring_ptr, feed, red_it);
+  run_part<FMT, FMT, R1, NB>(p, sh, ring_ptr, feed, red_it);
+  grid_arrive(p.bar + 8);
+  grid_wait(p.bar + 8, abort_flag, p);
+  if (FMT == I8) {
+    quantize_h(p, sh);
+    grid_arrive(p.bar + 16);
+    grid_wait(p.bar + 16, abort_flag, p);
+  }
+  run_part<FMT, FMT, R2, NB>(p, sh, ring_ptr, feed, red_it);
+  grid_arrive(p.bar + 24);
+  if (blockIdx.x == 0) write_choice(p, sh, prob);
+  slot_rows(p, sh);
+  grid_wait(p.bar + 24, abort_flag, p);
+  combine(p, sh, part_geo<FMT>(p, R2, sh->nact).ks);
+  cp_async_wait<0>();
 }
 
 template <int FMT, int TP>
-cudaError_t run(FewParams &p, cudaStream_t s) {
-  const size_t fixed = sizeof(Shared) + scratch_bytes(p.T, p.E) + (size_t)p.sc_slots * p.sc_slot;
-  int stages = (int)((SMEM_LIMIT - fixed) / p.stage_bytes);
-  stages = stages < MAX_STAGES ? stages : MAX_STAGES;
-  p.solo = p.sc_slots && p.sc_slots < CW ? p.sc_slots : CW;
-  p.solo = stages < p.solo ? stages : p.solo;
-  if (p.sc_slots) p.sc_slots -= p.sc_slots % p.solo;
-  p.stages = stages - stages % p.solo;
-  const size_t smem = fixed + (size_t)p.stages * p.stage_bytes;
+cudaError_t run(const FewParams &p, cudaStream_t s) {
+  const size_t smem = (size_t)CW * DEPTH * unit_bytes(FMT) + scratch_bytes(p.T, p.E) + sizeof(Shared);
   auto kern = few_kernel<FMT, TP>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
@@ -1320,21 +1376,26 @@ cudaError_t run(FewParams &p, cudaStream_t s) {
   attr[0].val.cooperative = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = sm_count();
-  cfg.blockDim = THREADS;
+  cfg.blockDim = CT;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
+static_assert((size_t)CW * DEPTH * unit_bytes(Q4) + scratch_bytes(MAX_T, kMaxExperts) + sizeof(Shared) <= (size_t)SMEM_LIMIT,
+              "shared memory");
 
 template <int FMT>
-cudaError_t run_t(FewParams &p, cudaStream_t s) {
+cudaError_t run_t(const FewParams &p, cudaStream_t s) {
   if (p.T <= 1) return run<FMT, 1>(p, s);
   if (p.T <= 4) return run<FMT, 4>(p, s);
   if (p.T <= 8) return run<FMT, 8>(p, s);
   return run<FMT, 16>(p, s);
 }
+
+// parts of K that y has room for: small batches only, where tasks are few
+int k_split(const moe_config &c) { return c.num_tokens * c.top_k <= 32 ? MAX_KSPLIT : 1; }
 
 struct FewLayout {
   size_t logits, xq, xs, h, h_lo, hs, hs_lo, rowmax, hq, y, total;
@@ -1360,43 +1421,14 @@ FewLayout few_layout(const moe_config &c) {
   L.hs_lo = take(2 * T * Fs);
   L.rowmax = take(i8 ? sizeof(unsigned) * S : 0);
   L.hq = take(i8 ? S * F : 0);
-  L.y = take(sizeof(float) * (S + (Fs ? T : 0)) * d);
+  L.y = take(sizeof(float) * (S * k_split(c) + (Fs ? T : 0)) * d);
   L.total = off;
   return L;
 }
 
-// bytes of a row per stage: the longest row if that is short, so that short
-// rows get more stages
-int stage_ch(const moe_config &c) {
-  const long long K = c.hidden > c.intermediate ? c.hidden : c.intermediate;
-  long long b = c.weight_dtype == MOE_BF16 ? 2 * K : (c.weight_dtype == MOE_I8_CHANNEL ? K : K / 2);
-  if (c.shared_intermediate > 0) {
-    const long long s = 2LL * (c.hidden > c.shared_intermediate ? c.hidden : c.shared_intermediate);
-    b = b > s ? b : s;
-  }
-  b = (b + 127) / 128 * 128;
-  return (int)(b < MAX_CH ? b : MAX_CH);
-}
-
-int scale_slot(const moe_config &c) {
-  // 16 rows of K/64 scales and biases, 2 bytes each
-  const int K = c.hidden > c.intermediate ? c.hidden : c.intermediate;
-  return c.weight_dtype == MOE_Q4_AFFINE_G64 ? K / 64 * 2 * 2 * ROWS : 0;
-}
-
-int scale_slots(const moe_config &c) {
-  const int b = scale_slot(c);
-  const int n = b ? SC_BYTES / b : 0;
-  return b == 0 ? 0 : (n < 2 ? 2 : (n > MAX_SC ? MAX_SC : n));
-}
-
 }  // namespace
 
-bool few_supported(const moe_config &c) {
-  if (c.num_tokens > kFewTokens || c.act_dtype != MOE_BF16) return false;
-  // at least three stages beside the scales
-  return sizeof(Shared) + scratch_bytes(c.num_tokens, c.num_experts) + (size_t)scale_slots(c) * scale_slot(c) + 3 * (size_t)(ROWS * (MAX_CH + 64)) <= (size_t)SMEM_LIMIT;
-}
+bool few_supported(const moe_config &c) { return c.num_tokens <= kFewTokens && c.act_dtype == MOE_BF16; }
 
 size_t few_bytes(const moe_config &c) { return few_supported(c) ? few_layout(c).total : 0; }
 
@@ -1448,10 +1480,8 @@ cudaError_t launch_few(const FewArgs &a, cudaStream_t s) {
   p.rowmax = reinterpret_cast<unsigned *>(ws + L.rowmax);
   p.hq = reinterpret_cast<int8_t *>(ws + L.hq);
   p.y = reinterpret_cast<float *>(ws + L.y);
-  p.ch = stage_ch(c);
-  p.stage_bytes = ROWS * (p.ch + 64);
-  p.sc_slot = scale_slot(c);
-  p.sc_slots = scale_slots(c);
+  p.y_rows = c.num_tokens * c.top_k;
+  p.ksplit = k_split(c);
   switch (c.weight_dtype) {
     case MOE_BF16: return run_t<BF16>(p, s);
     case MOE_I8_CHANNEL: return run_t<I8>(p, s);

@@ -740,8 +740,7 @@ moe_status moe_forward_few(const moe_config *cfg, const void *x, const float *w_
   const moe_config &c = *cfg;
   if (!few_supported(c)) {
     set_error("%s%s", c.act_dtype != MOE_BF16 ? "moe_forward_few needs bf16 activations"
-                      : c.num_tokens > kFewTokens ? "moe_forward_few takes at most MOE_FEW_TOKENS tokens"
-                                                  : "moe_forward_few: 4-bit rows too long for its scale buffers");
+                                              : "moe_forward_few takes at most MOE_FEW_TOKENS tokens");
     return MOE_ERR_UNSUPPORTED;
   }
   if (!aligned16(x) || !aligned16(w_router) || !aligned16_or_null(router_bias) || !aligned16(out) ||

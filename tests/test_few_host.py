@@ -31,7 +31,6 @@ def test_few_tokens_constant_matches_header():
 @pytest.mark.parametrize("kw,status,word", [
     (dict(num_tokens=17), L.MOE_ERR_UNSUPPORTED, "MOE_FEW_TOKENS"),
     (dict(act_dtype="f32", weight_dtype="f32"), L.MOE_ERR_UNSUPPORTED, "bf16"),
-    (dict(weight_dtype="q4_affine_g64", hidden=131072), L.MOE_ERR_UNSUPPORTED, "4-bit"),
     (dict(num_experts=512), L.MOE_ERR_UNSUPPORTED, ""),
     (dict(top_k=9), L.MOE_ERR_INVALID_TOPK, ""),
 ])
