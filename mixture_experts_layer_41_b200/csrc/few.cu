@@ -303,31 +303,38 @@ __device__ __forceinline__ void cp_async_wait() {
 struct Feed {
   int part, limit;                          // part fetched from, and the first that is not known yet
   Geo g;
-  int j;                                    // task, from the block's first
+  int j, b;                                 // task, from the block's first, and its row block
   int u, nu;                                // unit of the task, and how many it has here
   int nseg;                                 // segments of the task here
-  int tail;                                 // valid bytes of this lane's piece of the row's last segment: 16 or 0
+  int tail;                                 // bytes of the row from this lane's piece of its last segment on
   bool ends;                                // the span reaches the row's end
+  bool full;                                // whole units, 16 rows: nothing to check
+  bool whole_blocks;                        // every row block has 16 rows
   const char *lo, *hi;                      // this lane's place in rows g and g + 8; null: no such row
-  const char *sc[4];                        // 4-bit: its place in s and b of row g, s and b of row g + 8
+  const char *lo0, *hi0;                    // where the task began
+  const char *sc[4];                        // 4-bit: its place in s and b of row g, s and b of row g + 8 (task's begin)
   int groups;                               // 4-bit: groups of the row from that place on
   uint32_t issued, used;                    // units so far
 };
 
+// The task f.j from scratch
 template <int FMT>
 __device__ __forceinline__ void feed_task(const FewParams &p, const Shared *sh, Feed &f) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const Task t = task_of(f.g, f.g.first + f.j);
   const Span w = warp_span(f.g, t.kp, warp);
   const Src s = task_src(p, f.part, f.part >= R1 ? sh->act[t.i] : 0, t.b, f.g.rb);
+  f.b = t.b;
   f.u = 0;
   f.nseg = w.n;
   f.nu = (w.n + SEGS - 1) / SEGS;
   f.ends = w.first + w.n == f.g.ns;
   f.tail = f.g.rb - (f.g.ns - 1) * SEG - c * 16;
+  f.full = w.n % SEGS == 0 && f.g.rb % SEG == 0 && s.n0 == 8 && s.n1 == 8;
+  f.whole_blocks = f.part == S1 || (f.part == R1 ? p.swiglu || p.F % ROWS == 0 : p.d % ROWS == 0);
   const size_t off = (size_t)w.first * SEG + c * 16;
-  f.lo = g < s.n0 ? s.w0 + (size_t)g * f.g.rb + off : nullptr;
-  f.hi = g < s.n1 ? s.w1 + (size_t)g * f.g.rb + off : nullptr;
+  f.lo = f.lo0 = g < s.n0 ? s.w0 + (size_t)g * f.g.rb + off : nullptr;
+  f.hi = f.hi0 = g < s.n1 ? s.w1 + (size_t)g * f.g.rb + off : nullptr;
   if (FMT == Q4) {
     // groups 2c, 2c + 1 of the unit's eight; words of two groups, from the
     // word that holds the first (a row of an odd number of groups may start
@@ -340,6 +347,26 @@ __device__ __forceinline__ void feed_task(const FewParams &p, const Shared *sh, 
         static_cast<const char *>(f.part == R2 ? p.s3 : p.s2), static_cast<const char *>(f.part == R2 ? p.b3 : p.b2)};
 #pragma unroll
     for (int q = 0; q < 4; ++q) f.sc[q] = base[q] + ((q < 2 ? i0 : i1) & ~(size_t)1) * 2;
+  }
+}
+
+// On to the task f.j, `by` row blocks further: usually the same expert's
+template <int FMT>
+__device__ __forceinline__ void feed_next(const FewParams &p, const Shared *sh, Feed &f, int by) {
+  f.b += by;
+  if (f.b < f.g.nb && f.whole_blocks) {
+    const bool pairs = f.part == S1 || (f.part == R1 && p.swiglu);
+    const int rows = (pairs ? 8 : ROWS) * by;
+    const size_t step = (size_t)rows * f.g.rb;
+    f.u = 0;
+    f.lo = f.lo0 = f.lo0 + step;
+    f.hi = f.hi0 = f.hi0 + step;
+    if (FMT == Q4) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) f.sc[q] += rows * (f.g.rb / 16);      // rb / 32 groups of 2 bytes
+    }
+  } else {
+    feed_task<FMT>(p, sh, f);
   }
 }
 
@@ -376,17 +403,23 @@ __device__ __forceinline__ void feed_step(const FewParams &p, const Shared *sh, 
     const bool q4 = FMT == Q4 && f.part >= R1;
     const uint32_t slot = ring + (f.issued % DEPTH) * unit_bytes(FMT);
     const uint32_t dst = slot + piece_at(q4);
-    const int n = min(SEGS, f.nseg - f.u * SEGS);
-    // (the row's last segment may be short of this lane's piece)
-    const int whole = f.ends && f.u + 1 == f.nu && f.tail <= 0 ? n - 1 : n;
+    if (f.full) {
 #pragma unroll
-    for (int s = 0; s < SEGS; ++s)
-      if (s < whole) {
+      for (int s = 0; s < SEGS; ++s) {
+        cp_async16(dst + s * 1024, f.lo + s * SEG);
+        cp_async16(dst + s * 1024 + 512, f.hi + s * SEG);
+      }
+    } else {
+      const int n = min(SEGS, f.nseg - f.u * SEGS);
+      // (the row's last segment may be short of this lane's piece)
+      const int whole = f.ends && f.u + 1 == f.nu && f.tail <= 0 ? n - 1 : n;
+      for (int s = 0; s < whole; ++s) {
         if (f.lo) cp_async16(dst + s * 1024, f.lo + s * SEG);
         if (f.hi) cp_async16(dst + s * 1024 + 512, f.hi + s * SEG);
       }
-    if (f.lo) f.lo += UNIT;
-    if (f.hi) f.hi += UNIT;
+    }
+    f.lo = f.lo ? f.lo + UNIT : f.lo;
+    f.hi = f.hi ? f.hi + UNIT : f.hi;
     if (q4) {
       const int KG = f.g.rb / 32;
       const int left = f.groups - f.u * 8;  // groups of the row from this lane's first on
@@ -402,10 +435,11 @@ __device__ __forceinline__ void feed_step(const FewParams &p, const Shared *sh, 
     }
     ++f.issued;
     if (++f.u == f.nu) {
-      f.j += f.g.solo ? CW : 1;
+      const int by = f.g.solo ? CW : 1;
+      f.j += by;
       if (f.j < f.g.n) {
-        if (f.part < R1) feed_task<BF16>(p, sh, f);
-        else feed_task<FMT>(p, sh, f);
+        if (FMT == Q4 && f.part >= R1) feed_next<Q4>(p, sh, f, by);
+        else feed_next<BF16>(p, sh, f, by);            // (addresses alone: no format but 4-bit differs)
       } else {
         f = feed_part<FMT>(p, sh, f, f.part + 1);
       }
@@ -698,7 +732,7 @@ __device__ __noinline__ void consume_part(const FewParams &p, Shared *sh, uint8_
   const int stride = SOLO ? CW : 1;
   const int lane_b = c * (FMT == Q4 ? 8 : 16) * R;
 
-  // a task's token rows at this lane and the warp's place in them
+  // a task's token rows at this lane, from the warp's first segment on
   auto enter = [&](int j, Cursor &cu, Span &w, const char *(&rp)[NB]) {
     cu = cursor_of<PART>(p, sh, g, g.first + j);
     w = warp_span(g, cu.kp, warp);
@@ -710,8 +744,11 @@ __device__ __noinline__ void consume_part(const FewParams &p, Shared *sh, uint8_
   if (j < g.n) {
     Cursor cu;
     Span w;
-    const char *rowp[NB];
+    const char *rowp[NB];                   // the task's, and the unit's place in them
     enter(j, cu, w, rowp);
+    const char *bp[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) bp[n] = rowp[n];
     BSeg<FMT, LO> bv[HELD][NBP];
 #pragma unroll
     for (int s = 0; s < HELD; ++s)
@@ -726,66 +763,77 @@ __device__ __noinline__ void consume_part(const FewParams &p, Shared *sh, uint8_
         for (int i = 0; i < 4; ++i) acc.f[n][0][i] = acc.f[n][1][i] = 0;
       const bool second = cu.rows > 8;
       const bool more = j + stride < g.n;
-      // the next task, whose first token operand is fetched during this one's last unit
+      // the next task, whose first token operand is fetched during this one's
+      // last unit: usually the same expert's next rows
       Cursor nc = cu;
-      Span nw{0, 0};
+      Span nw = w;
       const char *nrow[NB];
 #pragma unroll
       for (int n = 0; n < NB; ++n) nrow[n] = rowp[n];
+      nc.b += stride;
+      if (more && nc.b >= g.nb) enter(j + stride, nc, nw, nrow);
       const int nu = (w.n + SEGS - 1) / SEGS;
-      for (int u = 0; u < nu; ++u) {
+      int seg = 0;
+      for (int u = 0; u < nu; ++u, seg += SEGS) {
         const bool last = u + 1 == nu;
-        if (last && more) enter(j + stride, nc, nw, nrow);
-        const int n_seg = min(SEGS, w.n - u * SEGS);
-        const int row_left = g.rb - (w.first + u * SEGS) * SEG;          // bytes of the row from here on
-        // the unit after this one: its segments, their token rows, and what is left of the row there
-        const int next_seg = last ? min(SEGS, nw.n) : min(SEGS, w.n - (u + 1) * SEGS);
-        const int next_left = last ? g.rb - nw.first * SEG : row_left - UNIT;
-        const int here = u * UNIT * R, there = last ? 0 : here + UNIT * R;
+        // the segments of this unit, and of the one after it
+        const int n_seg = w.n - seg, next_seg = last ? (more ? nw.n : 0) : n_seg - SEGS;
+        const char *bn[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) bn[n] = last ? nrow[n] : bp[n] + UNIT * R;
         const uint8_t *slot = ring_ptr + (f.used % DEPTH) * unit_bytes(RFMT);
         cp_async_wait<DEPTH - 1>();
         if (FMT == Q4) __syncwarp();
         const uint8_t *a = FMT == Q4 ? slot + lg * 64 : slot + lane * 16;
         uint32_t sw[4] = {0u, 0u, 0u, 0u};
-        auto step = [&](auto check) {
-          constexpr bool CHECK = decltype(check)::value;
+        auto scales = [&](int s) {
+          const uint4 *t = reinterpret_cast<const uint4 *>(slot + ROWS * UNIT + (lg * 4 + s) * 32);
+          const uint4 x = t[0];
+          sw[0] = x.x; sw[1] = x.y; sw[2] = x.z; sw[3] = x.w;
+          if (odd_groups) {
+            const uint4 y = t[1];
+            sw[0] = __funnelshift_r(x.x, y.x, 16); sw[1] = __funnelshift_r(x.y, y.y, 16);
+            sw[2] = __funnelshift_r(x.z, y.z, 16); sw[3] = __funnelshift_r(x.w, y.w, 16);
+          }
+        };
+        if (even && n_seg >= SEGS && next_seg >= SEGS) {
+          // whole units on both sides: nothing to check
+#pragma unroll
+          for (int s = 0; s < SEGS; ++s) {
+            if constexpr (FMT == Q4) scales(s);
+            consume<FMT, LO, NB, NBP, false>(acc, bv[s % HELD], bp[NB - 1] + s * SEG * R, SEG, a + s * 1024, second, lg, c,
+                                             sw);
+            // the operand of the segment HELD further on takes its registers
+            const int t = s + HELD;
+#pragma unroll
+            for (int n = 0; n < NBP; ++n)
+              load_b<FMT, LO, false>(bv[s % HELD][n], t < SEGS ? bp[n] + t * SEG * R : bn[n] + (t - SEGS) * SEG * R,
+                                     lo_bytes, SEG, c);
+          }
+        } else {
+          const int row_left = g.rb - (w.first + seg) * SEG;             // bytes of the row from here on
+          const int next_left = last ? g.rb - nw.first * SEG : row_left - UNIT;
 #pragma unroll
           for (int s = 0; s < SEGS; ++s) {
             if (s < n_seg) {
-              if constexpr (FMT == Q4) {
-                const uint4 *t = reinterpret_cast<const uint4 *>(slot + ROWS * UNIT + (lg * 4 + s) * 32);
-                const uint4 x = t[0];
-                sw[0] = x.x; sw[1] = x.y; sw[2] = x.z; sw[3] = x.w;
-                if (odd_groups) {
-                  const uint4 y = t[1];
-                  sw[0] = __funnelshift_r(x.x, y.x, 16); sw[1] = __funnelshift_r(x.y, y.y, 16);
-                  sw[2] = __funnelshift_r(x.z, y.z, 16); sw[3] = __funnelshift_r(x.w, y.w, 16);
-                }
-              }
-              consume<FMT, LO, NB, NBP, CHECK>(acc, bv[s % HELD], rowp[NB - 1] + here + s * SEG * R, row_left - s * SEG,
-                                               a + s * 1024, second, lg, c, sw);
+              if constexpr (FMT == Q4) scales(s);
+              consume<FMT, LO, NB, NBP, true>(acc, bv[s % HELD], bp[NB - 1] + s * SEG * R, row_left - s * SEG, a + s * 1024,
+                                              second, lg, c, sw);
             }
-            // the operand of the segment HELD further on takes its registers
             const int t = s + HELD;
-            if (t < SEGS) {
-              if (t < n_seg) {
-#pragma unroll
-                for (int n = 0; n < NBP; ++n)
-                  load_b<FMT, LO, CHECK>(bv[s % HELD][n], rowp[n] + here + t * SEG * R, lo_bytes, row_left - t * SEG, c);
-              }
-            } else if (t - SEGS < next_seg) {
+            if (t < SEGS ? t < n_seg : t - SEGS < next_seg) {
 #pragma unroll
               for (int n = 0; n < NBP; ++n)
-                load_b<FMT, LO, CHECK>(bv[s % HELD][n], (last ? nrow[n] : rowp[n]) + there + (t - SEGS) * SEG * R, lo_bytes,
-                                       next_left - (t - SEGS) * SEG, c);
+                load_b<FMT, LO, true>(bv[s % HELD][n], t < SEGS ? bp[n] + t * SEG * R : bn[n] + (t - SEGS) * SEG * R,
+                                      lo_bytes, (t < SEGS ? row_left : next_left) - (t % SEGS) * SEG, c);
             }
           }
-        };
-        if (even) step(std::false_type{});
-        else step(std::true_type{});
+        }
         if (FMT == Q4) __syncwarp();
         ++f.used;
         feed_step<RFMT>(p, sh, f, ring);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) bp[n] = bn[n];
       }
       if (SOLO) {
         // accumulators 0, 1: row g, tokens 2c, 2c + 1; 2, 3: row g + 8
