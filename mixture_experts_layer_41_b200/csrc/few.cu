@@ -119,7 +119,25 @@ struct FewParams {
 
 __host__ __device__ constexpr size_t scratch_bytes(int T, int E) { return ((size_t)T * E * 8 + 127) / 128 * 128; }
 
+struct Geo {
+  int nb;        // row blocks per expert and part of K
+  int first, n;  // this block's tasks: first .. first + n - 1
+  int rb, ns;    // bytes of a weight row, and its segments
+  int ks;        // parts of K
+  bool solo;     // one task to a warp
+};
+
+// The fetching end of a warp's stream, as far as it changes with tasks only
+struct FeedState {
+  Geo g;
+  int part, limit;                          // part fetched from, and the first that is not known yet
+  int j, b;                                 // task, from the block's first, and its row block
+  int nseg;                                 // segments of the task here
+  int whole_blocks;                         // every row block has 16 rows
+};
+
 struct Shared {
+  FeedState feed[CW];
   int abort_flag;
   int nact;                                 // experts with rows
   uint32_t mask[kMaxExperts];               // tokens an expert keeps
@@ -175,14 +193,6 @@ template <int FMT>
 __device__ __forceinline__ int row_bytes(int K) {
   return FMT == BF16 ? 2 * K : (FMT == I8 ? K : K / 2);
 }
-
-struct Geo {
-  int nb;        // row blocks per expert and part of K
-  int first, n;  // this block's tasks: first .. first + n - 1
-  int rb, ns;    // bytes of a weight row, and its segments
-  int ks;        // parts of K
-  bool solo;     // one task to a warp
-};
 
 // Tasks of the routed down projection are cut along K while a block has few
 // of them: 512 tasks of 28 KB rows on 148 blocks are three or four each, and
@@ -299,166 +309,176 @@ __device__ __forceinline__ void cp_async_wait() {
 // The fetching end of a warp's stream: the next unit to fetch, DEPTH units
 // before the one in use.  Every fetch, and every step at which there is
 // nothing to fetch yet, closes a cp.async group, so the unit in use is always
-// at least DEPTH groups old.
+// at least DEPTH groups old.  What changes with tasks only lies in shared
+// memory (FeedState); the rest is a lane's own.
 struct Feed {
-  int part, limit;                          // part fetched from, and the first that is not known yet
-  Geo g;
-  int j, b;                                 // task, from the block's first, and its row block
-  int u, nu;                                // unit of the task, and how many it has here
-  int nseg;                                 // segments of the task here
-  int tail;                                 // bytes of the row from this lane's piece of its last segment on
-  bool ends;                                // the span reaches the row's end
-  bool full;                                // whole units, 16 rows: nothing to check
-  bool whole_blocks;                        // every row block has 16 rows
-  const char *lo, *hi;                      // this lane's place in rows g and g + 8; null: no such row
-  const char *lo0, *hi0;                    // where the task began
-  const char *sc[4];                        // 4-bit: its place in s and b of row g, s and b of row g + 8 (task's begin)
-  int groups;                               // 4-bit: groups of the row from that place on
+  const char *lo, *hi;                      // this lane's place in rows g and g + 8
+  size_t sc_lo, sc_hi;                      // 4-bit: byte of its scale words of the two rows
+  int left;                                 // units of the task not yet fetched (0: nothing to fetch)
+  int flags;                                // see below
+  int groups;                               // 4-bit: groups of the row from the next unit's place on
   uint32_t issued, used;                    // units so far
 };
+enum FeedFlags { FULL = 1, HAS_LO = 2, HAS_HI = 4, SHORT = 8, ROUTED = 16, DOWN = 32 };
+// FULL: whole units of 16 rows; HAS_LO / HAS_HI: there is such a row; SHORT:
+// the row's last segment, in the task's last unit, ends before this lane's
+// piece; ROUTED: 4-bit rows in a 4-bit kernel; DOWN: of the down projection
 
-// The task f.j from scratch
+// The task st.j from scratch
 template <int FMT>
-__device__ __forceinline__ void feed_task(const FewParams &p, const Shared *sh, Feed &f) {
+__device__ __forceinline__ void feed_task(const FewParams &p, const Shared *sh, FeedState &st, Feed &f) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const Task t = task_of(f.g, f.g.first + f.j);
-  const Span w = warp_span(f.g, t.kp, warp);
-  const Src s = task_src(p, f.part, f.part >= R1 ? sh->act[t.i] : 0, t.b, f.g.rb);
-  f.b = t.b;
-  f.u = 0;
-  f.nseg = w.n;
-  f.nu = (w.n + SEGS - 1) / SEGS;
-  f.ends = w.first + w.n == f.g.ns;
-  f.tail = f.g.rb - (f.g.ns - 1) * SEG - c * 16;
-  f.full = w.n % SEGS == 0 && f.g.rb % SEG == 0 && s.n0 == 8 && s.n1 == 8;
-  f.whole_blocks = f.part == S1 || (f.part == R1 ? p.swiglu || p.F % ROWS == 0 : p.d % ROWS == 0);
+  const Geo &ge = st.g;
+  const Task t = task_of(ge, ge.first + st.j);
+  const Span w = warp_span(ge, t.kp, warp);
+  const Src s = task_src(p, st.part, st.part >= R1 ? sh->act[t.i] : 0, t.b, ge.rb);
+  st.b = t.b;
+  st.nseg = w.n;
+  st.whole_blocks = st.part == S1 || (st.part == R1 ? p.swiglu || p.F % ROWS == 0 : p.d % ROWS == 0);
+  f.left = (w.n + SEGS - 1) / SEGS;
+  const bool ends = w.first + w.n == ge.ns;                 // the span reaches the row's end
+  const int tail = ge.rb - (ge.ns - 1) * SEG - c * 16;      // of the row from this lane's piece of its last segment on
+  f.flags = (w.n % SEGS == 0 && ge.rb % SEG == 0 && s.n0 == 8 && s.n1 == 8 ? FULL : 0) | (g < s.n0 ? HAS_LO : 0) |
+            (g < s.n1 ? HAS_HI : 0) | (ends && tail <= 0 ? SHORT : 0) | (st.part >= R1 ? ROUTED : 0) |
+            (st.part == R2 ? DOWN : 0);
   const size_t off = (size_t)w.first * SEG + c * 16;
-  f.lo = f.lo0 = g < s.n0 ? s.w0 + (size_t)g * f.g.rb + off : nullptr;
-  f.hi = f.hi0 = g < s.n1 ? s.w1 + (size_t)g * f.g.rb + off : nullptr;
+  f.lo = s.w0 + (size_t)g * ge.rb + off;
+  f.hi = s.w1 + (size_t)g * ge.rb + off;
   if (FMT == Q4) {
     // groups 2c, 2c + 1 of the unit's eight; words of two groups, from the
     // word that holds the first (a row of an odd number of groups may start
     // in the middle of one)
-    const int KG = f.g.rb / 32, g0 = w.first * 2 + 2 * c;
+    const int KG = ge.rb / 32, g0 = w.first * 2 + 2 * c;
     f.groups = KG - g0;
-    const size_t i0 = (s.r0 + g) * (size_t)KG + g0, i1 = (s.r1 + g) * (size_t)KG + g0;
-    const char *const base[4] = {
-        static_cast<const char *>(f.part == R2 ? p.s3 : p.s1), static_cast<const char *>(f.part == R2 ? p.b3 : p.b1),
-        static_cast<const char *>(f.part == R2 ? p.s3 : p.s2), static_cast<const char *>(f.part == R2 ? p.b3 : p.b2)};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) f.sc[q] = base[q] + ((q < 2 ? i0 : i1) & ~(size_t)1) * 2;
-  }
-}
-
-// On to the task f.j, `by` row blocks further: usually the same expert's
-template <int FMT>
-__device__ __forceinline__ void feed_next(const FewParams &p, const Shared *sh, Feed &f, int by) {
-  f.b += by;
-  if (f.b < f.g.nb && f.whole_blocks) {
-    const bool pairs = f.part == S1 || (f.part == R1 && p.swiglu);
-    const int rows = (pairs ? 8 : ROWS) * by;
-    const size_t step = (size_t)rows * f.g.rb;
-    f.u = 0;
-    f.lo = f.lo0 = f.lo0 + step;
-    f.hi = f.hi0 = f.hi0 + step;
-    if (FMT == Q4) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) f.sc[q] += rows * (f.g.rb / 16);      // rb / 32 groups of 2 bytes
-    }
-  } else {
-    feed_task<FMT>(p, sh, f);
+    f.sc_lo = (((s.r0 + g) * (size_t)KG + g0) & ~(size_t)1) * 2;
+    f.sc_hi = (((s.r1 + g) * (size_t)KG + g0) & ~(size_t)1) * 2;
   }
 }
 
 // The stream at the first part from `part` on in which this warp has a task.
 // (By value: a reference would keep the caller's copy in memory.)
 template <int FMT>
-__device__ __noinline__ Feed feed_part(const FewParams &p, const Shared *sh, Feed f, int part) {
+__device__ __noinline__ Feed feed_part(const FewParams &p, Shared *sh, Feed f, int part) {
   const int warp = threadIdx.x >> 5;
-  for (; part < f.limit; ++part) {
-    f.g = part < R1 ? part_geo<BF16>(p, part, sh->nact) : part_geo<FMT>(p, part, sh->nact);
-    f.j = f.g.solo ? warp : 0;
-    if (f.j < f.g.n) break;
+  FeedState &st = sh->feed[warp];
+  __syncwarp();
+  FeedState n = st;
+  for (; part < n.limit; ++part) {
+    n.g = part < R1 ? part_geo<BF16>(p, part, sh->nact) : part_geo<FMT>(p, part, sh->nact);
+    n.j = n.g.solo ? warp : 0;
+    if (n.j < n.g.n) break;
   }
-  f.part = part;
-  if (part < f.limit) {
-    if (part < R1) feed_task<BF16>(p, sh, f);
-    else feed_task<FMT>(p, sh, f);
-  }
+  n.part = part;
+  f.left = 0;
+  if (part < n.limit) feed_task<FMT>(p, sh, n, f);
+  __syncwarp();
+  st = n;                                   // (every lane the same)
+  __syncwarp();
   return f;
 }
 
-// 4-bit pieces: lane (g, c) keeps its 16 bytes so that the eight bytes that
-// the lanes of four rows read at once lie in different banks
-__device__ __forceinline__ uint32_t piece_at(bool q4) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  return q4 ? g * 64 + ((c ^ (g & 2)) << 4) : lane * 16;
+// On to the warp's next task: usually the same expert's next row block.
+template <int FMT>
+__device__ __noinline__ Feed feed_next(const FewParams &p, Shared *sh, Feed f) {
+  FeedState &st = sh->feed[threadIdx.x >> 5];
+  __syncwarp();
+  FeedState n = st;
+  const int by = n.g.solo ? CW : 1;
+  n.j += by;
+  n.b += by;
+  if (n.j >= n.g.n) return feed_part<FMT>(p, sh, f, n.part + 1);
+  if (n.b < n.g.nb && n.whole_blocks) {
+    const int nu = (n.nseg + SEGS - 1) / SEGS;
+    const bool pairs = n.part == S1 || (n.part == R1 && p.swiglu);
+    const int rows = (pairs ? 8 : ROWS) * by;
+    const ptrdiff_t step = (ptrdiff_t)rows * n.g.rb - (ptrdiff_t)nu * UNIT;
+    f.lo += step;
+    f.hi += step;
+    f.left = nu;
+    if (FMT == Q4) {                        // rb / 32 groups of 2 bytes a row, 8 groups a unit
+      const ptrdiff_t sc = (ptrdiff_t)rows * (n.g.rb / 16) - (ptrdiff_t)nu * 16;
+      f.sc_lo += sc;
+      f.sc_hi += sc;
+      f.groups += nu * 8;
+    }
+  } else {
+    feed_task<FMT>(p, sh, n, f);
+  }
+  __syncwarp();
+  st = n;
+  __syncwarp();
+  return f;
 }
 
 // Fetches the next unit (if there is one yet) and closes its group.
 template <int FMT>
-__device__ __forceinline__ void feed_step(const FewParams &p, const Shared *sh, Feed &f, uint32_t ring) {
-  if (f.part < f.limit) {
-    const int lane = threadIdx.x & 31;
-    const bool q4 = FMT == Q4 && f.part >= R1;
+__device__ __forceinline__ void feed_step(const FewParams &p, Shared *sh, Feed &f, uint32_t ring) {
+  if (f.left > 0) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const bool q4 = FMT == Q4;              // (a 4-bit layer has no shared expert)
     const uint32_t slot = ring + (f.issued % DEPTH) * unit_bytes(FMT);
-    const uint32_t dst = slot + piece_at(q4);
-    if (f.full) {
+    // 4-bit pieces: lane (g, c) keeps its 16 bytes so that the eight bytes that
+    // the lanes of four rows read at once lie in different banks
+    const uint32_t dst = slot + (q4 ? g * 64 + ((c ^ (g & 2)) << 4) : lane * 16);
+    if (f.flags & FULL) {
 #pragma unroll
       for (int s = 0; s < SEGS; ++s) {
         cp_async16(dst + s * 1024, f.lo + s * SEG);
         cp_async16(dst + s * 1024 + 512, f.hi + s * SEG);
       }
     } else {
-      const int n = min(SEGS, f.nseg - f.u * SEGS);
-      // (the row's last segment may be short of this lane's piece)
-      const int whole = f.ends && f.u + 1 == f.nu && f.tail <= 0 ? n - 1 : n;
-      for (int s = 0; s < whole; ++s) {
-        if (f.lo) cp_async16(dst + s * 1024, f.lo + s * SEG);
-        if (f.hi) cp_async16(dst + s * 1024 + 512, f.hi + s * SEG);
+      int n = SEGS;
+      if (f.left == 1) {
+        const int rest = sh->feed[threadIdx.x >> 5].nseg % SEGS;
+        n = (rest ? rest : SEGS) - (f.flags & SHORT ? 1 : 0);
+      }
+#pragma unroll 1
+      for (int s = 0; s < n; ++s) {
+        if (f.flags & HAS_LO) cp_async16(dst + s * 1024, f.lo + s * SEG);
+        if (f.flags & HAS_HI) cp_async16(dst + s * 1024 + 512, f.hi + s * SEG);
       }
     }
-    f.lo = f.lo ? f.lo + UNIT : f.lo;
-    f.hi = f.hi ? f.hi + UNIT : f.hi;
+    f.lo += UNIT;
+    f.hi += UNIT;
     if (q4) {
-      const int KG = f.g.rb / 32;
-      const int left = f.groups - f.u * 8;  // groups of the row from this lane's first on
-      const bool odd = (KG & 1) && ((lane >> 2) & 1);     // the first group is the high half of its word
+      // a row of an odd number of groups: row g's first is the high half of its word
+      const bool odd = (sh->feed[threadIdx.x >> 5].g.rb / 32 & 1) && (g & 1);
       const uint32_t d = slot + ROWS * UNIT + lane * 32;
-      if (left > 0) {
+      if (f.groups > 0) {
+        const bool down = f.flags & DOWN;
+        const char *const base[4] = {
+            static_cast<const char *>(down ? p.s3 : p.s1) + f.sc_lo, static_cast<const char *>(down ? p.b3 : p.b1) + f.sc_lo,
+            static_cast<const char *>(down ? p.s3 : p.s2) + f.sc_hi, static_cast<const char *>(down ? p.b3 : p.b2) + f.sc_hi};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          cp_async4(d + q * 4, f.sc[q] + f.u * 16);
-          if (odd && left > 1) cp_async4(d + 16 + q * 4, f.sc[q] + f.u * 16 + 4);
+          cp_async4(d + q * 4, base[q]);
+          if (odd && f.groups > 1) cp_async4(d + 16 + q * 4, base[q] + 4);
         }
       }
+      f.sc_lo += 16;
+      f.sc_hi += 16;
+      f.groups -= 8;
     }
     ++f.issued;
-    if (++f.u == f.nu) {
-      const int by = f.g.solo ? CW : 1;
-      f.j += by;
-      if (f.j < f.g.n) {
-        if (FMT == Q4 && f.part >= R1) feed_next<Q4>(p, sh, f, by);
-        else feed_next<BF16>(p, sh, f, by);            // (addresses alone: no format but 4-bit differs)
-      } else {
-        f = feed_part<FMT>(p, sh, f, f.part + 1);
-      }
-    }
+    if (--f.left == 0) f = feed_next<FMT>(p, sh, f);
   }
   cp_async_commit();
 }
 
 // Lets the stream go on into parts before `limit`, and fills it up.
 template <int FMT>
-__device__ __noinline__ void feed_open(const FewParams &p, const Shared *sh, Feed &feed, uint32_t ring, int limit) {
-  Feed f = feed;
-  const int from = f.part;
-  const bool stopped = f.part >= f.limit;
-  f.limit = limit;
-  if (stopped) f = feed_part<FMT>(p, sh, f, from);
+__device__ __noinline__ Feed feed_open(const FewParams &p, Shared *sh, Feed f, uint32_t ring, int limit) {
+  FeedState &st = sh->feed[threadIdx.x >> 5];
   __syncwarp();
+  const int from = st.part;
+  const bool stopped = from >= st.limit;
+  __syncwarp();
+  st.limit = limit;
+  __syncwarp();
+  if (stopped) f = feed_part<FMT>(p, sh, f, from);
+#pragma unroll 1
   for (uint32_t i = f.issued - f.used; i < DEPTH; ++i) feed_step<FMT>(p, sh, f, ring);
-  feed = f;
+  return f;
 }
 
 // ---------------------------------------------------------------- products
@@ -635,13 +655,12 @@ struct Cursor {
   uint32_t mask;
 };
 
-template <int PART>
-__device__ __forceinline__ Cursor cursor_of(const FewParams &p, const Shared *sh, const Geo &g, int task) {
+__device__ __forceinline__ Cursor cursor_of(const FewParams &p, const Shared *sh, const Geo &g, int part, int task) {
   Cursor cu;
   const Task t = task_of(g, task);
   cu.kp = t.kp;
   cu.b = t.b;
-  if (PART == S1 || PART == S2) {
+  if (part < R1) {
     cu.e = 0;
     cu.mask = (1u << p.T) - 1u;
     cu.row0 = 0;
@@ -657,15 +676,15 @@ __device__ __forceinline__ Cursor cursor_of(const FewParams &p, const Shared *sh
 
 // Row r of a task's token operand.  A row past the task's last repeats the
 // last: each token is a column of its own, and those columns are not stored.
-template <int FMT, int PART>
-__device__ __forceinline__ const char *b_row(const FewParams &p, const Cursor &cu, int r) {
+template <int FMT, bool PHASE2>
+__device__ __forceinline__ const char *b_row(const FewParams &p, const Cursor &cu, int part, int r) {
   r = min(r, cu.rows - 1);
-  if (PART == S1 || PART == R1) {
-    const int t = PART == S1 ? r : nth_bit(cu.mask, r);
+  if (!PHASE2) {
+    const int t = part == S1 ? r : nth_bit(cu.mask, r);
     return FMT == I8 ? reinterpret_cast<const char *>(p.xq + (size_t)t * p.d)
                      : reinterpret_cast<const char *>(p.x + (size_t)t * p.d);
   }
-  if (PART == S2) return reinterpret_cast<const char *>(p.hs + (size_t)r * p.Fs);
+  if (part == S2) return reinterpret_cast<const char *>(p.hs + (size_t)r * p.Fs);
   return FMT == I8 ? reinterpret_cast<const char *>(p.hq + (size_t)(cu.row0 + r) * p.F)
                    : reinterpret_cast<const char *>(p.h + (size_t)(cu.row0 + r) * p.F);
 }
@@ -673,12 +692,11 @@ __device__ __forceinline__ const char *b_row(const FewParams &p, const Cursor &c
 // What becomes of one finished value: row f of the task's `cols` (with its up
 // projection u where the task holds pairs), token tok.  Returns the magnitude
 // of the stored bf16 h (8-bit weights: the row maxima are taken from it).
-template <int FMT, int PART>
-__device__ __forceinline__ float emit(const FewParams &p, const Cursor &cu, int f, int tok, float v, float u) {
-  constexpr bool PHASE2 = PART == S2 || PART == R2;
-  const bool pairs = PART == S1 || (PART == R1 && p.swiglu);
+template <int FMT, bool PHASE2>
+__device__ __forceinline__ float emit(const FewParams &p, const Cursor &cu, int part, bool pairs, int f, int tok, float v,
+                                      float u) {
   const int col = cu.b * (pairs ? 8 : ROWS) + f;
-  const int N = PART == S1 ? p.Fs : (PART == R1 ? p.F : p.d);
+  const int N = PHASE2 ? p.d : (part == S1 ? p.Fs : p.F);
   if (tok >= cu.rows || col >= N) return 0.f;
   const size_t row = (size_t)cu.row0 + tok;
   if (FMT == I8) {
@@ -695,52 +713,52 @@ __device__ __forceinline__ float emit(const FewParams &p, const Cursor &cu, int 
     if (pairs) u *= xs * __ldg(static_cast<const float *>(p.s2) + r0);
   }
   if (PHASE2) {
-    p.y[(PART == S2 ? (size_t)p.ksplit * p.y_rows + tok : (size_t)cu.kp * p.y_rows + row) * p.d + col] = v;
+    p.y[(part == S2 ? (size_t)p.ksplit * p.y_rows + tok : (size_t)cu.kp * p.y_rows + row) * p.d + col] = v;
     return 0.f;
   }
   if (pairs) v = silu_f(v) * u;
   else v = v < 0.f ? 0.f : v;               // a NaN stays one
   const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-  uint16_t *h = PART == S1 ? p.hs + (size_t)tok * p.Fs + col : p.h + row * p.F + col;
+  uint16_t *h = part == S1 ? p.hs + (size_t)tok * p.Fs + col : p.h + row * p.F + col;
   *h = *reinterpret_cast<const uint16_t *>(&hi);
   if (FMT == BF16) {
     const float rest = v - __bfloat162float(hi);
     const __nv_bfloat16 lo = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
-    h[PART == S1 ? p.hs_lo : p.h_lo] = *reinterpret_cast<const uint16_t *>(&lo);
+    h[part == S1 ? p.hs_lo : p.h_lo] = *reinterpret_cast<const uint16_t *>(&lo);
   }
   return __bfloat162float(hi);
 }
 
-// The block's tasks of one part.  RFMT: the routed experts' format, which the
-// stream may go on to.
-template <int FMT, int RFMT, int PART, int NB, bool SOLO>
-__device__ __noinline__ void consume_part(const FewParams &p, Shared *sh, uint8_t *ring_ptr, Feed &feed, uint32_t &red_it,
-                                          const Geo &geo) {
-  constexpr bool PHASE2 = PART == S2 || PART == R2;
+// The block's tasks of one part (of phase 1 or 2).  RFMT: the routed experts'
+// format, which the stream may go on to.
+template <int FMT, int RFMT, bool PHASE2, int NB>
+__device__ __noinline__ Feed consume_part(const FewParams &p, Shared *sh, uint8_t *ring_ptr, Feed f, uint32_t &red_it_ref,
+                                          int part) {
+  uint32_t red_it = red_it_ref;
   constexpr bool LO = PHASE2 && FMT == BF16;
   constexpr int NBP = FMT == Q4 ? 1 : NB;   // blocks of eight tokens whose operand is fetched ahead
   constexpr int R = ratio_of<FMT>();
   constexpr int HELD = held_of<FMT>();
-  const Geo g = geo;
-  Feed f = feed;
+  const Geo g = part_geo<FMT>(p, part, sh->nact);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, c = lane & 3;
   const uint32_t ring = smem_u32(ring_ptr);
-  const size_t lo_bytes = 2 * (PART == S2 ? p.hs_lo : p.h_lo);
+  const size_t lo_bytes = 2 * (part == S2 ? p.hs_lo : p.h_lo);
   const bool even = g.rb % SEG == 0;        // whole segments only
   const bool odd_groups = FMT == Q4 && (g.rb / 32 & 1) && (lg & 1);
-  const bool pairs = PART == S1 || (PART == R1 && p.swiglu);
-  const int stride = SOLO ? CW : 1;
+  const bool pairs = !PHASE2 && (part == S1 || p.swiglu);
+  const bool top_of_h = FMT == I8 && part == R1;
+  const int stride = g.solo ? CW : 1;
   const int lane_b = c * (FMT == Q4 ? 8 : 16) * R;
 
   // a task's token rows at this lane, from the warp's first segment on
   auto enter = [&](int j, Cursor &cu, Span &w, const char *(&rp)[NB]) {
-    cu = cursor_of<PART>(p, sh, g, g.first + j);
+    cu = cursor_of(p, sh, g, part, g.first + j);
     w = warp_span(g, cu.kp, warp);
 #pragma unroll
-    for (int n = 0; n < NB; ++n) rp[n] = b_row<FMT, PART>(p, cu, lg + 8 * n) + lane_b + (size_t)w.first * SEG * R;
+    for (int n = 0; n < NB; ++n) rp[n] = b_row<FMT, PHASE2>(p, cu, part, lg + 8 * n) + lane_b + (size_t)w.first * SEG * R;
   };
 
-  int j = SOLO ? warp : 0;
+  int j = g.solo ? warp : 0;
   if (j < g.n) {
     Cursor cu;
     Span w;
@@ -835,7 +853,7 @@ __device__ __noinline__ void consume_part(const FewParams &p, Shared *sh, uint8_
 #pragma unroll
         for (int n = 0; n < NB; ++n) bp[n] = bn[n];
       }
-      if (SOLO) {
+      if (g.solo) {
         // accumulators 0, 1: row g, tokens 2c, 2c + 1; 2, 3: row g + 8
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
@@ -845,9 +863,9 @@ __device__ __noinline__ void consume_part(const FewParams &p, Shared *sh, uint8_
             const int tok = 8 * n + 2 * c + i;
             const float v0 = (float)(acc.f[n][0][i] + acc.f[n][1][i]);
             const float v1 = (float)(acc.f[n][0][i + 2] + acc.f[n][1][i + 2]);
-            float m = emit<FMT, PART>(p, cu, lg, tok, v0, v1);
-            if (!pairs) m = abs_max(m, emit<FMT, PART>(p, cu, lg + 8, tok, v1, 0.f));
-            if (FMT == I8 && PART == R1) {
+            float m = emit<FMT, PHASE2>(p, cu, part, pairs, lg, tok, v0, v1);
+            if (!pairs) m = abs_max(m, emit<FMT, PHASE2>(p, cu, part, pairs, lg + 8, tok, v1, 0.f));
+            if (top_of_h) {
               uint32_t top = __float_as_uint(m) & 0x7FFFFFFFu;
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -890,10 +908,10 @@ __device__ __noinline__ void consume_part(const FewParams &p, Shared *sh, uint8_
         const int most = cols * 8 * (second ? 2 : 1);
         // (whole warps, other ones from task to task: the scales they fetch are not waited for by all)
         for (int i = (threadIdx.x + 64 * red_it) % CT; i < most; i += CT) {
-          const int tok = i / cols, q = i - tok * cols;
+          const int tok = i >> (pairs ? 3 : 4), q = i & (cols - 1);
           const float m =
-              tok < cu.rows ? emit<FMT, PART>(p, cu, q, tok, total(q, tok), pairs ? total(q + 8, tok) : 0.f) : 0.f;
-          if (FMT == I8 && PART == R1) {
+              tok < cu.rows ? emit<FMT, PHASE2>(p, cu, part, pairs, q, tok, total(q, tok), pairs ? total(q + 8, tok) : 0.f) : 0.f;
+          if (top_of_h) {
             // the row's largest |h|: over the task's columns (8 or 16 neighbouring lanes), then the grid
             uint32_t top = __float_as_uint(m) & 0x7FFFFFFFu;
             for (int o = 1; o < cols; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -909,14 +927,8 @@ __device__ __noinline__ void consume_part(const FewParams &p, Shared *sh, uint8_
       for (int n = 0; n < NB; ++n) rowp[n] = nrow[n];
     }
   }
-  feed = f;
-}
-
-template <int FMT, int RFMT, int PART, int NB>
-__device__ __forceinline__ void run_part(const FewParams &p, Shared *sh, uint8_t *ring, Feed &feed, uint32_t &red_it) {
-  const Geo g = part_geo<FMT>(p, PART, sh->nact);
-  if (g.solo) consume_part<FMT, RFMT, PART, NB, true>(p, sh, ring, feed, red_it, g);
-  else consume_part<FMT, RFMT, PART, NB, false>(p, sh, ring, feed, red_it, g);
+  red_it_ref = red_it;
+  return f;
 }
 
 // ---------------------------------------------------------------- router
@@ -1377,25 +1389,28 @@ __global__ void __launch_bounds__(CT, 1) few_kernel(const __grid_constant__ FewP
     sh->nact = 0;
     if (blockIdx.x == 0) *p.dropped = 0;
   }
+  if ((threadIdx.x & 31) == 0) {
+    FeedState &st = sh->feed[threadIdx.x >> 5];
+    st.part = st.limit = p.Fs ? S1 : R1;
+  }
   sh->bias[threadIdx.x] = p.bias && threadIdx.x < p.E ? __ldg(p.bias + threadIdx.x) : 0.f;
   __syncthreads();
   Feed feed{};
   uint32_t red_it = 0;
-  if (p.Fs) feed_open<FMT>(p, sh, feed, ring, R1);
-  else feed.part = feed.limit = R1;
+  if (p.Fs) feed = feed_open<FMT>(p, sh, feed, ring, R1);
   if (FMT == I8) {
     quantize_x(p, sh);
     if (blockIdx.x == 0)
       for (int i = threadIdx.x; i < p.T * p.k; i += CT) p.rowmax[i] = 0u;
   }
   route_logits<TP>(p, sh);
-  if (p.Fs) run_part<BF16, FMT, S1, NB>(p, sh, ring_ptr, feed, red_it);
+  if (p.Fs) feed = consume_part<BF16, FMT, false, NB>(p, sh, ring_ptr, feed, red_it, S1);
   grid_arrive(p.bar);
   grid_wait(p.bar, abort_flag, p);
   make_plan(p, sh, prob);
-  feed_open<FMT>(p, sh, feed, ring, END);
-  if (p.Fs) run_part<BF16, FMT, S2, NB>(p, sh, ring_ptr, feed, red_it);
-  run_part<FMT, FMT, R1, NB>(p, sh, ring_ptr, feed, red_it);
+  feed = feed_open<FMT>(p, sh, feed, ring, END);
+  if (p.Fs) feed = consume_part<BF16, FMT, true, NB>(p, sh, ring_ptr, feed, red_it, S2);
+  feed = consume_part<FMT, FMT, false, NB>(p, sh, ring_ptr, feed, red_it, R1);
   grid_arrive(p.bar + 8);
   grid_wait(p.bar + 8, abort_flag, p);
   if (FMT == I8) {
@@ -1403,7 +1418,7 @@ __global__ void __launch_bounds__(CT, 1) few_kernel(const __grid_constant__ FewP
     grid_arrive(p.bar + 16);
     grid_wait(p.bar + 16, abort_flag, p);
   }
-  run_part<FMT, FMT, R2, NB>(p, sh, ring_ptr, feed, red_it);
+  feed = consume_part<FMT, FMT, true, NB>(p, sh, ring_ptr, feed, red_it, R2);
   grid_arrive(p.bar + 24);
   if (blockIdx.x == 0) write_choice(p, sh, prob);
   slot_rows(p, sh);
