@@ -320,7 +320,7 @@ struct Feed {
   uint32_t issued, used;                    // units so far
 };
 enum FeedFlags { FULL = 1, HAS_LO = 2, HAS_HI = 4, SHORT = 8, ROUTED = 16, DOWN = 32 };
-// FULL: whole units of 16 rows; HAS_LO / HAS_HI: there is such a row; SHORT:
+// FULL: 16 rows of whole segments; HAS_LO / HAS_HI: there is such a row; SHORT:
 // the row's last segment, in the task's last unit, ends before this lane's
 // piece; ROUTED: 4-bit rows in a 4-bit kernel; DOWN: of the down projection
 
@@ -338,7 +338,7 @@ __device__ __forceinline__ void feed_task(const FewParams &p, const Shared *sh, 
   f.left = (w.n + SEGS - 1) / SEGS;
   const bool ends = w.first + w.n == ge.ns;                 // the span reaches the row's end
   const int tail = ge.rb - (ge.ns - 1) * SEG - c * 16;      // of the row from this lane's piece of its last segment on
-  f.flags = (w.n % SEGS == 0 && ge.rb % SEG == 0 && s.n0 == 8 && s.n1 == 8 ? FULL : 0) | (g < s.n0 ? HAS_LO : 0) |
+  f.flags = (ge.rb % SEG == 0 && s.n0 == 8 && s.n1 == 8 ? FULL : 0) | (g < s.n0 ? HAS_LO : 0) |
             (g < s.n1 ? HAS_HI : 0) | (ends && tail <= 0 ? SHORT : 0) | (st.part >= R1 ? ROUTED : 0) |
             (st.part == R2 ? DOWN : 0);
   const size_t off = (size_t)w.first * SEG + c * 16;
@@ -420,18 +420,15 @@ __device__ __forceinline__ void feed_step(const FewParams &p, Shared *sh, Feed &
     // 4-bit pieces: lane (g, c) keeps its 16 bytes so that the eight bytes that
     // the lanes of four rows read at once lie in different banks
     const uint32_t dst = slot + (q4 ? g * 64 + ((c ^ (g & 2)) << 4) : lane * 16);
-    if (f.flags & FULL) {
+    const int rest = f.left == 1 ? sh->feed[threadIdx.x >> 5].nseg % SEGS : 0;      // of the task's last unit
+    if ((f.flags & FULL) && rest == 0) {
 #pragma unroll
       for (int s = 0; s < SEGS; ++s) {
         cp_async16(dst + s * 1024, f.lo + s * SEG);
         cp_async16(dst + s * 1024 + 512, f.hi + s * SEG);
       }
     } else {
-      int n = SEGS;
-      if (f.left == 1) {
-        const int rest = sh->feed[threadIdx.x >> 5].nseg % SEGS;
-        n = (rest ? rest : SEGS) - (f.flags & SHORT ? 1 : 0);
-      }
+      const int n = (rest ? rest : SEGS) - (f.left == 1 && (f.flags & SHORT) ? 1 : 0);
 #pragma unroll 1
       for (int s = 0; s < n; ++s) {
         if (f.flags & HAS_LO) cp_async16(dst + s * 1024, f.lo + s * SEG);
@@ -527,10 +524,12 @@ template <int FMT>
 __host__ __device__ constexpr int ratio_of() {
   return FMT == Q4 ? 4 : 1;
 }
-// segments whose token operand a warp holds at once (4-bit: four times the registers each)
+// segments whose token operand a warp holds at once (4-bit: four times the
+// registers each, and a body of a few hundred instructions per segment, which
+// stays in the instruction cache only if it is a loop's)
 template <int FMT>
 __host__ __device__ constexpr int held_of() {
-  return FMT == Q4 ? 2 : 4;
+  return FMT == Q4 ? 1 : SEGS;
 }
 
 // B operand of one segment.  bf16 and 8-bit: 16 bytes of the token row (and of
@@ -814,37 +813,39 @@ __device__ __noinline__ Feed consume_part(const FewParams &p, Shared *sh, uint8_
             sw[2] = __funnelshift_r(x.z, y.z, 16); sw[3] = __funnelshift_r(x.w, y.w, 16);
           }
         };
-        if (even && n_seg >= SEGS && next_seg >= SEGS) {
-          // whole units on both sides: nothing to check
-#pragma unroll
-          for (int s = 0; s < SEGS; ++s) {
+        const int row_left = g.rb - (w.first + seg) * SEG;               // bytes of the row from here on
+        const int next_left = last ? g.rb - nw.first * SEG : row_left - UNIT;
+        auto step = [&](int s, auto check) {
+          constexpr bool CHECK = decltype(check)::value;
+          if (s < n_seg) {
             if constexpr (FMT == Q4) scales(s);
-            consume<FMT, LO, NB, NBP, false>(acc, bv[s % HELD], bp[NB - 1] + s * SEG * R, SEG, a + s * 1024, second, lg, c,
-                                             sw);
-            // the operand of the segment HELD further on takes its registers
-            const int t = s + HELD;
+            consume<FMT, LO, NB, NBP, CHECK>(acc, bv[s % HELD], bp[NB - 1] + s * SEG * R, row_left - s * SEG, a + s * 1024,
+                                             second, lg, c, sw);
+          }
+          // the operand of the segment HELD further on takes its registers
+          const int t = s + HELD;
+          if (t < SEGS ? t < n_seg : t - SEGS < next_seg) {
 #pragma unroll
             for (int n = 0; n < NBP; ++n)
-              load_b<FMT, LO, false>(bv[s % HELD][n], t < SEGS ? bp[n] + t * SEG * R : bn[n] + (t - SEGS) * SEG * R,
-                                     lo_bytes, SEG, c);
+              load_b<FMT, LO, CHECK>(bv[s % HELD][n], t < SEGS ? bp[n] + t * SEG * R : bn[n] + (t - SEGS) * SEG * R, lo_bytes,
+                                     (t < SEGS ? row_left : next_left) - (t % SEGS) * SEG, c);
+          }
+        };
+        if (even) {
+          if constexpr (FMT == Q4) {
+#pragma unroll 1
+            for (int s = 0; s < SEGS; ++s) step(s, std::false_type{});
+          } else {
+#pragma unroll
+            for (int s = 0; s < SEGS; ++s) step(s, std::false_type{});
           }
         } else {
-          const int row_left = g.rb - (w.first + seg) * SEG;             // bytes of the row from here on
-          const int next_left = last ? g.rb - nw.first * SEG : row_left - UNIT;
+          if constexpr (FMT == Q4) {
+#pragma unroll 1
+            for (int s = 0; s < SEGS; ++s) step(s, std::true_type{});
+          } else {
 #pragma unroll
-          for (int s = 0; s < SEGS; ++s) {
-            if (s < n_seg) {
-              if constexpr (FMT == Q4) scales(s);
-              consume<FMT, LO, NB, NBP, true>(acc, bv[s % HELD], bp[NB - 1] + s * SEG * R, row_left - s * SEG, a + s * 1024,
-                                              second, lg, c, sw);
-            }
-            const int t = s + HELD;
-            if (t < SEGS ? t < n_seg : t - SEGS < next_seg) {
-#pragma unroll
-              for (int n = 0; n < NBP; ++n)
-                load_b<FMT, LO, true>(bv[s % HELD][n], t < SEGS ? bp[n] + t * SEG * R : bn[n] + (t - SEGS) * SEG * R,
-                                      lo_bytes, (t < SEGS ? row_left : next_left) - (t % SEGS) * SEG, c);
-            }
+            for (int s = 0; s < SEGS; ++s) step(s, std::true_type{});
           }
         }
         if (FMT == Q4) __syncwarp();
