@@ -20,7 +20,7 @@
 // The shared expert needs no choice: its phase 1 runs beside the router, its
 // phase 2 before the routed experts'.
 //
-// How the weights move.  Each of a block's eight warps walks its own units, 16
+// How the weights move.  Each of a block's sixteen warps walks its own units, 16
 // rows x 256 bytes, and each lane fetches with cp.async the 16-byte pieces
 // that it will multiply itself, DEPTH units ahead, into slots of its own: there
 // is nobody to hand over to, so the stream has no barriers, and it runs on
@@ -63,13 +63,12 @@ namespace {
 
 using namespace ptx;
 
-constexpr int CW = 8;                       // warps
+constexpr int CW = 16;                      // warps
 constexpr int CT = 32 * CW;
 constexpr int ROWS = 16;                    // weight rows per task
 constexpr int UNIT = 256;                   // bytes of a row per unit
 constexpr int SEG = 64;                     // and per product step: 16 bytes for each lane of a quad
 constexpr int SEGS = UNIT / SEG;
-constexpr int DEPTH = 4;                    // units in flight per warp
 constexpr int SOLO_BYTES = 2048;            // rows of at most that many bytes go one task to a warp
 constexpr int MAX_KSPLIT = 4;               // parts of K a down-projection task may be cut into
 constexpr int MAX_T = kFewTokens;
@@ -78,6 +77,8 @@ constexpr int SMEM_LIMIT = 227 * 1024;
 
 enum Fmt { BF16 = 0, I8 = 1, Q4 = 2 };
 
+// units in flight per warp
+__host__ __device__ constexpr int depth_of(int fmt, int TP) { return fmt != 2 && TP <= 4 ? 3 : 2; }
 // shared memory of one unit: the lanes' pieces, and 32 bytes of scales and biases per lane
 __host__ __device__ constexpr int unit_bytes(int fmt) { return ROWS * UNIT + (fmt == Q4 ? 32 * 32 : 0); }
 
@@ -136,7 +137,7 @@ struct FeedState {
   int whole_blocks;                         // every row block has 16 rows
 };
 
-struct Shared {
+struct __align__(16) Shared {
   FeedState feed[CW];
   int abort_flag;
   int nact;                                 // experts with rows
@@ -149,9 +150,16 @@ struct Shared {
   float bias[kMaxExperts];                  // the router's, zeros without one
   uint8_t raw[kMaxExperts];                 // tokens that chose an expert
   int warp_n[CW], warp_rows[CW];            // per 32 experts: how many have rows, and the rows
-  // partial results of the warps, two tasks in turn; scratch of the router and the choice
-  __align__(16) uint32_t red[2][CW][2][32][4];
 };
+// Behind it: partial results of the warps, two tasks in turn; scratch of the
+// router and the choice (a row of 256 keys for each token)
+template <int NB>
+struct Partial {
+  __align__(16) uint32_t red[2][CW][NB][32][4];
+};
+__device__ __forceinline__ uint32_t *partials(const Shared *sh) {
+  return reinterpret_cast<uint32_t *>(const_cast<Shared *>(sh) + 1);
+}
 
 // ---------------------------------------------------------------- grid barrier
 // Arrival and wait are apart, so work that does not depend on the other blocks
@@ -411,7 +419,7 @@ __device__ __noinline__ Feed feed_next(const FewParams &p, Shared *sh, Feed f) {
 }
 
 // Fetches the next unit (if there is one yet) and closes its group.
-template <int FMT>
+template <int FMT, int DEPTH>
 __device__ __forceinline__ void feed_step(const FewParams &p, Shared *sh, Feed &f, uint32_t ring) {
   if (f.left > 0) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -463,7 +471,7 @@ __device__ __forceinline__ void feed_step(const FewParams &p, Shared *sh, Feed &
 }
 
 // Lets the stream go on into parts before `limit`, and fills it up.
-template <int FMT>
+template <int FMT, int DEPTH>
 __device__ __noinline__ Feed feed_open(const FewParams &p, Shared *sh, Feed f, uint32_t ring, int limit) {
   FeedState &st = sh->feed[threadIdx.x >> 5];
   __syncwarp();
@@ -474,7 +482,7 @@ __device__ __noinline__ Feed feed_open(const FewParams &p, Shared *sh, Feed f, u
   __syncwarp();
   if (stopped) f = feed_part<FMT>(p, sh, f, from);
 #pragma unroll 1
-  for (uint32_t i = f.issued - f.used; i < DEPTH; ++i) feed_step<FMT>(p, sh, f, ring);
+  for (uint32_t i = f.issued - f.used; i < DEPTH; ++i) feed_step<FMT, DEPTH>(p, sh, f, ring);
   return f;
 }
 
@@ -528,8 +536,8 @@ __host__ __device__ constexpr int ratio_of() {
 // registers each, and a body of a few hundred instructions per segment, which
 // stays in the instruction cache only if it is a loop's)
 template <int FMT>
-__host__ __device__ constexpr int held_of() {
-  return FMT == Q4 ? 1 : SEGS;
+__host__ __device__ constexpr int held_of(bool lo, int NB) {
+  return FMT == Q4 ? 1 : (lo || NB > 1 ? SEGS / 2 : SEGS);
 }
 
 // B operand of one segment.  bf16 and 8-bit: 16 bytes of the token row (and of
@@ -730,14 +738,14 @@ __device__ __forceinline__ float emit(const FewParams &p, const Cursor &cu, int 
 
 // The block's tasks of one part (of phase 1 or 2).  RFMT: the routed experts'
 // format, which the stream may go on to.
-template <int FMT, int RFMT, bool PHASE2, int NB>
+template <int FMT, int RFMT, bool PHASE2, int NB, int DEPTH>
 __device__ __noinline__ Feed consume_part(const FewParams &p, Shared *sh, uint8_t *ring_ptr, Feed f, uint32_t &red_it_ref,
                                           int part) {
   uint32_t red_it = red_it_ref;
   constexpr bool LO = PHASE2 && FMT == BF16;
   constexpr int NBP = FMT == Q4 ? 1 : NB;   // blocks of eight tokens whose operand is fetched ahead
   constexpr int R = ratio_of<FMT>();
-  constexpr int HELD = held_of<FMT>();
+  constexpr int HELD = held_of<FMT>(LO, NB);
   const Geo g = part_geo<FMT>(p, part, sh->nact);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, c = lane & 3;
   const uint32_t ring = smem_u32(ring_ptr);
@@ -850,7 +858,7 @@ __device__ __noinline__ Feed consume_part(const FewParams &p, Shared *sh, uint8_
         }
         if (FMT == Q4) __syncwarp();
         ++f.used;
-        feed_step<RFMT>(p, sh, f, ring);
+        feed_step<RFMT, DEPTH>(p, sh, f, ring);
 #pragma unroll
         for (int n = 0; n < NB; ++n) bp[n] = bn[n];
       }
@@ -875,9 +883,9 @@ __device__ __noinline__ Feed consume_part(const FewParams &p, Shared *sh, uint8_
           }
         }
       } else {
-        // the eight warps' partial results meet; two buffers in turn, so one
+        // the warps' partial results meet; two buffers in turn, so one
         // barrier per task keeps writers and readers apart
-        uint32_t(*red)[2][32][4] = sh->red[red_it & 1u];
+        uint32_t(*red)[NB][32][4] = reinterpret_cast<Partial<NB> *>(partials(sh))->red[red_it & 1u];
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
           uint32_t v[4];
@@ -969,7 +977,7 @@ __device__ __forceinline__ int warp_argmax(unsigned long long key, int i) {
 template <int TP>
 __device__ __forceinline__ void route_logits(const FewParams &p, Shared *sh) {
   constexpr int IT = TP <= 4 ? 8 : (TP <= 8 ? 4 : 2);   // steps of 256 elements whose weights are in flight at once
-  double(*sums)[MAX_T] = reinterpret_cast<double(*)[MAX_T]>(sh->red);
+  double(*sums)[MAX_T] = reinterpret_cast<double(*)[MAX_T]>(partials(sh));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = p.E <= (int)gridDim.x ? CW : CW / 2, at_once = CW / per;
   const int slice = ((p.d + per - 1) / per + 7) / 8 * 8;
@@ -1172,10 +1180,11 @@ __device__ __forceinline__ void choose(const FewParams &p, Shared *sh, int t, do
 // launch, and fetching its instructions is much of its time.
 __device__ __noinline__ void make_plan(const FewParams &p, Shared *sh, double *prob) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  static_assert(sizeof(((Shared *)0)->red) >= CW * kMaxExperts * 8, "selection scratch");
-  unsigned long long *keys = reinterpret_cast<unsigned long long *>(sh->red) + warp * kMaxExperts;
-  sh->mask[tid] = 0u;
-  static_assert(CT == kMaxExperts, "a thread per expert");
+  static_assert(sizeof(Partial<1>) >= 8 * kMaxExperts * 8 && sizeof(Partial<2>) >= MAX_T * kMaxExperts * 8,
+                "selection scratch: a row of keys per token");
+  unsigned long long *keys = reinterpret_cast<unsigned long long *>(partials(sh)) + warp * kMaxExperts;
+  if (tid < kMaxExperts) sh->mask[tid] = 0u;
+  static_assert(CT >= kMaxExperts && CW >= MAX_T, "a thread per expert, a warp per token");
   // logits (softmax: with the bias) or sigmoid scores, a thread per (token, expert)
   const int n_logits = p.T * p.E;
 #pragma unroll 1
@@ -1198,8 +1207,7 @@ __device__ __noinline__ void make_plan(const FewParams &p, Shared *sh, double *p
     prob[i] = l;
   }
   __syncthreads();
-#pragma unroll 1
-  for (int t = warp; t < p.T; t += CW) choose(p, sh, t, prob + (size_t)t * p.E, keys, lane);
+  if (const int t = warp; t < p.T) choose(p, sh, t, prob + (size_t)t * p.E, keys, lane);
   __syncthreads();
   const int slots = p.T * p.k;
 #pragma unroll 1
@@ -1208,9 +1216,14 @@ __device__ __noinline__ void make_plan(const FewParams &p, Shared *sh, double *p
     if (e >= 0) atomicOr(&sh->mask[e], 1u << (i / p.k));
   }
   __syncthreads();
+  if (blockIdx.x == 0 && tid < p.E) {
+    double s = 0.0;
+    for (int t = 0; t < p.T; ++t) s += prob[(size_t)t * p.E + tid];
+    p.prob_sum[tid] = (float)s;
+  }
   // thread e: expert e.  In-order dropping: the first `cap` tokens stay
-  uint32_t m = sh->mask[tid];
-  sh->raw[tid] = (uint8_t)__popc(m);
+  uint32_t m = tid < kMaxExperts ? sh->mask[tid] : 0u;
+  if (tid < kMaxExperts) sh->raw[tid] = (uint8_t)__popc(m);
   if (p.cap >= 0)
     while (__popc(m) > p.cap) m &= ~(0x80000000u >> __clz(m));
   const int cnt = __popc(m);
@@ -1225,7 +1238,7 @@ __device__ __noinline__ void make_plan(const FewParams &p, Shared *sh, double *p
     sh->warp_n[warp] = __popc(live);
     sh->warp_rows[warp] = pre;
   }
-  sh->mask[tid] = m;
+  if (tid < kMaxExperts) sh->mask[tid] = m;
   __syncthreads();
   int n = 0, rows = 0, all_n = 0, all_rows = 0;
 #pragma unroll
@@ -1250,17 +1263,14 @@ __device__ __noinline__ void make_plan(const FewParams &p, Shared *sh, double *p
 }
 
 // What the call returns beside the output; one block, while it waits
-__device__ __forceinline__ void write_choice(const FewParams &p, const Shared *sh, const double *prob) {
+__device__ __forceinline__ void write_choice(const FewParams &p, const Shared *sh) {
   const int e = threadIdx.x;
   for (int i = e; i < p.T * p.k; i += CT) {
     p.ids[i] = sh->sel_id[i];
     p.wts[i] = sh->sel_w[i];
   }
   if (e < p.E) {
-    double s = 0.0;
-    for (int t = 0; t < p.T; ++t) s += prob[(size_t)t * p.E + e];
     const int raw = sh->raw[e], kept = __popc(sh->mask[e]);
-    p.prob_sum[e] = (float)s;
     p.raw_counts[e] = raw;
     p.kept_counts[e] = kept;
     if (raw > kept) atomicAdd(p.dropped, raw - kept);
@@ -1314,7 +1324,7 @@ __device__ __forceinline__ uint2 codes8(uint4 v, uint32_t top) {
 // token rows: one block each, from the last block down (the router's units
 // start at the first)
 __device__ __forceinline__ void quantize_x(const FewParams &p, Shared *sh) {
-  uint32_t *scratch = &sh->red[0][0][0][0][0];
+  uint32_t *scratch = partials(sh);
   for (int t = (int)gridDim.x - 1 - (int)blockIdx.x; t < p.T; t += gridDim.x) {
     const uint4 *row = reinterpret_cast<const uint4 *>(p.x + (size_t)t * p.d);
     uint32_t m = 0;
@@ -1378,12 +1388,15 @@ __device__ __forceinline__ void combine(const FewParams &p, const Shared *sh, in
 
 template <int FMT, int TP>
 __global__ void __launch_bounds__(CT, 1) few_kernel(const __grid_constant__ FewParams p) {
-  constexpr int NB = TP > 8 ? 2 : 1;
+  constexpr int NB = TP > 8 ? 2 : 1, DEPTH = depth_of(FMT, TP);
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t *ring_ptr = smem_raw + (threadIdx.x >> 5) * DEPTH * unit_bytes(FMT);      // this warp's
   const uint32_t ring = smem_u32(ring_ptr);
-  double *prob = reinterpret_cast<double *>(smem_raw + CW * DEPTH * unit_bytes(FMT));
-  Shared *sh = reinterpret_cast<Shared *>(reinterpret_cast<uint8_t *>(prob) + scratch_bytes(p.T, p.E));
+  // the tokens' probabilities: in the slots where nothing is fetched before the
+  // choice (no shared expert with 4-bit weights), else behind them
+  uint8_t *behind = smem_raw + CW * DEPTH * unit_bytes(FMT);
+  double *prob = reinterpret_cast<double *>(FMT == Q4 ? smem_raw : behind);
+  Shared *sh = reinterpret_cast<Shared *>(behind + (FMT == Q4 ? 0 : scratch_bytes(p.T, p.E)));
   volatile int *abort_flag = &sh->abort_flag;
   if (threadIdx.x == 0) {
     sh->abort_flag = 0;
@@ -1394,24 +1407,24 @@ __global__ void __launch_bounds__(CT, 1) few_kernel(const __grid_constant__ FewP
     FeedState &st = sh->feed[threadIdx.x >> 5];
     st.part = st.limit = p.Fs ? S1 : R1;
   }
-  sh->bias[threadIdx.x] = p.bias && threadIdx.x < p.E ? __ldg(p.bias + threadIdx.x) : 0.f;
+  if (threadIdx.x < kMaxExperts) sh->bias[threadIdx.x] = p.bias && threadIdx.x < p.E ? __ldg(p.bias + threadIdx.x) : 0.f;
   __syncthreads();
   Feed feed{};
   uint32_t red_it = 0;
-  if (p.Fs) feed = feed_open<FMT>(p, sh, feed, ring, R1);
+  if (p.Fs) feed = feed_open<FMT, DEPTH>(p, sh, feed, ring, R1);
   if (FMT == I8) {
     quantize_x(p, sh);
     if (blockIdx.x == 0)
       for (int i = threadIdx.x; i < p.T * p.k; i += CT) p.rowmax[i] = 0u;
   }
   route_logits<TP>(p, sh);
-  if (p.Fs) feed = consume_part<BF16, FMT, false, NB>(p, sh, ring_ptr, feed, red_it, S1);
+  if (p.Fs) feed = consume_part<BF16, FMT, false, NB, DEPTH>(p, sh, ring_ptr, feed, red_it, S1);
   grid_arrive(p.bar);
   grid_wait(p.bar, abort_flag, p);
   make_plan(p, sh, prob);
-  feed = feed_open<FMT>(p, sh, feed, ring, END);
-  if (p.Fs) feed = consume_part<BF16, FMT, true, NB>(p, sh, ring_ptr, feed, red_it, S2);
-  feed = consume_part<FMT, FMT, false, NB>(p, sh, ring_ptr, feed, red_it, R1);
+  feed = feed_open<FMT, DEPTH>(p, sh, feed, ring, END);
+  if (p.Fs) feed = consume_part<BF16, FMT, true, NB, DEPTH>(p, sh, ring_ptr, feed, red_it, S2);
+  feed = consume_part<FMT, FMT, false, NB, DEPTH>(p, sh, ring_ptr, feed, red_it, R1);
   grid_arrive(p.bar + 8);
   grid_wait(p.bar + 8, abort_flag, p);
   if (FMT == I8) {
@@ -1419,9 +1432,9 @@ __global__ void __launch_bounds__(CT, 1) few_kernel(const __grid_constant__ FewP
     grid_arrive(p.bar + 16);
     grid_wait(p.bar + 16, abort_flag, p);
   }
-  feed = consume_part<FMT, FMT, true, NB>(p, sh, ring_ptr, feed, red_it, R2);
+  feed = consume_part<FMT, FMT, true, NB, DEPTH>(p, sh, ring_ptr, feed, red_it, R2);
   grid_arrive(p.bar + 24);
-  if (blockIdx.x == 0) write_choice(p, sh, prob);
+  if (blockIdx.x == 0) write_choice(p, sh);
   slot_rows(p, sh);
   grid_wait(p.bar + 24, abort_flag, p);
   combine(p, sh, part_geo<FMT>(p, R2, sh->nact).ks);
@@ -1429,8 +1442,14 @@ __global__ void __launch_bounds__(CT, 1) few_kernel(const __grid_constant__ FewP
 }
 
 template <int FMT, int TP>
+__host__ constexpr size_t smem_bytes(int T, int E) {
+  return (size_t)CW * depth_of(FMT, TP) * unit_bytes(FMT) + (FMT == Q4 ? 0 : scratch_bytes(T, E)) + sizeof(Shared) +
+         (TP > 8 ? sizeof(Partial<2>) : sizeof(Partial<1>));
+}
+
+template <int FMT, int TP>
 cudaError_t run(const FewParams &p, cudaStream_t s) {
-  const size_t smem = (size_t)CW * DEPTH * unit_bytes(FMT) + scratch_bytes(p.T, p.E) + sizeof(Shared);
+  const size_t smem = smem_bytes<FMT, TP>(p.T, p.E);
   auto kern = few_kernel<FMT, TP>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
@@ -1447,7 +1466,8 @@ cudaError_t run(const FewParams &p, cudaStream_t s) {
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
-static_assert((size_t)CW * DEPTH * unit_bytes(Q4) + scratch_bytes(MAX_T, kMaxExperts) + sizeof(Shared) <= (size_t)SMEM_LIMIT,
+static_assert(smem_bytes<BF16, 4>(4, kMaxExperts) <= SMEM_LIMIT && smem_bytes<BF16, 16>(MAX_T, kMaxExperts) <= SMEM_LIMIT &&
+                  smem_bytes<Q4, 16>(MAX_T, kMaxExperts) <= SMEM_LIMIT,
               "shared memory");
 
 template <int FMT>
