@@ -518,7 +518,9 @@ moe_status moe_forward(const moe_config *cfg, const void *x, const float *w_rout
  * Results agree with moe_forward's within bf16 rounding, not bit for bit: ids
  * can differ only for tokens whose selection margin is within 1e-4, expert
  * outputs are kept in fp32 up to the combine, and the intermediate keeps 16
- * significant bits (8-bit experts: bf16, which is then quantised).
+ * significant bits (8-bit experts: bf16, which is then quantised; 4-bit
+ * experts: x and the intermediate as 16-bit integers over the largest
+ * magnitude of their row).
  * A token whose router scores are NaN chooses no expert: ids -1, and a device
  * status.  The kernel's blocks wait for one another, so it is launched
  * cooperatively: it starts when every SM has room for its block, and two

@@ -40,12 +40,15 @@
 //               in shared memory, one barrier per task;
 //   short rows  (solo) each warp takes whole tasks.
 //
-// Precision: bf16 weights take h as the sum of two bf16 (16 bits); with 4-bit
-// ones, whose unpacking is what bounds them, h is one bf16, as in the staged
-// layer.  4-bit codes are multiplied as exact small integers and scaled per
-// group of 64 in fp32 (w = s q + b: s sum(q x) + b sum(x)).  Expert outputs
-// stay fp32 until the combine.  8-bit weights follow the 8-bit layer's
-// definition (rows of x and of the bf16 h quantised).
+// Precision: bf16 weights take h as the sum of two bf16 (16 bits).  8-bit
+// weights follow the 8-bit layer's definition (rows of x and of the bf16 h
+// quantised).  4-bit weights are bound by unpacking, and integers unpack
+// cheapest: a word's eight codes are two registers of four bytes (three
+// instructions; as bf16 pairs seven).  So x, and the fp32 h, become integers
+// of 16 bits over their row's largest element (an error of 2^-17 of it, far
+// below the codes' own), in two digits of 8 bits: v = 256 hi + lo.  Per group
+// of 64, s sum(q v) + b sum(v), the sums exact in int32, scaled and added in
+// fp32.  Expert outputs stay fp32 until the combine.
 //
 // Results do not depend on timing: every sum has a fixed order, and the row
 // maxima behind the 8-bit codes of h are integer maxima.
@@ -105,14 +108,17 @@ struct FewParams {
   int *status;
   unsigned *bar;                            // grid barrier counters, zeroed before the launch
   double *logits;                           // [T][E]
-  int8_t *xq;                               // 8-bit: [T][d] codes and scales of x
-  float *xs;
-  uint16_t *h;                              // [T*k][F], the low parts h_lo elements further
+  int8_t *xq;                               // 8-bit: [T][d] codes of x; 4-bit: [T][2][d] its two digits
+  float *xs;                                // [T] their scales
+  float *xg;                                // 4-bit: [T][d/64] sums of x's integers over the groups
+  uint16_t *h;                              // [T*k][F], bf16: the low parts h_lo elements further
+  float *hf;                                // 4-bit: [T*k][F] in fp32 instead
   size_t h_lo;
   uint16_t *hs;                             // [T][Fs] of the shared expert, likewise
   size_t hs_lo;
-  unsigned *rowmax;                         // 8-bit: [T*k] largest |h| of a row, as fp32 bits
-  int8_t *hq;                               // 8-bit: [T*k][F]
+  unsigned *rowmax;                         // 8-bit, 4-bit: [T*k] largest |h| of a row, as fp32 bits
+  int8_t *hq;                               // 8-bit: [T*k][F] codes; 4-bit: [T*k][2][F] digits
+  float *hg;                                // 4-bit: [T*k][F/64]
   float *y;                                 // [ksplit][T*k][d] expert outputs, then [T][d] of the shared expert
   int y_rows;                               // T*k
   int ksplit;                               // most parts of K that y has room for
@@ -494,14 +500,6 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// with a zero accumulator
-__device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                               uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %10, %10, %10};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
 __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1) {
   asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -509,9 +507,21 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
       : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// nibbles i and i + 4 of a code word as the exact bf16 pair (128 + q_i, 128 + q_{i+4})
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) {
-  return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+// unsigned codes times signed digits
+__device__ __forceinline__ void mma_u8s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// with a zero accumulator
+__device__ __forceinline__ void mma_u8s8_first(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
 }
 // 16 bytes of a token's row, kept in L1.  The rows that this kernel writes
 // (codes of x, h) are read after a grid barrier, whose acquire keeps older
@@ -527,10 +537,12 @@ __device__ __forceinline__ float abs_max(float a, float b) {
 }
 __device__ __forceinline__ float silu_f(float g) { return g / (1.f + expf(-g)); }
 
-// bytes of the token row per byte of the weight row
+constexpr float DIGITS_MAX = 32512.f;       // 127 * 256: the high digit stays in [-127, 127]
+
+// bytes of the token row (4-bit: of one digit of it) per byte of the weight row
 template <int FMT>
 __host__ __device__ constexpr int ratio_of() {
-  return FMT == Q4 ? 4 : 1;
+  return FMT == Q4 ? 2 : 1;
 }
 // segments whose token operand a warp holds at once (4-bit: four times the
 // registers each, and a body of a few hundred instructions per segment, which
@@ -540,28 +552,25 @@ __host__ __device__ constexpr int held_of(bool lo, int NB) {
   return FMT == Q4 ? 1 : (lo || NB > 1 ? SEGS / 2 : SEGS);
 }
 
-// B operand of one segment.  bf16 and 8-bit: 16 bytes of the token row (and of
-// its low part).  4-bit: a segment is two groups of 64 codes; 16 elements of
-// the token row per group.
+// B operand of one segment: 16 bytes of the token row (bf16 phase 2: and of its
+// low part).  4-bit: a segment is two groups of 64 codes; 16 bytes of each
+// digit per group.
 template <int FMT, bool LO>
 struct BSeg {
-  uint4 v[FMT == Q4 ? 4 : 1][LO ? 2 : 1];
+  uint4 v[FMT == Q4 ? 2 : 1][LO || FMT == Q4 ? 2 : 1];
 };
 
-// row: this lane's place in the segment's stretch of the token row; left:
-// bytes of the weight row from the segment on.  CHECK: the segment may reach
-// past the row's end.
+// row: this lane's place in the segment's stretch of the token row; second:
+// bytes from there to the low part or digit; left: bytes of the weight row
+// from the segment on.  CHECK: the segment may reach past the row's end.
 template <int FMT, bool LO, bool CHECK>
-__device__ __forceinline__ void load_b(BSeg<FMT, LO> &bv, const char *row, size_t lo_bytes, int left, int c) {
+__device__ __forceinline__ void load_b(BSeg<FMT, LO> &bv, const char *row, size_t second, int left, int c) {
 #pragma unroll
-  for (int q = 0; q < (FMT == Q4 ? 4 : 1); ++q) {
-    // 4-bit: group q / 2 of the segment, elements 16 c + 8 (q % 2) ..
-    constexpr int R = ratio_of<FMT>();
-    const int at = FMT == Q4 ? (q >> 1) * 32 + (q & 1) * 4 : 0;
-    const bool ok = !CHECK || at + c * (FMT == Q4 ? 8 : 16) < left;
+  for (int q = 0; q < (FMT == Q4 ? 2 : 1); ++q) {
+    const bool ok = !CHECK || (FMT == Q4 ? q * 32 : c * 16) < left;
 #pragma unroll
-    for (int l = 0; l < (LO ? 2 : 1); ++l)
-      bv.v[q][l] = ok ? ld_l1(row + at * R + (l ? lo_bytes : 0)) : make_uint4(0u, 0u, 0u, 0u);
+    for (int l = 0; l < (LO || FMT == Q4 ? 2 : 1); ++l)
+      bv.v[q][l] = ok ? ld_l1(row + q * 64 + (l ? second : 0)) : make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
@@ -578,14 +587,16 @@ struct Acc<I8, NB> {
 
 // One segment of the 16 rows times the tokens.  a: this lane's place in the
 // segment's slots (4-bit: row g's); left: bytes of the rows from the segment
-// on.  sw: 4-bit, the lane's scale words of the segment (s and b of row g, of
-// row g + 8, two groups each).  The first NBP blocks of eight tokens have
-// their operand in registers; a further one (4-bit weights, whose operand is
-// four times as long, and only for an expert that more than eight tokens
+// on.  4-bit: sw, the lane's scale words of the segment (s and b of row g, of
+// row g + 8, two groups each), and gs(n, q, j), the sum of token 2c + j of
+// block n over the segment's group q.  The first NBP blocks of eight tokens
+// have their operand in registers; a further one (4-bit weights, whose operand
+// is four times as long, and only for an expert that more than eight tokens
 // chose) fetches it here from `far`.
-template <int FMT, bool LO, int NB, int NBP, bool CHECK>
-__device__ __forceinline__ void consume(Acc<FMT, NB> &acc, const BSeg<FMT, LO> (&bv)[NBP], const char *far, int left,
-                                        const uint8_t *a, bool second, int g, int c, const uint32_t (&sw)[4]) {
+template <int FMT, bool LO, int NB, int NBP, bool CHECK, class Sums>
+__device__ __forceinline__ void consume(Acc<FMT, NB> &acc, const BSeg<FMT, LO> (&bv)[NBP], const char *far, size_t far_second,
+                                        int left, const uint8_t *a, bool second, int g, int c, const uint32_t (&sw)[4],
+                                        Sums gs) {
   if constexpr (FMT != Q4) {
     uint4 lo = *reinterpret_cast<const uint4 *>(a), hi = *reinterpret_cast<const uint4 *>(a + 512);
     if (CHECK && c * 16 >= left) lo = hi = make_uint4(0u, 0u, 0u, 0u);
@@ -605,47 +616,38 @@ __device__ __forceinline__ void consume(Acc<FMT, NB> &acc, const BSeg<FMT, LO> (
       }
     }
   } else {
+    BSeg<FMT, LO> own;
+    if (NB > NBP && second) load_b<FMT, LO, CHECK>(own, far, far_second, left, c);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       if (CHECK && q * 32 >= left) break;
       const int half = (q ^ ((g >> 1) & 1)) * 32 + c * 8;
       const uint2 lo = *reinterpret_cast<const uint2 *>(a + half);
       const uint2 hi = *reinterpret_cast<const uint2 *>(a + 512 + half);
-      // scale and bias of rows g and g + 8 for this group.  The codes enter as
-      // 128 + q (an exact bf16 by its bits), so the bias takes 128 s off again
+      // a word's codes 0, 2, 4, 6 and 1, 3, 5, 7: the digits lie in that order
+      constexpr uint32_t nib = 0x0F0F0F0Fu;
+      const uint32_t l0 = lo.x & nib, l1 = (lo.x >> 4) & nib, l2 = lo.y & nib, l3 = (lo.y >> 4) & nib;
+      const uint32_t h0 = hi.x & nib, h1 = (hi.x >> 4) & nib, h2 = hi.y & nib, h3 = (hi.y >> 4) & nib;
       const float s_lo = __uint_as_float(q ? sw[0] & 0xFFFF0000u : sw[0] << 16);
       const float s_hi = __uint_as_float(q ? sw[2] & 0xFFFF0000u : sw[2] << 16);
-      const float b_lo = fmaf(-128.f, s_lo, __uint_as_float(q ? sw[1] & 0xFFFF0000u : sw[1] << 16));
-      const float b_hi = fmaf(-128.f, s_hi, __uint_as_float(q ? sw[3] & 0xFFFF0000u : sw[3] << 16));
+      const float b_lo = __uint_as_float(q ? sw[1] & 0xFFFF0000u : sw[1] << 16);
+      const float b_hi = __uint_as_float(q ? sw[3] & 0xFFFF0000u : sw[3] << 16);
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
         if (n > 0 && !second) break;
-        BSeg<FMT, LO> own;
-        if (n >= NBP) load_b<FMT, LO, CHECK>(own, far, 0, left, c);
-        float dq[4], dx[4];
+        int d[2][4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t wl = u ? lo.y : lo.x, wh = u ? hi.y : hi.x;
-          constexpr uint32_t one = 0x3F803F80u;
-          // elements (i, i + 4) of the token's 8, in the order of the nibble pairs
-          const uint4 b = n < NBP ? bv[n < NBP ? n : 0].v[2 * q + u][0] : own.v[2 * q + u][0];
-          const uint32_t p0 = __byte_perm(b.x, b.z, 0x5410), p1 = __byte_perm(b.x, b.z, 0x7632);
-          const uint32_t p2 = __byte_perm(b.y, b.w, 0x5410), p3 = __byte_perm(b.y, b.w, 0x7632);
-          if (u == 0) {
-            mma_bf16_first(dq, code_pair(wl, 0), code_pair(wh, 0), code_pair(wl, 1), code_pair(wh, 1), p0, p1);
-            mma_bf16_first(dx, one, one, one, one, p0, p1);
-          } else {
-            mma_bf16(dq, code_pair(wl, 0), code_pair(wh, 0), code_pair(wl, 1), code_pair(wh, 1), p0, p1);
-            mma_bf16(dx, one, one, one, one, p0, p1);
-          }
-          mma_bf16(dq, code_pair(wl, 2), code_pair(wh, 2), code_pair(wl, 3), code_pair(wh, 3), p2, p3);
-          mma_bf16(dx, one, one, one, one, p2, p3);
+        for (int l = 0; l < 2; ++l) {
+          const uint4 b = n < NBP ? bv[n < NBP ? n : 0].v[q][l] : own.v[q][l];
+          mma_u8s8_first(d[l], l0, h0, l1, h1, b.x, b.y);
+          mma_u8s8(d[l], l2, h2, l3, h3, b.z, b.w);
         }
+        const float g0 = gs(n, q, 0), g1 = gs(n, q, 1);
         float(&t)[4] = acc.f[n][q];
-        t[0] = fmaf(s_lo, dq[0], fmaf(b_lo, dx[0], t[0]));
-        t[1] = fmaf(s_lo, dq[1], fmaf(b_lo, dx[1], t[1]));
-        t[2] = fmaf(s_hi, dq[2], fmaf(b_hi, dx[2], t[2]));
-        t[3] = fmaf(s_hi, dq[3], fmaf(b_hi, dx[3], t[3]));
+        t[0] = fmaf(s_lo, (float)(d[0][0] * 256 + d[1][0]), fmaf(b_lo, g0, t[0]));
+        t[1] = fmaf(s_lo, (float)(d[0][1] * 256 + d[1][1]), fmaf(b_lo, g1, t[1]));
+        t[2] = fmaf(s_hi, (float)(d[0][2] * 256 + d[1][2]), fmaf(b_hi, g0, t[2]));
+        t[3] = fmaf(s_hi, (float)(d[0][3] * 256 + d[1][3]), fmaf(b_hi, g1, t[3]));
       }
     }
   }
@@ -688,17 +690,24 @@ __device__ __forceinline__ const char *b_row(const FewParams &p, const Cursor &c
   r = min(r, cu.rows - 1);
   if (!PHASE2) {
     const int t = part == S1 ? r : nth_bit(cu.mask, r);
-    return FMT == I8 ? reinterpret_cast<const char *>(p.xq + (size_t)t * p.d)
-                     : reinterpret_cast<const char *>(p.x + (size_t)t * p.d);
+    return FMT == BF16 ? reinterpret_cast<const char *>(p.x + (size_t)t * p.d)
+                       : reinterpret_cast<const char *>(p.xq + (size_t)t * (FMT == Q4 ? 2 : 1) * p.d);
   }
   if (part == S2) return reinterpret_cast<const char *>(p.hs + (size_t)r * p.Fs);
-  return FMT == I8 ? reinterpret_cast<const char *>(p.hq + (size_t)(cu.row0 + r) * p.F)
-                   : reinterpret_cast<const char *>(p.h + (size_t)(cu.row0 + r) * p.F);
+  return FMT == BF16 ? reinterpret_cast<const char *>(p.h + (size_t)(cu.row0 + r) * p.F)
+                     : reinterpret_cast<const char *>(p.hq + (size_t)(cu.row0 + r) * (FMT == Q4 ? 2 : 1) * p.F);
+}
+
+// 4-bit: its sums over the groups
+template <bool PHASE2>
+__device__ __forceinline__ const float *g_row(const FewParams &p, const Cursor &cu, int r) {
+  r = min(r, cu.rows - 1);
+  return PHASE2 ? p.hg + (size_t)(cu.row0 + r) * (p.F / 64) : p.xg + (size_t)nth_bit(cu.mask, r) * (p.d / 64);
 }
 
 // What becomes of one finished value: row f of the task's `cols` (with its up
 // projection u where the task holds pairs), token tok.  Returns the magnitude
-// of the stored bf16 h (8-bit weights: the row maxima are taken from it).
+// of the stored h (8-bit and 4-bit weights: the row maxima are taken from it).
 template <int FMT, bool PHASE2>
 __device__ __forceinline__ float emit(const FewParams &p, const Cursor &cu, int part, bool pairs, int f, int tok, float v,
                                       float u) {
@@ -706,18 +715,24 @@ __device__ __forceinline__ float emit(const FewParams &p, const Cursor &cu, int 
   const int N = PHASE2 ? p.d : (part == S1 ? p.Fs : p.F);
   if (tok >= cu.rows || col >= N) return 0.f;
   const size_t row = (size_t)cu.row0 + tok;
-  if (FMT == I8) {
+  if (FMT != BF16) {
     // row scale: of the token (phase 1), of the row of h (phase 2)
     float xs;
     if (PHASE2) {
       const uint32_t top = __ldcg(p.rowmax + row);
-      xs = top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __fdiv_rn(__uint_as_float(top), 127.f);
+      xs = top >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
+                              : __fdiv_rn(__uint_as_float(top), FMT == Q4 ? DIGITS_MAX : 127.f);
     } else {
       xs = __ldcg(p.xs + nth_bit(cu.mask, tok));
     }
-    const size_t r0 = (size_t)cu.e * (PHASE2 ? p.d : p.w_stride) + col;
-    v *= xs * __ldg(static_cast<const float *>(PHASE2 ? p.s3 : p.s1) + r0);
-    if (pairs) u *= xs * __ldg(static_cast<const float *>(p.s2) + r0);
+    if (FMT == I8) {
+      const size_t r0 = (size_t)cu.e * (PHASE2 ? p.d : p.w_stride) + col;
+      if (pairs) u *= xs * __ldg(static_cast<const float *>(p.s2) + r0);
+      xs *= __ldg(static_cast<const float *>(PHASE2 ? p.s3 : p.s1) + r0);
+    } else if (pairs) {
+      u *= xs;
+    }
+    v *= xs;
   }
   if (PHASE2) {
     p.y[(part == S2 ? (size_t)p.ksplit * p.y_rows + tok : (size_t)cu.kp * p.y_rows + row) * p.d + col] = v;
@@ -725,6 +740,10 @@ __device__ __forceinline__ float emit(const FewParams &p, const Cursor &cu, int 
   }
   if (pairs) v = silu_f(v) * u;
   else v = v < 0.f ? 0.f : v;               // a NaN stays one
+  if (FMT == Q4) {
+    p.hf[row * p.F + col] = v;
+    return v;
+  }
   const __nv_bfloat16 hi = __float2bfloat16_rn(v);
   uint16_t *h = part == S1 ? p.hs + (size_t)tok * p.Fs + col : p.h + row * p.F + col;
   *h = *reinterpret_cast<const uint16_t *>(&hi);
@@ -749,13 +768,14 @@ __device__ __noinline__ Feed consume_part(const FewParams &p, Shared *sh, uint8_
   const Geo g = part_geo<FMT>(p, part, sh->nact);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, c = lane & 3;
   const uint32_t ring = smem_u32(ring_ptr);
-  const size_t lo_bytes = 2 * (part == S2 ? p.hs_lo : p.h_lo);
+  const size_t lo_bytes = FMT == Q4 ? (PHASE2 ? p.F : p.d) : 2 * (part == S2 ? p.hs_lo : p.h_lo);   // to the low part or digit
   const bool even = g.rb % SEG == 0;        // whole segments only
   const bool odd_groups = FMT == Q4 && (g.rb / 32 & 1) && (lg & 1);
   const bool pairs = !PHASE2 && (part == S1 || p.swiglu);
-  const bool top_of_h = FMT == I8 && part == R1;
+  const bool top_of_h = FMT != BF16 && part == R1;
   const int stride = g.solo ? CW : 1;
-  const int lane_b = c * (FMT == Q4 ? 8 : 16) * R;
+  const int lane_b = c * 16;
+  const int KG = g.rb / 32;                 // 4-bit: groups of a row
 
   // a task's token rows at this lane, from the warp's first segment on
   auto enter = [&](int j, Cursor &cu, Span &w, const char *(&rp)[NB]) {
@@ -774,6 +794,19 @@ __device__ __noinline__ Feed consume_part(const FewParams &p, Shared *sh, uint8_
     const char *bp[NB];
 #pragma unroll
     for (int n = 0; n < NB; ++n) bp[n] = rowp[n];
+    // 4-bit: sums of the lane's token rows over groups c and c + 4 of a unit's
+    // eight, fetched a unit ahead
+    float gsum[NB][2];
+    auto load_sums = [&](const Cursor &cc, int group) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        if (n > 0 && cc.rows <= 8) break;
+        const float *row = g_row<PHASE2>(p, cc, lg + 8 * n) + group + c;
+        gsum[n][0] = group + c < KG ? __ldcg(row) : 0.f;
+        gsum[n][1] = group + c + 4 < KG ? __ldcg(row + 4) : 0.f;
+      }
+    };
+    if constexpr (FMT == Q4) load_sums(cu, 2 * w.first);
     BSeg<FMT, LO> bv[HELD][NBP];
 #pragma unroll
     for (int s = 0; s < HELD; ++s)
@@ -810,6 +843,16 @@ __device__ __noinline__ Feed consume_part(const FewParams &p, Shared *sh, uint8_
         cp_async_wait<DEPTH - 1>();
         if (FMT == Q4) __syncwarp();
         const uint8_t *a = FMT == Q4 ? slot + lg * 64 : slot + lane * 16;
+        float now[NB][2];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          now[n][0] = gsum[n][0];
+          now[n][1] = gsum[n][1];
+        }
+        if constexpr (FMT == Q4) {
+          if (!last) load_sums(cu, 2 * (w.first + seg + SEGS));
+          else if (more) load_sums(nc, 2 * nw.first);
+        }
         uint32_t sw[4] = {0u, 0u, 0u, 0u};
         auto scales = [&](int s) {
           const uint4 *t = reinterpret_cast<const uint4 *>(slot + ROWS * UNIT + (lg * 4 + s) * 32);
@@ -827,8 +870,11 @@ __device__ __noinline__ Feed consume_part(const FewParams &p, Shared *sh, uint8_
           constexpr bool CHECK = decltype(check)::value;
           if (s < n_seg) {
             if constexpr (FMT == Q4) scales(s);
-            consume<FMT, LO, NB, NBP, CHECK>(acc, bv[s % HELD], bp[NB - 1] + s * SEG * R, row_left - s * SEG, a + s * 1024,
-                                             second, lg, c, sw);
+            consume<FMT, LO, NB, NBP, CHECK>(
+                acc, bv[s % HELD], bp[NB - 1] + s * SEG * R, lo_bytes, row_left - s * SEG, a + s * 1024, second, lg, c, sw,
+                [&](int n, int q, int j) {              // group 2 s + q of the unit, held by the lanes of quad column
+                  return __shfl_sync(0xffffffffu, s < 2 ? now[n][0] : now[n][1], c * 8 + j * 4 + (2 * s + q) % 4);
+                });
           }
           // the operand of the segment HELD further on takes its registers
           const int t = s + HELD;
@@ -1321,8 +1367,53 @@ __device__ __forceinline__ uint2 codes8(uint4 v, uint32_t top) {
   return o;
 }
 
+// 16-bit integers of 8 elements of a row with largest magnitude `top`, as two
+// digits, in the order in which a word's codes unpack (0, 2, 4, 6, 1, 3, 5, 7);
+// returns their sum.
+__device__ __forceinline__ int digits8(const float (&x)[8], uint32_t top, uint2 &hi, uint2 &lo) {
+  hi = lo = make_uint2(0u, 0u);
+  if (top == 0u || top >= 0x7F800000u) return 0;
+  float a = __uint_as_float(top);
+  const float pre = a < 0x1p-60f ? 0x1p64f : (a > 0x1p100f ? 0x1p-32f : 1.f);
+  a *= pre;
+  const float r = __fdiv_rn(DIGITS_MAX, a);
+  int v[8], sum = 0;
+  uint32_t t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = __float_as_int(fmaf(x[i] * pre, r, 12582912.f)) - 0x4B400000;   // rounded to the nearest, |v| <= 32512
+    t[i] = (uint32_t)(v[i] + 128);          // its second byte: (v + 128) >> 8
+    sum += v[i];
+  }
+  auto low = [](uint32_t a0, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a0, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+  };
+  auto next = [](uint32_t a0, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a0, b, 0x0051), __byte_perm(c, d, 0x0051), 0x5410);
+  };
+  lo = make_uint2(low(v[0], v[2], v[4], v[6]), low(v[1], v[3], v[5], v[7]));
+  hi = make_uint2(next(t[0], t[2], t[4], t[6]), next(t[1], t[3], t[5], t[7]));
+  return sum;
+}
+
+// One step of a digit pass: eight elements per thread (live ones: whole groups
+// of eight neighbouring threads), vector i of a row of K.  Called by whole warps.
+__device__ __forceinline__ void store_digits(const float (&x)[8], uint32_t top, bool live, int i, int K, int8_t *digits,
+                                             float *sums) {
+  uint2 hi, lo;
+  int sum = digits8(x, top, hi, lo);
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (live) {
+    reinterpret_cast<uint2 *>(digits)[i] = hi;
+    reinterpret_cast<uint2 *>(digits + K)[i] = lo;
+    if ((i & 7) == 0) sums[i >> 3] = (float)sum;
+  }
+}
+
 // token rows: one block each, from the last block down (the router's units
 // start at the first)
+template <int FMT>
 __device__ __forceinline__ void quantize_x(const FewParams &p, Shared *sh) {
   uint32_t *scratch = partials(sh);
   for (int t = (int)gridDim.x - 1 - (int)blockIdx.x; t < p.T; t += gridDim.x) {
@@ -1337,21 +1428,49 @@ __device__ __forceinline__ void quantize_x(const FewParams &p, Shared *sh) {
     if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = m;
     __syncthreads();
     for (int w = 0; w < CW; ++w) m = max(m, scratch[w]);
-    for (int i = threadIdx.x; i < p.d / 8; i += CT)
-      reinterpret_cast<uint2 *>(p.xq + (size_t)t * p.d)[i] = codes8(__ldg(row + i), m);
+    if (FMT == I8) {
+      for (int i = threadIdx.x; i < p.d / 8; i += CT)
+        reinterpret_cast<uint2 *>(p.xq + (size_t)t * p.d)[i] = codes8(__ldg(row + i), m);
+    } else {
+      for (int i0 = 0; i0 < p.d / 8; i0 += CT) {
+        const int i = i0 + threadIdx.x;
+        const bool live = i < p.d / 8;
+        const uint4 v = live ? __ldg(row + i) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[2 * e] = __uint_as_float(w[e] << 16);
+          x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        }
+        store_digits(x, m, live, i, p.d, p.xq + (size_t)t * 2 * p.d, p.xg + (size_t)t * (p.d / 64));
+      }
+    }
     if (threadIdx.x == 0)
-      p.xs[t] = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __fdiv_rn(__uint_as_float(m), 127.f);
+      p.xs[t] = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __fdiv_rn(__uint_as_float(m), FMT == Q4 ? DIGITS_MAX : 127.f);
     __syncthreads();                        // the scratch has been read
   }
 }
 
 // rows of h, all blocks together
+template <int FMT>
 __device__ __forceinline__ void quantize_h(const FewParams &p, const Shared *sh) {
   const int rows = sh->row0[sh->nact], nv = p.F / 8;
-  for (long long i = (long long)blockIdx.x * CT + threadIdx.x; i < (long long)rows * nv; i += (long long)gridDim.x * CT) {
-    const int r = (int)(i / nv);
-    reinterpret_cast<uint2 *>(p.hq)[i] =
-        codes8(__ldcg(reinterpret_cast<const uint4 *>(p.h) + i), __ldcg(p.rowmax + r));
+  const long long n = (long long)rows * nv, step = (long long)gridDim.x * CT;
+  for (long long i0 = (long long)blockIdx.x * CT; i0 < n; i0 += step) {
+    const long long i = i0 + threadIdx.x;
+    const bool live = i < n;
+    const int r = live ? (int)(i / nv) : 0;
+    const uint32_t top = live ? __ldcg(p.rowmax + r) : 0u;
+    if (FMT == I8) {
+      if (live) reinterpret_cast<uint2 *>(p.hq)[i] = codes8(__ldcg(reinterpret_cast<const uint4 *>(p.h) + i), top);
+    } else {
+      const float4 *src = reinterpret_cast<const float4 *>(p.hf) + 2 * i;
+      const float4 u = live ? __ldcg(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 v = live ? __ldcg(src + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float x[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+      store_digits(x, top, live, (int)(i - (long long)r * nv), p.F, p.hq + (size_t)r * 2 * p.F, p.hg + (size_t)r * (p.F / 64));
+    }
   }
 }
 
@@ -1412,8 +1531,8 @@ __global__ void __launch_bounds__(CT, 1) few_kernel(const __grid_constant__ FewP
   Feed feed{};
   uint32_t red_it = 0;
   if (p.Fs) feed = feed_open<FMT, DEPTH>(p, sh, feed, ring, R1);
-  if (FMT == I8) {
-    quantize_x(p, sh);
+  if (FMT != BF16) {
+    quantize_x<FMT>(p, sh);
     if (blockIdx.x == 0)
       for (int i = threadIdx.x; i < p.T * p.k; i += CT) p.rowmax[i] = 0u;
   }
@@ -1427,8 +1546,8 @@ __global__ void __launch_bounds__(CT, 1) few_kernel(const __grid_constant__ FewP
   feed = consume_part<FMT, FMT, false, NB, DEPTH>(p, sh, ring_ptr, feed, red_it, R1);
   grid_arrive(p.bar + 8);
   grid_wait(p.bar + 8, abort_flag, p);
-  if (FMT == I8) {
-    quantize_h(p, sh);
+  if (FMT != BF16) {
+    quantize_h<FMT>(p, sh);
     grid_arrive(p.bar + 16);
     grid_wait(p.bar + 16, abort_flag, p);
   }
@@ -1482,7 +1601,7 @@ cudaError_t run_t(const FewParams &p, cudaStream_t s) {
 int k_split(const moe_config &c) { return c.num_tokens * c.top_k <= 32 ? MAX_KSPLIT : 1; }
 
 struct FewLayout {
-  size_t logits, xq, xs, h, h_lo, hs, hs_lo, rowmax, hq, y, total;
+  size_t logits, xq, xs, xg, hg, h, h_lo, hs, hs_lo, rowmax, hq, y, total;
 };
 
 FewLayout few_layout(const moe_config &c) {
@@ -1497,14 +1616,17 @@ FewLayout few_layout(const moe_config &c) {
   const size_t Fs = c.shared_intermediate > 0 ? c.shared_intermediate : 0;
   const bool i8 = c.weight_dtype == MOE_I8_CHANNEL;
   L.logits = take(sizeof(double) * T * c.num_experts);
-  L.xq = take(i8 ? T * d : 0);
-  L.xs = take(i8 ? sizeof(float) * T : 0);
-  L.h = take(2 * S * F);
-  L.h_lo = take(i8 ? 0 : 2 * S * F);
+  const bool q4 = c.weight_dtype == MOE_Q4_AFFINE_G64, ints = i8 || q4;
+  L.xq = take(ints ? (q4 ? 2 : 1) * T * d : 0);
+  L.xs = take(ints ? sizeof(float) * T : 0);
+  L.xg = take(q4 ? sizeof(float) * T * (d / 64) : 0);
+  L.hg = take(q4 ? sizeof(float) * S * (F / 64) : 0);
+  L.h = take((q4 ? sizeof(float) : 2) * S * F);
+  L.h_lo = take(ints ? 0 : 2 * S * F);
   L.hs = take(2 * T * Fs);
   L.hs_lo = take(2 * T * Fs);
-  L.rowmax = take(i8 ? sizeof(unsigned) * S : 0);
-  L.hq = take(i8 ? S * F : 0);
+  L.rowmax = take(ints ? sizeof(unsigned) * S : 0);
+  L.hq = take(ints ? (q4 ? 2 : 1) * S * F : 0);
   L.y = take(sizeof(float) * (S * k_split(c) + (Fs ? T : 0)) * d);
   L.total = off;
   return L;
@@ -1557,7 +1679,10 @@ cudaError_t launch_few(const FewArgs &a, cudaStream_t s) {
   p.logits = reinterpret_cast<double *>(ws + L.logits);
   p.xq = reinterpret_cast<int8_t *>(ws + L.xq);
   p.xs = reinterpret_cast<float *>(ws + L.xs);
+  p.xg = reinterpret_cast<float *>(ws + L.xg);
+  p.hg = reinterpret_cast<float *>(ws + L.hg);
   p.h = reinterpret_cast<uint16_t *>(ws + L.h);
+  p.hf = reinterpret_cast<float *>(ws + L.h);
   p.h_lo = (L.h_lo - L.h) / 2;
   p.hs = reinterpret_cast<uint16_t *>(ws + L.hs);
   p.hs_lo = (L.hs_lo - L.hs) / 2;

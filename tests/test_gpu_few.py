@@ -106,23 +106,27 @@ def dense(run, e):
     return m, a
 
 
-def ffn(x, m, a, act):
+def ffn(x, m, a, act, fixed=False):
     """(y, bound): the expert in float64 and how far fp32 sums over its products
     and an intermediate of 16 bits may be from it.  A sum over K takes K / 128
     dependent tensor-core additions per warp and 8 + 8 further ones, each off
-    by at most 2^-22 of the magnitudes added."""
+    by at most 2^-22 of the magnitudes added.  ``fixed`` (4-bit weights): x and
+    the intermediate are rounded to integer multiples of their row's largest
+    magnitude over 32512, so each element is off by at most half of that (and
+    the quotient by 2^-22 of the element, two fp32 roundings)."""
     eps = lambda K: (K / 128 + 24) * 2.0 ** -22
+    fix = lambda v: np.abs(v).max(1, keepdims=True) / 65024 + 2.0 ** -22 * np.abs(v) if fixed else 0.0 * v
     ax = np.abs(x)
     g = x @ m["1"].T
-    dg = eps(x.shape[1]) * (ax @ a["1"].T)
+    dg = eps(x.shape[1]) * (ax @ a["1"].T) + fix(x) @ a["1"].T
     if act == "relu":
         h, dh = np.maximum(g, 0.0), dg
     else:
         u = x @ m["2"].T
-        du = eps(x.shape[1]) * (ax @ a["2"].T)
+        du = eps(x.shape[1]) * (ax @ a["2"].T) + fix(x) @ a["2"].T
         h = R.silu(g) * u
         dh = 1.1 * dg * (np.abs(u) + du) + np.abs(R.silu(g)) * du + 2.0 ** -20 * np.abs(h)    # |silu'| < 1.1
-    dh = dh + 2.0 ** -16 * np.abs(h)
+    dh = dh + (fix(np.abs(h) + dh) if fixed else 2.0 ** -16 * np.abs(h))
     y = h @ m["3"].T
     return y, dh @ a["3"].T + eps(h.shape[1]) * ((np.abs(h) + dh) @ a["3"].T)
 
@@ -144,7 +148,7 @@ def check_few(run):
         if hasattr(run, "host"):
             y, b = R.expert_ffn(x[t], {k: v[e] for k, v in run.host.items()}, w.act)
         else:
-            y, b = ffn(x[t], *dense(run, e), w.act)
+            y, b = ffn(x[t], *dense(run, e), w.act, w.weight_format == "q4_affine_g64")
         np.add.at(out, t, y * wts[t, j][:, None])
         # fp32 scales, weights and the sum of k + 1 terms
         np.add.at(bound, t, (b + (w.k + 8) * R.F32_HALF_STEP * (np.abs(y) + b)) * wts[t, j][:, None])
