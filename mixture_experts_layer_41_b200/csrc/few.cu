@@ -67,6 +67,7 @@ namespace {
 using namespace ptx;
 
 constexpr int CW = 16;                      // warps
+constexpr int GW = 8;                       // warps that share a task of long rows: the block has two such groups
 constexpr int CT = 32 * CW;
 constexpr int ROWS = 16;                    // weight rows per task
 constexpr int UNIT = 256;                   // bytes of a row per unit
@@ -134,13 +135,11 @@ struct Geo {
   bool solo;     // one task to a warp
 };
 
-// The fetching end of a warp's stream, as far as it changes with tasks only
+// Where a warp's stream stands, as far as it changes from run to run only
 struct FeedState {
   Geo g;
   int part, limit;                          // part fetched from, and the first that is not known yet
-  int j, b;                                 // task, from the block's first, and its row block
-  int nseg;                                 // segments of the task here
-  int whole_blocks;                         // every row block has 16 rows
+  int j, run;                               // first task of the run (from the block's first), and its tasks
 };
 
 struct __align__(16) Shared {
@@ -264,8 +263,17 @@ struct Span {
 __device__ __forceinline__ Span warp_span(const Geo &g, int kp, int warp) {
   const int a = g.ks == 1 ? 0 : kp * g.ns / g.ks, b = g.ks == 1 ? g.ns : (kp + 1) * g.ns / g.ks;
   if (g.solo) return {a, b - a};
-  const int c = a + warp * (b - a) / CW;
-  return {c, a + (warp + 1) * (b - a) / CW - c};
+  const int w = warp % GW, c = a + w * (b - a) / GW;
+  return {c, a + (w + 1) * (b - a) / GW - c};
+}
+
+// A warp's (solo) or group's tasks: every `stride`-th of the block's
+__device__ __forceinline__ int first_task(const Geo &g, int warp) { return g.solo ? warp : warp / GW; }
+__device__ __forceinline__ int task_stride(const Geo &g) { return g.solo ? CW : CW / GW; }
+// How many of them, from task j with row block b on, are the same expert's (and part of K's)
+__device__ __forceinline__ int run_of(const Geo &g, int j, int b) {
+  const int by = task_stride(g);
+  return min((g.nb - b + by - 1) / by, (g.n - j + by - 1) / by);
 }
 
 // Weight rows of a task: rows 0-7 from w0, 8-15 from w1
@@ -327,37 +335,45 @@ __device__ __forceinline__ void cp_async_wait() {
 // memory (FeedState); the rest is a lane's own.
 struct Feed {
   const char *lo, *hi;                      // this lane's place in rows g and g + 8
+  ptrdiff_t step;                           // from a task's end to the next one's begin, within a run
   size_t sc_lo, sc_hi;                      // 4-bit: byte of its scale words of the two rows
-  int left;                                 // units of the task not yet fetched (0: nothing to fetch)
-  int flags;                                // see below
+  int sc_step;
+  int left, nu;                             // units of the task not yet fetched (0: nothing to fetch), and in all
+  int run;                                  // tasks of the run, this one included
+  int flags;                                // see below; and from bit 8 on the segments of the last unit (0: whole)
   int groups;                               // 4-bit: groups of the row from the next unit's place on
   uint32_t issued, used;                    // units so far
 };
-enum FeedFlags { FULL = 1, HAS_LO = 2, HAS_HI = 4, SHORT = 8, ROUTED = 16, DOWN = 32 };
-// FULL: 16 rows of whole segments; HAS_LO / HAS_HI: there is such a row; SHORT:
-// the row's last segment, in the task's last unit, ends before this lane's
-// piece; ROUTED: 4-bit rows in a 4-bit kernel; DOWN: of the down projection
+enum FeedFlags { FULL = 1, HAS_LO = 2, HAS_HI = 4, SHORT = 8, DOWN = 16, ODD = 32 };
+// FULL: 16 rows of whole segments; HAS_LO / HAS_HI: there is such a row;
+// SHORT: the row's last segment, in the task's last unit, ends before this
+// lane's piece; DOWN: of the down projection; ODD: 4-bit, the lane's rows begin
+// in the middle of a word of scales
 
-// The task st.j from scratch
+// The run that begins with task st.j
 template <int FMT>
-__device__ __forceinline__ void feed_task(const FewParams &p, const Shared *sh, FeedState &st, Feed &f) {
+__device__ __forceinline__ void feed_run(const FewParams &p, const Shared *sh, FeedState &st, Feed &f) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const Geo &ge = st.g;
   const Task t = task_of(ge, ge.first + st.j);
   const Span w = warp_span(ge, t.kp, warp);
   const Src s = task_src(p, st.part, st.part >= R1 ? sh->act[t.i] : 0, t.b, ge.rb);
-  st.b = t.b;
-  st.nseg = w.n;
-  st.whole_blocks = st.part == S1 || (st.part == R1 ? p.swiglu || p.F % ROWS == 0 : p.d % ROWS == 0);
-  f.left = (w.n + SEGS - 1) / SEGS;
+  st.run = run_of(ge, st.j, t.b);
+  // a last row block of fewer than 16 rows is a run of its own
+  const bool pairs = st.part == S1 || (st.part == R1 && p.swiglu);
+  const int N = st.part == S1 ? p.Fs : (st.part == R1 ? p.F : p.d);
+  if (!pairs && N % ROWS && st.run > 1 && t.b + (st.run - 1) * task_stride(ge) == ge.nb - 1) --st.run;
+  f.run = st.run;
+  f.left = f.nu = (w.n + SEGS - 1) / SEGS;
   const bool ends = w.first + w.n == ge.ns;                 // the span reaches the row's end
   const int tail = ge.rb - (ge.ns - 1) * SEG - c * 16;      // of the row from this lane's piece of its last segment on
   f.flags = (ge.rb % SEG == 0 && s.n0 == 8 && s.n1 == 8 ? FULL : 0) | (g < s.n0 ? HAS_LO : 0) |
-            (g < s.n1 ? HAS_HI : 0) | (ends && tail <= 0 ? SHORT : 0) | (st.part >= R1 ? ROUTED : 0) |
-            (st.part == R2 ? DOWN : 0);
+            (g < s.n1 ? HAS_HI : 0) | (ends && tail <= 0 ? SHORT : 0) | (st.part == R2 ? DOWN : 0) | (w.n % SEGS) << 8;
   const size_t off = (size_t)w.first * SEG + c * 16;
   f.lo = s.w0 + (size_t)g * ge.rb + off;
   f.hi = s.w1 + (size_t)g * ge.rb + off;
+  const int rows = (pairs ? 8 : ROWS) * task_stride(ge);    // from one task of the run to the next
+  f.step = (ptrdiff_t)rows * ge.rb - (ptrdiff_t)f.nu * UNIT;
   if (FMT == Q4) {
     // groups 2c, 2c + 1 of the unit's eight; words of two groups, from the
     // word that holds the first (a row of an odd number of groups may start
@@ -366,6 +382,8 @@ __device__ __forceinline__ void feed_task(const FewParams &p, const Shared *sh, 
     f.groups = KG - g0;
     f.sc_lo = (((s.r0 + g) * (size_t)KG + g0) & ~(size_t)1) * 2;
     f.sc_hi = (((s.r1 + g) * (size_t)KG + g0) & ~(size_t)1) * 2;
+    f.sc_step = rows * KG * 2 - f.nu * 16;
+    if ((KG & 1) && (g & 1)) f.flags |= ODD;
   }
 }
 
@@ -379,45 +397,27 @@ __device__ __noinline__ Feed feed_part(const FewParams &p, Shared *sh, Feed f, i
   FeedState n = st;
   for (; part < n.limit; ++part) {
     n.g = part < R1 ? part_geo<BF16>(p, part, sh->nact) : part_geo<FMT>(p, part, sh->nact);
-    n.j = n.g.solo ? warp : 0;
+    n.j = first_task(n.g, warp);
     if (n.j < n.g.n) break;
   }
   n.part = part;
   f.left = 0;
-  if (part < n.limit) feed_task<FMT>(p, sh, n, f);
+  if (part < n.limit) feed_run<FMT>(p, sh, n, f);
   __syncwarp();
   st = n;                                   // (every lane the same)
   __syncwarp();
   return f;
 }
 
-// On to the warp's next task: usually the same expert's next row block.
+// The run after the one that is used up
 template <int FMT>
 __device__ __noinline__ Feed feed_next(const FewParams &p, Shared *sh, Feed f) {
   FeedState &st = sh->feed[threadIdx.x >> 5];
   __syncwarp();
   FeedState n = st;
-  const int by = n.g.solo ? CW : 1;
-  n.j += by;
-  n.b += by;
+  n.j += n.run * task_stride(n.g);
   if (n.j >= n.g.n) return feed_part<FMT>(p, sh, f, n.part + 1);
-  if (n.b < n.g.nb && n.whole_blocks) {
-    const int nu = (n.nseg + SEGS - 1) / SEGS;
-    const bool pairs = n.part == S1 || (n.part == R1 && p.swiglu);
-    const int rows = (pairs ? 8 : ROWS) * by;
-    const ptrdiff_t step = (ptrdiff_t)rows * n.g.rb - (ptrdiff_t)nu * UNIT;
-    f.lo += step;
-    f.hi += step;
-    f.left = nu;
-    if (FMT == Q4) {                        // rb / 32 groups of 2 bytes a row, 8 groups a unit
-      const ptrdiff_t sc = (ptrdiff_t)rows * (n.g.rb / 16) - (ptrdiff_t)nu * 16;
-      f.sc_lo += sc;
-      f.sc_hi += sc;
-      f.groups += nu * 8;
-    }
-  } else {
-    feed_task<FMT>(p, sh, n, f);
-  }
+  feed_run<FMT>(p, sh, n, f);
   __syncwarp();
   st = n;
   __syncwarp();
@@ -429,12 +429,11 @@ template <int FMT, int DEPTH>
 __device__ __forceinline__ void feed_step(const FewParams &p, Shared *sh, Feed &f, uint32_t ring) {
   if (f.left > 0) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const bool q4 = FMT == Q4;              // (a 4-bit layer has no shared expert)
     const uint32_t slot = ring + (f.issued % DEPTH) * unit_bytes(FMT);
     // 4-bit pieces: lane (g, c) keeps its 16 bytes so that the eight bytes that
     // the lanes of four rows read at once lie in different banks
-    const uint32_t dst = slot + (q4 ? g * 64 + ((c ^ (g & 2)) << 4) : lane * 16);
-    const int rest = f.left == 1 ? sh->feed[threadIdx.x >> 5].nseg % SEGS : 0;      // of the task's last unit
+    const uint32_t dst = slot + (FMT == Q4 ? g * 64 + ((c ^ (g & 2)) << 4) : lane * 16);
+    const int rest = f.left == 1 ? f.flags >> 8 : 0;
     if ((f.flags & FULL) && rest == 0) {
 #pragma unroll
       for (int s = 0; s < SEGS; ++s) {
@@ -451,9 +450,7 @@ __device__ __forceinline__ void feed_step(const FewParams &p, Shared *sh, Feed &
     }
     f.lo += UNIT;
     f.hi += UNIT;
-    if (q4) {
-      // a row of an odd number of groups: row g's first is the high half of its word
-      const bool odd = (sh->feed[threadIdx.x >> 5].g.rb / 32 & 1) && (g & 1);
+    if (FMT == Q4) {                        // (no shared expert here: every part is of 4-bit rows)
       const uint32_t d = slot + ROWS * UNIT + lane * 32;
       if (f.groups > 0) {
         const bool down = f.flags & DOWN;
@@ -463,7 +460,7 @@ __device__ __forceinline__ void feed_step(const FewParams &p, Shared *sh, Feed &
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           cp_async4(d + q * 4, base[q]);
-          if (odd && f.groups > 1) cp_async4(d + 16 + q * 4, base[q] + 4);
+          if ((f.flags & ODD) && f.groups > 1) cp_async4(d + 16 + q * 4, base[q] + 4);
         }
       }
       f.sc_lo += 16;
@@ -471,7 +468,20 @@ __device__ __forceinline__ void feed_step(const FewParams &p, Shared *sh, Feed &
       f.groups -= 8;
     }
     ++f.issued;
-    if (--f.left == 0) f = feed_next<FMT>(p, sh, f);
+    if (--f.left == 0) {
+      if (--f.run > 0) {
+        f.lo += f.step;
+        f.hi += f.step;
+        f.left = f.nu;
+        if (FMT == Q4) {
+          f.sc_lo += f.sc_step;
+          f.sc_hi += f.sc_step;
+          f.groups += f.nu * 8;
+        }
+      } else {
+        f = feed_next<FMT>(p, sh, f);
+      }
+    }
   }
   cp_async_commit();
 }
@@ -544,14 +554,6 @@ template <int FMT>
 __host__ __device__ constexpr int ratio_of() {
   return FMT == Q4 ? 2 : 1;
 }
-// segments whose token operand a warp holds at once (4-bit: four times the
-// registers each, and a body of a few hundred instructions per segment, which
-// stays in the instruction cache only if it is a loop's)
-template <int FMT>
-__host__ __device__ constexpr int held_of(bool lo, int NB) {
-  return FMT == Q4 ? 1 : (lo || NB > 1 ? SEGS / 2 : SEGS);
-}
-
 // B operand of one segment: 16 bytes of the token row (bf16 phase 2: and of its
 // low part).  4-bit: a segment is two groups of 64 codes; 16 bytes of each
 // digit per group.
@@ -589,14 +591,10 @@ struct Acc<I8, NB> {
 // segment's slots (4-bit: row g's); left: bytes of the rows from the segment
 // on.  4-bit: sw, the lane's scale words of the segment (s and b of row g, of
 // row g + 8, two groups each), and gs(n, q, j), the sum of token 2c + j of
-// block n over the segment's group q.  The first NBP blocks of eight tokens
-// have their operand in registers; a further one (4-bit weights, whose operand
-// is four times as long, and only for an expert that more than eight tokens
-// chose) fetches it here from `far`.
-template <int FMT, bool LO, int NB, int NBP, bool CHECK, class Sums>
-__device__ __forceinline__ void consume(Acc<FMT, NB> &acc, const BSeg<FMT, LO> (&bv)[NBP], const char *far, size_t far_second,
-                                        int left, const uint8_t *a, bool second, int g, int c, const uint32_t (&sw)[4],
-                                        Sums gs) {
+// block n over the segment's group q.
+template <int FMT, bool LO, int NB, bool CHECK, class Sums>
+__device__ __forceinline__ void consume(Acc<FMT, NB> &acc, const BSeg<FMT, LO> (&bv)[NB], int left, const uint8_t *a,
+                                        bool second, int g, int c, const uint32_t (&sw)[4], Sums gs) {
   if constexpr (FMT != Q4) {
     uint4 lo = *reinterpret_cast<const uint4 *>(a), hi = *reinterpret_cast<const uint4 *>(a + 512);
     if (CHECK && c * 16 >= left) lo = hi = make_uint4(0u, 0u, 0u, 0u);
@@ -616,8 +614,6 @@ __device__ __forceinline__ void consume(Acc<FMT, NB> &acc, const BSeg<FMT, LO> (
       }
     }
   } else {
-    BSeg<FMT, LO> own;
-    if (NB > NBP && second) load_b<FMT, LO, CHECK>(own, far, far_second, left, c);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       if (CHECK && q * 32 >= left) break;
@@ -638,7 +634,7 @@ __device__ __forceinline__ void consume(Acc<FMT, NB> &acc, const BSeg<FMT, LO> (
         int d[2][4];
 #pragma unroll
         for (int l = 0; l < 2; ++l) {
-          const uint4 b = n < NBP ? bv[n < NBP ? n : 0].v[q][l] : own.v[q][l];
+          const uint4 b = bv[n].v[q][l];
           mma_u8s8_first(d[l], l0, h0, l1, h1, b.x, b.y);
           mma_u8s8(d[l], l2, h2, l3, h3, b.z, b.w);
         }
@@ -705,34 +701,43 @@ __device__ __forceinline__ const float *g_row(const FewParams &p, const Cursor &
   return PHASE2 ? p.hg + (size_t)(cu.row0 + r) * (p.F / 64) : p.xg + (size_t)nth_bit(cu.mask, r) * (p.d / 64);
 }
 
-// What becomes of one finished value: row f of the task's `cols` (with its up
-// projection u where the task holds pairs), token tok.  Returns the magnitude
-// of the stored h (8-bit and 4-bit weights: the row maxima are taken from it).
+// What a finished value is multiplied by: the row's scale (of the token in
+// phase 1, of the row of h in phase 2) and with 8-bit weights the channel's.
+// Fetched when a task begins, for the value that the thread will hold at its end.
+struct Scale {
+  float v, u;
+};
 template <int FMT, bool PHASE2>
-__device__ __forceinline__ float emit(const FewParams &p, const Cursor &cu, int part, bool pairs, int f, int tok, float v,
-                                      float u) {
-  const int col = cu.b * (pairs ? 8 : ROWS) + f;
+__device__ __forceinline__ float row_scale(const FewParams &p, const Cursor &cu, int tok) {
+  if (FMT == BF16 || tok >= cu.rows) return 1.f;
+  if (!PHASE2) return __ldcg(p.xs + nth_bit(cu.mask, tok));
+  const uint32_t top = __ldcg(p.rowmax + cu.row0 + tok);
+  return top >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
+                            : __fdiv_rn(__uint_as_float(top), FMT == Q4 ? DIGITS_MAX : 127.f);
+}
+template <int FMT, bool PHASE2>
+__device__ __forceinline__ Scale scale_of(const FewParams &p, const Cursor &cu, bool pairs, int col, float row) {
+  Scale s{row, row};
+  if (FMT == I8 && col < (PHASE2 ? p.d : p.F)) {
+    const size_t r0 = (size_t)cu.e * (PHASE2 ? p.d : p.w_stride) + col;
+    s.v *= __ldg(static_cast<const float *>(PHASE2 ? p.s3 : p.s1) + r0);
+    if (pairs) s.u *= __ldg(static_cast<const float *>(p.s2) + r0);
+  }
+  return s;
+}
+
+// What becomes of one finished value: column col of token tok (with its up
+// projection u where the task holds pairs).  Returns the magnitude of the
+// stored h (8-bit and 4-bit weights: the row maxima are taken from it).
+template <int FMT, bool PHASE2>
+__device__ __forceinline__ float emit(const FewParams &p, const Cursor &cu, int part, bool pairs, int col, int tok, float v,
+                                      float u, Scale s) {
   const int N = PHASE2 ? p.d : (part == S1 ? p.Fs : p.F);
   if (tok >= cu.rows || col >= N) return 0.f;
   const size_t row = (size_t)cu.row0 + tok;
   if (FMT != BF16) {
-    // row scale: of the token (phase 1), of the row of h (phase 2)
-    float xs;
-    if (PHASE2) {
-      const uint32_t top = __ldcg(p.rowmax + row);
-      xs = top >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
-                              : __fdiv_rn(__uint_as_float(top), FMT == Q4 ? DIGITS_MAX : 127.f);
-    } else {
-      xs = __ldcg(p.xs + nth_bit(cu.mask, tok));
-    }
-    if (FMT == I8) {
-      const size_t r0 = (size_t)cu.e * (PHASE2 ? p.d : p.w_stride) + col;
-      if (pairs) u *= xs * __ldg(static_cast<const float *>(p.s2) + r0);
-      xs *= __ldg(static_cast<const float *>(PHASE2 ? p.s3 : p.s1) + r0);
-    } else if (pairs) {
-      u *= xs;
-    }
-    v *= xs;
+    v *= s.v;
+    if (pairs) u *= s.u;
   }
   if (PHASE2) {
     p.y[(part == S2 ? (size_t)p.ksplit * p.y_rows + tok : (size_t)cu.kp * p.y_rows + row) * p.d + col] = v;
@@ -755,6 +760,11 @@ __device__ __forceinline__ float emit(const FewParams &p, const Cursor &cu, int 
   return __bfloat162float(hi);
 }
 
+// One barrier of a group's warps (of the two groups, in turn numbers 1 and 2)
+__device__ __forceinline__ void group_sync() {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + (threadIdx.x >> 5) / GW), "n"(32 * GW) : "memory");
+}
+
 // The block's tasks of one part (of phase 1 or 2).  RFMT: the routed experts'
 // format, which the stream may go on to.
 template <int FMT, int RFMT, bool PHASE2, int NB, int DEPTH>
@@ -762,151 +772,141 @@ __device__ __noinline__ Feed consume_part(const FewParams &p, Shared *sh, uint8_
                                           int part) {
   uint32_t red_it = red_it_ref;
   constexpr bool LO = PHASE2 && FMT == BF16;
-  constexpr int NBP = FMT == Q4 ? 1 : NB;   // blocks of eight tokens whose operand is fetched ahead
   constexpr int R = ratio_of<FMT>();
-  constexpr int HELD = held_of<FMT>(LO, NB);
   const Geo g = part_geo<FMT>(p, part, sh->nact);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, c = lane & 3;
   const uint32_t ring = smem_u32(ring_ptr);
   const size_t lo_bytes = FMT == Q4 ? (PHASE2 ? p.F : p.d) : 2 * (part == S2 ? p.hs_lo : p.h_lo);   // to the low part or digit
-  const bool even = g.rb % SEG == 0;        // whole segments only
   const bool odd_groups = FMT == Q4 && (g.rb / 32 & 1) && (lg & 1);
   const bool pairs = !PHASE2 && (part == S1 || p.swiglu);
   const bool top_of_h = FMT != BF16 && part == R1;
-  const int stride = g.solo ? CW : 1;
-  const int lane_b = c * 16;
+  const int by = task_stride(g);
+  const int cols = pairs ? 8 : ROWS;        // outputs of a task
   const int KG = g.rb / 32;                 // 4-bit: groups of a row
+  // long rows: this thread of its group sums up output (value) number id and,
+  // with more than eight tokens, maybe one 256 further
+  const int id0 = threadIdx.x % (32 * GW);
 
-  // a task's token rows at this lane, from the warp's first segment on
-  auto enter = [&](int j, Cursor &cu, Span &w, const char *(&rp)[NB]) {
-    cu = cursor_of(p, sh, g, part, g.first + j);
-    w = warp_span(g, cu.kp, warp);
+  for (int j = first_task(g, warp); j < g.n;) {
+    // a run of tasks of one expert (and part of K): the same tokens, the same place in K
+    Cursor cu = cursor_of(p, sh, g, part, g.first + j);
+    const Span w = warp_span(g, cu.kp, warp);
+    const int run = run_of(g, j, cu.b);
+    const bool second = cu.rows > 8;
+    const char *rowp[NB];
 #pragma unroll
-    for (int n = 0; n < NB; ++n) rp[n] = b_row<FMT, PHASE2>(p, cu, part, lg + 8 * n) + lane_b + (size_t)w.first * SEG * R;
-  };
-
-  int j = g.solo ? warp : 0;
-  if (j < g.n) {
-    Cursor cu;
-    Span w;
-    const char *rowp[NB];                   // the task's, and the unit's place in them
-    enter(j, cu, w, rowp);
-    const char *bp[NB];
+    for (int n = 0; n < NB; ++n) rowp[n] = b_row<FMT, PHASE2>(p, cu, part, lg + 8 * n) + c * 16 + (size_t)w.first * SEG * R;
+    const float *sums[NB];
+    if constexpr (FMT == Q4) {
 #pragma unroll
-    for (int n = 0; n < NB; ++n) bp[n] = rowp[n];
-    // 4-bit: sums of the lane's token rows over groups c and c + 4 of a unit's
-    // eight, fetched a unit ahead
-    float gsum[NB][2];
-    auto load_sums = [&](const Cursor &cc, int group) {
+      for (int n = 0; n < NB; ++n) sums[n] = g_row<PHASE2>(p, cu, lg + 8 * n) + 2 * w.first + c;
+    }
+    // whole units of the warp's span: the rest, and a last segment that is not
+    // whole, go through the checked path
+    const bool uneven = g.rb % SEG != 0 && w.first + w.n == g.ns;
+    const int whole = (w.n - (uneven ? 1 : 0)) / SEGS;
+    float row_sc[NB][2];                    // solo: of tokens 2c, 2c + 1 of each block
+    if (FMT != BF16 && g.solo) {
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        if (n > 0 && cc.rows <= 8) break;
-        const float *row = g_row<PHASE2>(p, cc, lg + 8 * n) + group + c;
-        gsum[n][0] = group + c < KG ? __ldcg(row) : 0.f;
-        gsum[n][1] = group + c + 4 < KG ? __ldcg(row + 4) : 0.f;
+        row_sc[n][0] = row_scale<FMT, PHASE2>(p, cu, 8 * n + 2 * c);
+        row_sc[n][1] = row_scale<FMT, PHASE2>(p, cu, 8 * n + 2 * c + 1);
       }
-    };
-    if constexpr (FMT == Q4) load_sums(cu, 2 * w.first);
-    BSeg<FMT, LO> bv[HELD][NBP];
-#pragma unroll
-    for (int s = 0; s < HELD; ++s)
-#pragma unroll
-      for (int n = 0; n < NBP; ++n)
-        load_b<FMT, LO, true>(bv[s][n], rowp[n] + s * SEG * R, lo_bytes, g.rb - (w.first + s) * SEG, c);
-    for (;;) {
+    }
+    for (int r = 0; r < run; ++r, cu.b += by) {
       Acc<FMT, NB> acc;
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc.f[n][0][i] = acc.f[n][1][i] = 0;
-      const bool second = cu.rows > 8;
-      const bool more = j + stride < g.n;
-      // the next task, whose first token operand is fetched during this one's
-      // last unit: usually the same expert's next rows
-      Cursor nc = cu;
-      Span nw = w;
-      const char *nrow[NB];
+      // the scales of what this thread will hold at the end
+      Scale sc[2]{{1.f, 1.f}, {1.f, 1.f}};
+      const int id = (id0 + 64 * red_it) % (32 * GW);     // (other warps from task to task)
+      if (FMT == I8) {
+        if (g.solo) {
+          sc[0] = scale_of<FMT, PHASE2>(p, cu, pairs, cu.b * cols + lg, 1.f);
+          if (!pairs) sc[1] = scale_of<FMT, PHASE2>(p, cu, pairs, cu.b * cols + lg + 8, 1.f);
+        } else if (id < cols * 8) {
+          sc[0] = scale_of<FMT, PHASE2>(p, cu, pairs, cu.b * cols + (id & (cols - 1)),
+                                        row_scale<FMT, PHASE2>(p, cu, id >> (pairs ? 3 : 4)));
+        }
+      }
+      const char *bp[NB];
 #pragma unroll
-      for (int n = 0; n < NB; ++n) nrow[n] = rowp[n];
-      nc.b += stride;
-      if (more && nc.b >= g.nb) enter(j + stride, nc, nw, nrow);
-      const int nu = (w.n + SEGS - 1) / SEGS;
-      int seg = 0;
-      for (int u = 0; u < nu; ++u, seg += SEGS) {
-        const bool last = u + 1 == nu;
-        // the segments of this unit, and of the one after it
-        const int n_seg = w.n - seg, next_seg = last ? (more ? nw.n : 0) : n_seg - SEGS;
-        const char *bn[NB];
-#pragma unroll
-        for (int n = 0; n < NB; ++n) bn[n] = last ? nrow[n] : bp[n] + UNIT * R;
+      for (int n = 0; n < NB; ++n) bp[n] = rowp[n];
+      for (int u = 0; u * SEGS < w.n; ++u) {
         const uint8_t *slot = ring_ptr + (f.used % DEPTH) * unit_bytes(RFMT);
-        cp_async_wait<DEPTH - 1>();
-        if (FMT == Q4) __syncwarp();
         const uint8_t *a = FMT == Q4 ? slot + lg * 64 : slot + lane * 16;
-        float now[NB][2];
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          now[n][0] = gsum[n][0];
-          now[n][1] = gsum[n][1];
-        }
+        float gsum[NB][2] = {};             // 4-bit: sums of the lane's token rows over groups c, c + 4 of the unit
         if constexpr (FMT == Q4) {
-          if (!last) load_sums(cu, 2 * (w.first + seg + SEGS));
-          else if (more) load_sums(nc, 2 * nw.first);
+#pragma unroll
+          for (int n = 0; n < NB; ++n) {
+            if (n > 0 && !second) break;
+            const int at = 2 * (w.first + u * SEGS) + c;
+            gsum[n][0] = at < KG ? __ldcg(sums[n] + u * 8) : 0.f;
+            gsum[n][1] = at + 4 < KG ? __ldcg(sums[n] + u * 8 + 4) : 0.f;
+          }
         }
-        uint32_t sw[4] = {0u, 0u, 0u, 0u};
-        auto scales = [&](int s) {
-          const uint4 *t = reinterpret_cast<const uint4 *>(slot + ROWS * UNIT + (lg * 4 + s) * 32);
-          const uint4 x = t[0];
-          sw[0] = x.x; sw[1] = x.y; sw[2] = x.z; sw[3] = x.w;
-          if (odd_groups) {
-            const uint4 y = t[1];
-            sw[0] = __funnelshift_r(x.x, y.x, 16); sw[1] = __funnelshift_r(x.y, y.y, 16);
-            sw[2] = __funnelshift_r(x.z, y.z, 16); sw[3] = __funnelshift_r(x.w, y.w, 16);
-          }
-        };
-        const int row_left = g.rb - (w.first + seg) * SEG;               // bytes of the row from here on
-        const int next_left = last ? g.rb - nw.first * SEG : row_left - UNIT;
-        auto step = [&](int s, auto check) {
-          constexpr bool CHECK = decltype(check)::value;
-          if (s < n_seg) {
-            if constexpr (FMT == Q4) scales(s);
-            consume<FMT, LO, NB, NBP, CHECK>(
-                acc, bv[s % HELD], bp[NB - 1] + s * SEG * R, lo_bytes, row_left - s * SEG, a + s * 1024, second, lg, c, sw,
-                [&](int n, int q, int j) {              // group 2 s + q of the unit, held by the lanes of quad column
-                  return __shfl_sync(0xffffffffu, s < 2 ? now[n][0] : now[n][1], c * 8 + j * 4 + (2 * s + q) % 4);
-                });
-          }
-          // the operand of the segment HELD further on takes its registers
-          const int t = s + HELD;
-          if (t < SEGS ? t < n_seg : t - SEGS < next_seg) {
-#pragma unroll
-            for (int n = 0; n < NBP; ++n)
-              load_b<FMT, LO, CHECK>(bv[s % HELD][n], t < SEGS ? bp[n] + t * SEG * R : bn[n] + (t - SEGS) * SEG * R, lo_bytes,
-                                     (t < SEGS ? row_left : next_left) - (t % SEGS) * SEG, c);
-          }
-        };
-        if (even) {
+        auto segment = [&](int s, const BSeg<FMT, LO>(&bv)[NB], int left, auto check) {
+          uint32_t sw[4] = {0u, 0u, 0u, 0u};
           if constexpr (FMT == Q4) {
-#pragma unroll 1
-            for (int s = 0; s < SEGS; ++s) step(s, std::false_type{});
-          } else {
+            const uint4 *t = reinterpret_cast<const uint4 *>(slot + ROWS * UNIT + (lg * 4 + s) * 32);
+            const uint4 x = t[0];
+            sw[0] = x.x; sw[1] = x.y; sw[2] = x.z; sw[3] = x.w;
+            if (odd_groups) {
+              const uint4 y = t[1];
+              sw[0] = __funnelshift_r(x.x, y.x, 16); sw[1] = __funnelshift_r(x.y, y.y, 16);
+              sw[2] = __funnelshift_r(x.z, y.z, 16); sw[3] = __funnelshift_r(x.w, y.w, 16);
+            }
+          }
+          consume<FMT, LO, NB, decltype(check)::value>(
+              acc, bv, left, a + s * 1024, second, lg, c, sw, [&](int n, int q, int i) {
+                // group 2 s + q of the unit, held by the lanes of one quad column
+                return __shfl_sync(0xffffffffu, s < 2 ? gsum[n][0] : gsum[n][1], c * 8 + i * 4 + (2 * s + q) % 4);
+              });
+        };
+        if (u < whole) {
+          // the token operand is on its way while the weights are waited for
+          constexpr int HELD = FMT == Q4 ? 1 : (LO && NB > 1 ? 2 : SEGS);
+          BSeg<FMT, LO> bv[HELD][NB];
 #pragma unroll
-            for (int s = 0; s < SEGS; ++s) step(s, std::false_type{});
+          for (int s = 0; s < HELD; ++s)
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+              if (n == 0 || second) load_b<FMT, LO, false>(bv[s][n], bp[n] + s * SEG * R, lo_bytes, SEG, c);
+          cp_async_wait<DEPTH - 1>();
+          if (FMT == Q4) __syncwarp();
+#pragma unroll
+          for (int s0 = 0; s0 < SEGS; s0 += HELD) {
+            if (s0 > 0) {
+#pragma unroll
+              for (int s = 0; s < HELD; ++s)
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+                  if (n == 0 || second) load_b<FMT, LO, false>(bv[s][n], bp[n] + (s0 + s) * SEG * R, lo_bytes, SEG, c);
+            }
+#pragma unroll
+            for (int s = 0; s < HELD; ++s) segment(s0 + s, bv[s], SEG, std::false_type{});
           }
         } else {
-          if constexpr (FMT == Q4) {
+          const int n_seg = min(SEGS, w.n - u * SEGS);
+          const int left = g.rb - (w.first + u * SEGS) * SEG;        // bytes of the row from here on
+          cp_async_wait<DEPTH - 1>();
+          if (FMT == Q4) __syncwarp();
 #pragma unroll 1
-            for (int s = 0; s < SEGS; ++s) step(s, std::true_type{});
-          } else {
+          for (int s = 0; s < n_seg; ++s) {
+            BSeg<FMT, LO> bv[NB];
 #pragma unroll
-            for (int s = 0; s < SEGS; ++s) step(s, std::true_type{});
+            for (int n = 0; n < NB; ++n)
+              if (n == 0 || second) load_b<FMT, LO, true>(bv[n], bp[n] + s * SEG * R, lo_bytes, left - s * SEG, c);
+            segment(s, bv, left - s * SEG, std::true_type{});
           }
         }
         if (FMT == Q4) __syncwarp();
+#pragma unroll
+        for (int n = 0; n < NB; ++n) bp[n] += UNIT * R;
         ++f.used;
         feed_step<RFMT, DEPTH>(p, sh, f, ring);
-#pragma unroll
-        for (int n = 0; n < NB; ++n) bp[n] = bn[n];
       }
       if (g.solo) {
         // accumulators 0, 1: row g, tokens 2c, 2c + 1; 2, 3: row g + 8
@@ -918,8 +918,11 @@ __device__ __noinline__ Feed consume_part(const FewParams &p, Shared *sh, uint8_
             const int tok = 8 * n + 2 * c + i;
             const float v0 = (float)(acc.f[n][0][i] + acc.f[n][1][i]);
             const float v1 = (float)(acc.f[n][0][i + 2] + acc.f[n][1][i + 2]);
-            float m = emit<FMT, PHASE2>(p, cu, part, pairs, lg, tok, v0, v1);
-            if (!pairs) m = abs_max(m, emit<FMT, PHASE2>(p, cu, part, pairs, lg + 8, tok, v1, 0.f));
+            const float rs = FMT != BF16 ? row_sc[n][i] : 1.f;
+            float m = emit<FMT, PHASE2>(p, cu, part, pairs, cu.b * cols + lg, tok, v0, v1, {sc[0].v * rs, sc[0].u * rs});
+            if (!pairs)
+              m = abs_max(m, emit<FMT, PHASE2>(p, cu, part, pairs, cu.b * cols + lg + 8, tok, v1, 0.f,
+                                               {sc[1].v * rs, 1.f}));
             if (top_of_h) {
               uint32_t top = __float_as_uint(m) & 0x7FFFFFFFu;
 #pragma unroll
@@ -929,11 +932,12 @@ __device__ __noinline__ Feed consume_part(const FewParams &p, Shared *sh, uint8_
           }
         }
       } else {
-        // the warps' partial results meet; two buffers in turn, so one
+        // the group's partial results meet; two buffers in turn, so one
         // barrier per task keeps writers and readers apart
-        uint32_t(*red)[NB][32][4] = reinterpret_cast<Partial<NB> *>(partials(sh))->red[red_it & 1u];
+        uint32_t(*red)[NB][32][4] = &reinterpret_cast<Partial<NB> *>(partials(sh))->red[red_it & 1u][warp / GW * GW];
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
+          if (n > 0 && !second) break;
           uint32_t v[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -941,9 +945,9 @@ __device__ __noinline__ Feed consume_part(const FewParams &p, Shared *sh, uint8_
             if constexpr (FMT == I8) v[i] = (uint32_t)sum;
             else v[i] = __float_as_uint(sum);
           }
-          *reinterpret_cast<uint4 *>(red[warp][n][lane]) = make_uint4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<uint4 *>(red[warp % GW][n][lane]) = make_uint4(v[0], v[1], v[2], v[3]);
         }
-        __syncthreads();
+        group_sync();
         ++red_it;
         // value (row, token) of the task: accumulator i of lane 4 (row % 8) + (token % 8) / 2
         auto total = [&](int row, int tok) {
@@ -951,21 +955,23 @@ __device__ __noinline__ Feed consume_part(const FewParams &p, Shared *sh, uint8_
           if (FMT == I8) {
             int v = 0;
 #pragma unroll
-            for (int q = 0; q < CW; ++q) v += (int)red[q][n][ln][i];
+            for (int q = 0; q < GW; ++q) v += (int)red[q][n][ln][i];
             return (float)v;
           }
           float v = 0.f;
 #pragma unroll
-          for (int q = 0; q < CW; ++q) v += __uint_as_float(red[q][n][ln][i]);
+          for (int q = 0; q < GW; ++q) v += __uint_as_float(red[q][n][ln][i]);
           return v;
         };
-        const int cols = pairs ? 8 : ROWS;
-        const int most = cols * 8 * (second ? 2 : 1);
-        // (whole warps, other ones from task to task: the scales they fetch are not waited for by all)
-        for (int i = (threadIdx.x + 64 * red_it) % CT; i < most; i += CT) {
-          const int tok = i >> (pairs ? 3 : 4), q = i & (cols - 1);
-          const float m =
-              tok < cu.rows ? emit<FMT, PHASE2>(p, cu, part, pairs, q, tok, total(q, tok), pairs ? total(q + 8, tok) : 0.f) : 0.f;
+        const int most = cols * 8 * (second ? 2 : 1);               // (at most the group's threads)
+        if (id < most) {
+          const int tok = id >> (pairs ? 3 : 4), q = id & (cols - 1);
+          if (FMT != BF16 && (FMT == Q4 || id >= cols * 8))
+            sc[0] = scale_of<FMT, PHASE2>(p, cu, pairs, cu.b * cols + q, row_scale<FMT, PHASE2>(p, cu, tok));
+          float m = 0.f;
+          if (tok < cu.rows)
+            m = emit<FMT, PHASE2>(p, cu, part, pairs, cu.b * cols + q, tok, total(q, tok), pairs ? total(q + 8, tok) : 0.f,
+                                  sc[0]);
           if (top_of_h) {
             // the row's largest |h|: over the task's columns (8 or 16 neighbouring lanes), then the grid
             uint32_t top = __float_as_uint(m) & 0x7FFFFFFFu;
@@ -974,13 +980,8 @@ __device__ __noinline__ Feed consume_part(const FewParams &p, Shared *sh, uint8_
           }
         }
       }
-      if (!more) break;
-      j += stride;
-      cu = nc;
-      w = nw;
-#pragma unroll
-      for (int n = 0; n < NB; ++n) rowp[n] = nrow[n];
     }
+    j += run * by;
   }
   red_it_ref = red_it;
   return f;
