@@ -517,18 +517,10 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
       : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// unsigned codes times signed digits
-__device__ __forceinline__ void mma_u8s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 // with a zero accumulator
-__device__ __forceinline__ void mma_u8s8_first(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+__device__ __forceinline__ void mma_s8_first(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%10, %10, %10, %10};"
       : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
@@ -635,8 +627,8 @@ __device__ __forceinline__ void consume(Acc<FMT, NB> &acc, const BSeg<FMT, LO> (
 #pragma unroll
         for (int l = 0; l < 2; ++l) {
           const uint4 b = bv[n].v[q][l];
-          mma_u8s8_first(d[l], l0, h0, l1, h1, b.x, b.y);
-          mma_u8s8(d[l], l2, h2, l3, h3, b.z, b.w);
+          mma_s8_first(d[l], l0, h0, l1, h1, b.x, b.y);
+          mma_s8(d[l], l2, h2, l3, h3, b.z, b.w);
         }
         const float g0 = gs(n, q, 0), g1 = gs(n, q, 1);
         float(&t)[4] = acc.f[n][q];
@@ -866,27 +858,33 @@ __device__ __noinline__ Feed consume_part(const FewParams &p, Shared *sh, uint8_
               });
         };
         if (u < whole) {
-          // the token operand is on its way while the weights are waited for
-          constexpr int HELD = FMT == Q4 ? 1 : (LO && NB > 1 ? 2 : SEGS);
-          BSeg<FMT, LO> bv[HELD][NB];
+          if constexpr (FMT == Q4) {
+            cp_async_wait<DEPTH - 1>();
+            __syncwarp();
+            // (rolled: the body is long, and fetching instructions would cost more)
+#pragma unroll 1
+            for (int s = 0; s < SEGS; ++s) {
+              BSeg<FMT, LO> bv[NB];
 #pragma unroll
-          for (int s = 0; s < HELD; ++s)
+              for (int n = 0; n < NB; ++n)
+                if (n == 0 || second) load_b<FMT, LO, false>(bv[n], bp[n] + s * SEG * R, lo_bytes, SEG, c);
+              segment(s, bv, SEG, std::false_type{});
+            }
+          } else {
+            // the token operand is on its way while the weights are waited for
+            constexpr int HELD = LO && NB > 1 ? 2 : SEGS;
+            BSeg<FMT, LO> bv[HELD][NB];
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
-              if (n == 0 || second) load_b<FMT, LO, false>(bv[s][n], bp[n] + s * SEG * R, lo_bytes, SEG, c);
-          cp_async_wait<DEPTH - 1>();
-          if (FMT == Q4) __syncwarp();
-#pragma unroll
-          for (int s0 = 0; s0 < SEGS; s0 += HELD) {
-            if (s0 > 0) {
+            for (int s0 = 0; s0 < SEGS; s0 += HELD) {
 #pragma unroll
               for (int s = 0; s < HELD; ++s)
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
                   if (n == 0 || second) load_b<FMT, LO, false>(bv[s][n], bp[n] + (s0 + s) * SEG * R, lo_bytes, SEG, c);
-            }
+              if (s0 == 0) cp_async_wait<DEPTH - 1>();
 #pragma unroll
-            for (int s = 0; s < HELD; ++s) segment(s0 + s, bv[s], SEG, std::false_type{});
+              for (int s = 0; s < HELD; ++s) segment(s0 + s, bv[s], SEG, std::false_type{});
+            }
           }
         } else {
           const int n_seg = min(SEGS, w.n - u * SEGS);
