@@ -586,13 +586,12 @@ struct Acc<I8, NB> {
 // block n over the segment's group q.
 template <int FMT, bool LO, int NB, bool CHECK, class Sums>
 __device__ __forceinline__ void consume(Acc<FMT, NB> &acc, const BSeg<FMT, LO> (&bv)[NB], int left, const uint8_t *a,
-                                        bool second, int g, int c, const uint32_t (&sw)[4], Sums gs) {
+                                        int g, int c, const uint32_t (&sw)[4], Sums gs) {
   if constexpr (FMT != Q4) {
     uint4 lo = *reinterpret_cast<const uint4 *>(a), hi = *reinterpret_cast<const uint4 *>(a + 512);
     if (CHECK && c * 16 >= left) lo = hi = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-      if (n > 0 && !second) break;
 #pragma unroll
       for (int l = 0; l < (LO ? 2 : 1); ++l) {
         const uint4 b = bv[n].v[0][l];
@@ -622,7 +621,6 @@ __device__ __forceinline__ void consume(Acc<FMT, NB> &acc, const BSeg<FMT, LO> (
       const float b_hi = __uint_as_float(q ? sw[3] & 0xFFFF0000u : sw[3] << 16);
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        if (n > 0 && !second) break;
         int d[2][4];
 #pragma unroll
         for (int l = 0; l < 2; ++l) {
@@ -757,231 +755,240 @@ __device__ __forceinline__ void group_sync() {
   asm volatile("bar.sync %0, %1;" ::"r"(1 + (threadIdx.x >> 5) / GW), "n"(32 * GW) : "memory");
 }
 
-// The block's tasks of one part (of phase 1 or 2).  RFMT: the routed experts'
-// format, which the stream may go on to.
-template <int FMT, int RFMT, bool PHASE2, int NB, int DEPTH>
-__device__ __noinline__ Feed consume_part(const FewParams &p, Shared *sh, uint8_t *ring_ptr, Feed f, uint32_t &red_it_ref,
-                                          int part) {
+// A run of a warp's tasks: `run` of them, every by-th row block from cu.b on, of
+// one expert (and part of K): the same tokens, the same place in K.  NB blocks
+// of eight tokens, MAXNB the most of any run (the layout of the meeting place).
+// RFMT: the routed experts' format, which the stream may go on to.
+template <int FMT, int RFMT, bool PHASE2, int NB, int MAXNB, int DEPTH>
+__device__ __noinline__ Feed consume_run(const FewParams &p, Shared *sh, uint8_t *ring_ptr, Feed f, uint32_t &red_it_ref,
+                                         int part, const Geo &geo, Cursor cu, int run) {
   uint32_t red_it = red_it_ref;
   constexpr bool LO = PHASE2 && FMT == BF16;
   constexpr int R = ratio_of<FMT>();
-  const Geo g = part_geo<FMT>(p, part, sh->nact);
+  const bool solo = geo.solo;
+  const int rb = geo.rb;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, c = lane & 3;
   const uint32_t ring = smem_u32(ring_ptr);
   const size_t lo_bytes = FMT == Q4 ? (PHASE2 ? p.F : p.d) : 2 * (part == S2 ? p.hs_lo : p.h_lo);   // to the low part or digit
-  const bool odd_groups = FMT == Q4 && (g.rb / 32 & 1) && (lg & 1);
+  const bool odd_groups = FMT == Q4 && (rb / 32 & 1) && (lg & 1);
   const bool pairs = !PHASE2 && (part == S1 || p.swiglu);
   const bool top_of_h = FMT != BF16 && part == R1;
-  const int by = task_stride(g);
+  const int by = task_stride(geo);
   const int cols = pairs ? 8 : ROWS;        // outputs of a task
-  const int KG = g.rb / 32;                 // 4-bit: groups of a row
+  const int KG = rb / 32;                   // 4-bit: groups of a row
   // long rows: this thread of its group sums up output (value) number id and,
   // with more than eight tokens, maybe one 256 further
   const int id0 = threadIdx.x % (32 * GW);
-
-  for (int j = first_task(g, warp); j < g.n;) {
-    // a run of tasks of one expert (and part of K): the same tokens, the same place in K
-    Cursor cu = cursor_of(p, sh, g, part, g.first + j);
-    const Span w = warp_span(g, cu.kp, warp);
-    const int run = run_of(g, j, cu.b);
-    const bool second = cu.rows > 8;
-    const char *rowp[NB];
+  constexpr bool second = NB > 1;
+  const Span w = warp_span(geo, cu.kp, warp);
+  const char *rowp[NB];
 #pragma unroll
-    for (int n = 0; n < NB; ++n) rowp[n] = b_row<FMT, PHASE2>(p, cu, part, lg + 8 * n) + c * 16 + (size_t)w.first * SEG * R;
-    const float *sums[NB];
-    if constexpr (FMT == Q4) {
+  for (int n = 0; n < NB; ++n) rowp[n] = b_row<FMT, PHASE2>(p, cu, part, lg + 8 * n) + c * 16 + (size_t)w.first * SEG * R;
+  const float *sums[NB];
+  if constexpr (FMT == Q4) {
 #pragma unroll
-      for (int n = 0; n < NB; ++n) sums[n] = g_row<PHASE2>(p, cu, lg + 8 * n) + 2 * w.first + c;
+    for (int n = 0; n < NB; ++n) sums[n] = g_row<PHASE2>(p, cu, lg + 8 * n) + 2 * w.first + c;
+  }
+  // whole units of the warp's span: the rest, and a last segment that is not
+  // whole, go through the checked path
+  const bool uneven = rb % SEG != 0 && w.first + w.n == geo.ns;
+  const int whole = (w.n - (uneven ? 1 : 0)) / SEGS;
+  float row_sc[NB][2];                      // solo: of tokens 2c, 2c + 1 of each block
+  if (FMT != BF16 && solo) {
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      row_sc[n][0] = row_scale<FMT, PHASE2>(p, cu, 8 * n + 2 * c);
+      row_sc[n][1] = row_scale<FMT, PHASE2>(p, cu, 8 * n + 2 * c + 1);
     }
-    // whole units of the warp's span: the rest, and a last segment that is not
-    // whole, go through the checked path
-    const bool uneven = g.rb % SEG != 0 && w.first + w.n == g.ns;
-    const int whole = (w.n - (uneven ? 1 : 0)) / SEGS;
-    float row_sc[NB][2];                    // solo: of tokens 2c, 2c + 1 of each block
-    if (FMT != BF16 && g.solo) {
+  }
+  for (int r = 0; r < run; ++r, cu.b += by) {
+    Acc<FMT, NB> acc;
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        row_sc[n][0] = row_scale<FMT, PHASE2>(p, cu, 8 * n + 2 * c);
-        row_sc[n][1] = row_scale<FMT, PHASE2>(p, cu, 8 * n + 2 * c + 1);
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc.f[n][0][i] = acc.f[n][1][i] = 0;
+    // the scales of what this thread will hold at the end
+    Scale sc[2]{{1.f, 1.f}, {1.f, 1.f}};
+    const int id = (id0 + 64 * red_it) % (32 * GW);     // (other warps from task to task)
+    if (FMT == I8) {
+      if (solo) {
+        sc[0] = scale_of<FMT, PHASE2>(p, cu, pairs, cu.b * cols + lg, 1.f);
+        if (!pairs) sc[1] = scale_of<FMT, PHASE2>(p, cu, pairs, cu.b * cols + lg + 8, 1.f);
+      } else if (id < cols * 8) {
+        sc[0] = scale_of<FMT, PHASE2>(p, cu, pairs, cu.b * cols + (id & (cols - 1)),
+                                      row_scale<FMT, PHASE2>(p, cu, id >> (pairs ? 3 : 4)));
       }
     }
-    for (int r = 0; r < run; ++r, cu.b += by) {
-      Acc<FMT, NB> acc;
+    const char *bp[NB];
 #pragma unroll
-      for (int n = 0; n < NB; ++n)
+    for (int n = 0; n < NB; ++n) bp[n] = rowp[n];
+    for (int u = 0; u * SEGS < w.n; ++u) {
+      const uint8_t *slot = ring_ptr + (f.used % DEPTH) * unit_bytes(RFMT);
+      const uint8_t *a = FMT == Q4 ? slot + lg * 64 : slot + lane * 16;
+      float gsum[NB][2] = {};             // 4-bit: sums of the lane's token rows over groups c, c + 4 of the unit
+      if constexpr (FMT == Q4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc.f[n][0][i] = acc.f[n][1][i] = 0;
-      // the scales of what this thread will hold at the end
-      Scale sc[2]{{1.f, 1.f}, {1.f, 1.f}};
-      const int id = (id0 + 64 * red_it) % (32 * GW);     // (other warps from task to task)
-      if (FMT == I8) {
-        if (g.solo) {
-          sc[0] = scale_of<FMT, PHASE2>(p, cu, pairs, cu.b * cols + lg, 1.f);
-          if (!pairs) sc[1] = scale_of<FMT, PHASE2>(p, cu, pairs, cu.b * cols + lg + 8, 1.f);
-        } else if (id < cols * 8) {
-          sc[0] = scale_of<FMT, PHASE2>(p, cu, pairs, cu.b * cols + (id & (cols - 1)),
-                                        row_scale<FMT, PHASE2>(p, cu, id >> (pairs ? 3 : 4)));
+        for (int n = 0; n < NB; ++n) {
+          const int at = 2 * (w.first + u * SEGS) + c;
+          gsum[n][0] = at < KG ? __ldcg(sums[n] + u * 8) : 0.f;
+          gsum[n][1] = at + 4 < KG ? __ldcg(sums[n] + u * 8 + 4) : 0.f;
         }
       }
-      const char *bp[NB];
-#pragma unroll
-      for (int n = 0; n < NB; ++n) bp[n] = rowp[n];
-      for (int u = 0; u * SEGS < w.n; ++u) {
-        const uint8_t *slot = ring_ptr + (f.used % DEPTH) * unit_bytes(RFMT);
-        const uint8_t *a = FMT == Q4 ? slot + lg * 64 : slot + lane * 16;
-        float gsum[NB][2] = {};             // 4-bit: sums of the lane's token rows over groups c, c + 4 of the unit
+      auto segment = [&](int s, const BSeg<FMT, LO>(&bv)[NB], int left, auto check) {
+        uint32_t sw[4] = {0u, 0u, 0u, 0u};
         if constexpr (FMT == Q4) {
-#pragma unroll
-          for (int n = 0; n < NB; ++n) {
-            if (n > 0 && !second) break;
-            const int at = 2 * (w.first + u * SEGS) + c;
-            gsum[n][0] = at < KG ? __ldcg(sums[n] + u * 8) : 0.f;
-            gsum[n][1] = at + 4 < KG ? __ldcg(sums[n] + u * 8 + 4) : 0.f;
+          const uint4 *t = reinterpret_cast<const uint4 *>(slot + ROWS * UNIT + (lg * 4 + s) * 32);
+          const uint4 x = t[0];
+          sw[0] = x.x; sw[1] = x.y; sw[2] = x.z; sw[3] = x.w;
+          if (odd_groups) {
+            const uint4 y = t[1];
+            sw[0] = __funnelshift_r(x.x, y.x, 16); sw[1] = __funnelshift_r(x.y, y.y, 16);
+            sw[2] = __funnelshift_r(x.z, y.z, 16); sw[3] = __funnelshift_r(x.w, y.w, 16);
           }
         }
-        auto segment = [&](int s, const BSeg<FMT, LO>(&bv)[NB], int left, auto check) {
-          uint32_t sw[4] = {0u, 0u, 0u, 0u};
-          if constexpr (FMT == Q4) {
-            const uint4 *t = reinterpret_cast<const uint4 *>(slot + ROWS * UNIT + (lg * 4 + s) * 32);
-            const uint4 x = t[0];
-            sw[0] = x.x; sw[1] = x.y; sw[2] = x.z; sw[3] = x.w;
-            if (odd_groups) {
-              const uint4 y = t[1];
-              sw[0] = __funnelshift_r(x.x, y.x, 16); sw[1] = __funnelshift_r(x.y, y.y, 16);
-              sw[2] = __funnelshift_r(x.z, y.z, 16); sw[3] = __funnelshift_r(x.w, y.w, 16);
-            }
-          }
-          consume<FMT, LO, NB, decltype(check)::value>(
-              acc, bv, left, a + s * 1024, second, lg, c, sw, [&](int n, int q, int i) {
-                // group 2 s + q of the unit, held by the lanes of one quad column
-                return __shfl_sync(0xffffffffu, s < 2 ? gsum[n][0] : gsum[n][1], c * 8 + i * 4 + (2 * s + q) % 4);
-              });
-        };
-        if (u < whole) {
-          if constexpr (FMT == Q4) {
-            cp_async_wait<DEPTH - 1>();
-            __syncwarp();
-            // (rolled: the body is long, and fetching instructions would cost more)
-#pragma unroll 1
-            for (int s = 0; s < SEGS; ++s) {
-              BSeg<FMT, LO> bv[NB];
-#pragma unroll
-              for (int n = 0; n < NB; ++n)
-                if (n == 0 || second) load_b<FMT, LO, false>(bv[n], bp[n] + s * SEG * R, lo_bytes, SEG, c);
-              segment(s, bv, SEG, std::false_type{});
-            }
-          } else {
-            // the token operand is on its way while the weights are waited for
-            constexpr int HELD = LO && NB > 1 ? 2 : SEGS;
-            BSeg<FMT, LO> bv[HELD][NB];
-#pragma unroll
-            for (int s0 = 0; s0 < SEGS; s0 += HELD) {
-#pragma unroll
-              for (int s = 0; s < HELD; ++s)
-#pragma unroll
-                for (int n = 0; n < NB; ++n)
-                  if (n == 0 || second) load_b<FMT, LO, false>(bv[s][n], bp[n] + (s0 + s) * SEG * R, lo_bytes, SEG, c);
-              if (s0 == 0) cp_async_wait<DEPTH - 1>();
-#pragma unroll
-              for (int s = 0; s < HELD; ++s) segment(s0 + s, bv[s], SEG, std::false_type{});
-            }
-          }
-        } else {
-          const int n_seg = min(SEGS, w.n - u * SEGS);
-          const int left = g.rb - (w.first + u * SEGS) * SEG;        // bytes of the row from here on
+        consume<FMT, LO, NB, decltype(check)::value>(
+            acc, bv, left, a + s * 1024, lg, c, sw, [&](int n, int q, int i) {
+              // group 2 s + q of the unit, held by the lanes of one quad column
+              return __shfl_sync(0xffffffffu, s < 2 ? gsum[n][0] : gsum[n][1], c * 8 + i * 4 + (2 * s + q) % 4);
+            });
+      };
+      if (u < whole) {
+        if constexpr (FMT == Q4) {
           cp_async_wait<DEPTH - 1>();
-          if (FMT == Q4) __syncwarp();
+          __syncwarp();
+          // (rolled: the body is long, and fetching instructions would cost more)
 #pragma unroll 1
-          for (int s = 0; s < n_seg; ++s) {
+          for (int s = 0; s < SEGS; ++s) {
             BSeg<FMT, LO> bv[NB];
 #pragma unroll
             for (int n = 0; n < NB; ++n)
-              if (n == 0 || second) load_b<FMT, LO, true>(bv[n], bp[n] + s * SEG * R, lo_bytes, left - s * SEG, c);
-            segment(s, bv, left - s * SEG, std::true_type{});
+              load_b<FMT, LO, false>(bv[n], bp[n] + s * SEG * R, lo_bytes, SEG, c);
+            segment(s, bv, SEG, std::false_type{});
           }
-        }
-        if (FMT == Q4) __syncwarp();
+        } else {
+          // the token operand is on its way while the weights are waited for
+          constexpr int HELD = LO && NB > 1 ? 2 : SEGS;
+          BSeg<FMT, LO> bv[HELD][NB];
 #pragma unroll
-        for (int n = 0; n < NB; ++n) bp[n] += UNIT * R;
-        ++f.used;
-        feed_step<RFMT, DEPTH>(p, sh, f, ring);
-      }
-      if (g.solo) {
-        // accumulators 0, 1: row g, tokens 2c, 2c + 1; 2, 3: row g + 8
+          for (int s0 = 0; s0 < SEGS; s0 += HELD) {
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          if (n > 0 && !second) break;
+            for (int s = 0; s < HELD; ++s)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int tok = 8 * n + 2 * c + i;
-            const float v0 = (float)(acc.f[n][0][i] + acc.f[n][1][i]);
-            const float v1 = (float)(acc.f[n][0][i + 2] + acc.f[n][1][i + 2]);
-            const float rs = FMT != BF16 ? row_sc[n][i] : 1.f;
-            float m = emit<FMT, PHASE2>(p, cu, part, pairs, cu.b * cols + lg, tok, v0, v1, {sc[0].v * rs, sc[0].u * rs});
-            if (!pairs)
-              m = abs_max(m, emit<FMT, PHASE2>(p, cu, part, pairs, cu.b * cols + lg + 8, tok, v1, 0.f,
-                                               {sc[1].v * rs, 1.f}));
-            if (top_of_h) {
-              uint32_t top = __float_as_uint(m) & 0x7FFFFFFFu;
+              for (int n = 0; n < NB; ++n)
+                load_b<FMT, LO, false>(bv[s][n], bp[n] + (s0 + s) * SEG * R, lo_bytes, SEG, c);
+            if (s0 == 0) cp_async_wait<DEPTH - 1>();
 #pragma unroll
-              for (int o = 4; o < 32; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-              if (lg == 0 && tok < cu.rows) atomicMax(p.rowmax + cu.row0 + tok, top);
-            }
+            for (int s = 0; s < HELD; ++s) segment(s0 + s, bv[s], SEG, std::false_type{});
           }
         }
       } else {
-        // the group's partial results meet; two buffers in turn, so one
-        // barrier per task keeps writers and readers apart
-        uint32_t(*red)[NB][32][4] = &reinterpret_cast<Partial<NB> *>(partials(sh))->red[red_it & 1u][warp / GW * GW];
+        const int n_seg = min(SEGS, w.n - u * SEGS);
+        const int left = rb - (w.first + u * SEGS) * SEG;        // bytes of the row from here on
+        cp_async_wait<DEPTH - 1>();
+        if (FMT == Q4) __syncwarp();
+#pragma unroll 1
+        for (int s = 0; s < n_seg; ++s) {
+          BSeg<FMT, LO> bv[NB];
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          if (n > 0 && !second) break;
-          uint32_t v[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const auto sum = acc.f[n][0][i] + acc.f[n][1][i];
-            if constexpr (FMT == I8) v[i] = (uint32_t)sum;
-            else v[i] = __float_as_uint(sum);
-          }
-          *reinterpret_cast<uint4 *>(red[warp % GW][n][lane]) = make_uint4(v[0], v[1], v[2], v[3]);
+          for (int n = 0; n < NB; ++n)
+            load_b<FMT, LO, true>(bv[n], bp[n] + s * SEG * R, lo_bytes, left - s * SEG, c);
+          segment(s, bv, left - s * SEG, std::true_type{});
         }
-        group_sync();
-        ++red_it;
-        // value (row, token) of the task: accumulator i of lane 4 (row % 8) + (token % 8) / 2
-        auto total = [&](int row, int tok) {
-          const int ln = (row & 7) * 4 + ((tok & 7) >> 1), i = (tok & 1) + (row >> 3) * 2, n = tok >> 3;
-          if (FMT == I8) {
-            int v = 0;
+      }
+      if (FMT == Q4) __syncwarp();
 #pragma unroll
-            for (int q = 0; q < GW; ++q) v += (int)red[q][n][ln][i];
-            return (float)v;
-          }
-          float v = 0.f;
+      for (int n = 0; n < NB; ++n) bp[n] += UNIT * R;
+      ++f.used;
+      feed_step<RFMT, DEPTH>(p, sh, f, ring);
+    }
+    if (solo) {
+      // accumulators 0, 1: row g, tokens 2c, 2c + 1; 2, 3: row g + 8
 #pragma unroll
-          for (int q = 0; q < GW; ++q) v += __uint_as_float(red[q][n][ln][i]);
-          return v;
-        };
-        const int most = cols * 8 * (second ? 2 : 1);               // (at most the group's threads)
-        if (id < most) {
-          const int tok = id >> (pairs ? 3 : 4), q = id & (cols - 1);
-          if (FMT != BF16 && (FMT == Q4 || id >= cols * 8))
-            sc[0] = scale_of<FMT, PHASE2>(p, cu, pairs, cu.b * cols + q, row_scale<FMT, PHASE2>(p, cu, tok));
-          float m = 0.f;
-          if (tok < cu.rows)
-            m = emit<FMT, PHASE2>(p, cu, part, pairs, cu.b * cols + q, tok, total(q, tok), pairs ? total(q + 8, tok) : 0.f,
-                                  sc[0]);
+      for (int n = 0; n < NB; ++n) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int tok = 8 * n + 2 * c + i;
+          const float v0 = (float)(acc.f[n][0][i] + acc.f[n][1][i]);
+          const float v1 = (float)(acc.f[n][0][i + 2] + acc.f[n][1][i + 2]);
+          const float rs = FMT != BF16 ? row_sc[n][i] : 1.f;
+          float m = emit<FMT, PHASE2>(p, cu, part, pairs, cu.b * cols + lg, tok, v0, v1, {sc[0].v * rs, sc[0].u * rs});
+          if (!pairs)
+            m = abs_max(m, emit<FMT, PHASE2>(p, cu, part, pairs, cu.b * cols + lg + 8, tok, v1, 0.f,
+                                             {sc[1].v * rs, 1.f}));
           if (top_of_h) {
-            // the row's largest |h|: over the task's columns (8 or 16 neighbouring lanes), then the grid
             uint32_t top = __float_as_uint(m) & 0x7FFFFFFFu;
-            for (int o = 1; o < cols; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            if (q == 0 && tok < cu.rows) atomicMax(p.rowmax + cu.row0 + tok, top);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (lg == 0 && tok < cu.rows) atomicMax(p.rowmax + cu.row0 + tok, top);
           }
         }
       }
+    } else {
+      // the group's partial results meet; two buffers in turn, so one
+      // barrier per task keeps writers and readers apart
+        uint32_t(*red)[MAXNB][32][4] = &reinterpret_cast<Partial<MAXNB> *>(partials(sh))->red[red_it & 1u][warp / GW * GW];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        uint32_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const auto sum = acc.f[n][0][i] + acc.f[n][1][i];
+          if constexpr (FMT == I8) v[i] = (uint32_t)sum;
+          else v[i] = __float_as_uint(sum);
+        }
+        *reinterpret_cast<uint4 *>(red[warp % GW][n][lane]) = make_uint4(v[0], v[1], v[2], v[3]);
+      }
+      group_sync();
+      ++red_it;
+      // value (row, token) of the task: accumulator i of lane 4 (row % 8) + (token % 8) / 2
+      auto total = [&](int row, int tok) {
+        const int ln = (row & 7) * 4 + ((tok & 7) >> 1), i = (tok & 1) + (row >> 3) * 2, n = tok >> 3;
+        if (FMT == I8) {
+          int v = 0;
+#pragma unroll
+          for (int q = 0; q < GW; ++q) v += (int)red[q][n][ln][i];
+          return (float)v;
+        }
+        float v = 0.f;
+#pragma unroll
+        for (int q = 0; q < GW; ++q) v += __uint_as_float(red[q][n][ln][i]);
+        return v;
+      };
+      const int most = cols * 8 * (second ? 2 : 1);               // (at most the group's threads)
+      if (id < most) {
+        const int tok = id >> (pairs ? 3 : 4), q = id & (cols - 1);
+        if (FMT != BF16 && (FMT == Q4 || id >= cols * 8))
+          sc[0] = scale_of<FMT, PHASE2>(p, cu, pairs, cu.b * cols + q, row_scale<FMT, PHASE2>(p, cu, tok));
+        float m = 0.f;
+        if (tok < cu.rows)
+          m = emit<FMT, PHASE2>(p, cu, part, pairs, cu.b * cols + q, tok, total(q, tok), pairs ? total(q + 8, tok) : 0.f,
+                                sc[0]);
+        if (top_of_h) {
+          // the row's largest |h|: over the task's columns (8 or 16 neighbouring lanes), then the grid
+          uint32_t top = __float_as_uint(m) & 0x7FFFFFFFu;
+          for (int o = 1; o < cols; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          if (q == 0 && tok < cu.rows) atomicMax(p.rowmax + cu.row0 + tok, top);
+        }
+      }
     }
-    j += run * by;
   }
   red_it_ref = red_it;
+  return f;
+}
+
+// The block's tasks of one part (of phase 1 or 2), run by run
+template <int FMT, int RFMT, bool PHASE2, int NB, int DEPTH>
+__device__ __noinline__ Feed consume_part(const FewParams &p, Shared *sh, uint8_t *ring_ptr, Feed f, uint32_t &red_it,
+                                          int part) {
+  const Geo g = part_geo<FMT>(p, part, sh->nact);
+  const int warp = threadIdx.x >> 5;
+  for (int j = first_task(g, warp); j < g.n;) {
+    const Cursor cu = cursor_of(p, sh, g, part, g.first + j);
+    const int run = run_of(g, j, cu.b);
+    if (NB > 1 && cu.rows > 8) f = consume_run<FMT, RFMT, PHASE2, NB, NB, DEPTH>(p, sh, ring_ptr, f, red_it, part, g, cu, run);
+    else f = consume_run<FMT, RFMT, PHASE2, 1, NB, DEPTH>(p, sh, ring_ptr, f, red_it, part, g, cu, run);
+    j += run * task_stride(g);
+  }
   return f;
 }
 
