@@ -82,7 +82,7 @@ constexpr int SMEM_LIMIT = 227 * 1024;
 enum Fmt { BF16 = 0, I8 = 1, Q4 = 2 };
 
 // units in flight per warp
-__host__ __device__ constexpr int depth_of(int fmt, int TP) { return fmt != 2 && TP <= 4 ? 3 : 2; }
+__host__ __device__ constexpr int depth_of(int fmt, int TP) { return fmt != 2 && TP <= 8 ? 3 : 2; }
 // shared memory of one unit: the lanes' pieces, and 32 bytes of scales and biases per lane
 __host__ __device__ constexpr int unit_bytes(int fmt) { return ROWS * UNIT + (fmt == Q4 ? 32 * 32 : 0); }
 
@@ -125,8 +125,6 @@ struct FewParams {
   int ksplit;                               // most parts of K that y has room for
 };
 
-__host__ __device__ constexpr size_t scratch_bytes(int T, int E) { return ((size_t)T * E * 8 + 127) / 128 * 128; }
-
 struct Geo {
   int nb;        // row blocks per expert and part of K
   int first, n;  // this block's tasks: first .. first + n - 1
@@ -157,7 +155,7 @@ struct __align__(16) Shared {
   int warp_n[CW], warp_rows[CW];            // per 32 experts: how many have rows, and the rows
 };
 // Behind it: partial results of the warps, two tasks in turn; scratch of the
-// router and the choice (a row of 256 keys for each token)
+// router, and the tokens' probabilities [T][E] while the choice is made
 template <int NB>
 struct Partial {
   __align__(16) uint32_t red[2][CW][NB][32][4];
@@ -319,8 +317,19 @@ __device__ __forceinline__ Src task_src(const FewParams &p, int part, int e, int
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ uint32_t ld_stream(const void *p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float ld_l1_f32(const float *p) {
+  float v;
+  asm volatile("ld.global.ca.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void st_shared4(uint32_t dst, const uint32_t (&v)[4]) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -343,6 +352,12 @@ struct Feed {
   int flags;                                // see below; and from bit 8 on the segments of the last unit (0: whole)
   int groups;                               // 4-bit: groups of the row from the next unit's place on
   uint32_t issued, used;                    // units so far
+};
+// 4-bit: the last unit's scale words, put into its slot a step later
+// (four-byte copies straight into shared memory go through L1 and would drive
+// the tokens' rows out of it)
+struct Words {
+  uint32_t w[2][4], at;                     // at 0: none
 };
 enum FeedFlags { FULL = 1, HAS_LO = 2, HAS_HI = 4, SHORT = 8, DOWN = 16, ODD = 32 };
 // FULL: 16 rows of whole segments; HAS_LO / HAS_HI: there is such a row;
@@ -424,9 +439,17 @@ __device__ __noinline__ Feed feed_next(const FewParams &p, Shared *sh, Feed f) {
   return f;
 }
 
+__device__ __forceinline__ void flush_words(Words &w) {
+  if (w.at) {
+    st_shared4(w.at, w.w[0]);
+    st_shared4(w.at + 16, w.w[1]);
+    w.at = 0;
+  }
+}
+
 // Fetches the next unit (if there is one yet) and closes its group.
 template <int FMT, int DEPTH>
-__device__ __forceinline__ void feed_step(const FewParams &p, Shared *sh, Feed &f, uint32_t ring) {
+__device__ __forceinline__ void feed_step(const FewParams &p, Shared *sh, Feed &f, Words &words, uint32_t ring) {
   if (f.left > 0) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const uint32_t slot = ring + (f.issued % DEPTH) * unit_bytes(FMT);
@@ -451,7 +474,8 @@ __device__ __forceinline__ void feed_step(const FewParams &p, Shared *sh, Feed &
     f.lo += UNIT;
     f.hi += UNIT;
     if (FMT == Q4) {                        // (no shared expert here: every part is of 4-bit rows)
-      const uint32_t d = slot + ROWS * UNIT + lane * 32;
+      flush_words(words);
+      words.at = slot + ROWS * UNIT + lane * 32;
       if (f.groups > 0) {
         const bool down = f.flags & DOWN;
         const char *const base[4] = {
@@ -459,8 +483,8 @@ __device__ __forceinline__ void feed_step(const FewParams &p, Shared *sh, Feed &
             static_cast<const char *>(down ? p.s3 : p.s2) + f.sc_hi, static_cast<const char *>(down ? p.b3 : p.b2) + f.sc_hi};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          cp_async4(d + q * 4, base[q]);
-          if ((f.flags & ODD) && f.groups > 1) cp_async4(d + 16 + q * 4, base[q] + 4);
+          words.w[0][q] = ld_stream(base[q]);
+          if ((f.flags & ODD) && f.groups > 1) words.w[1][q] = ld_stream(base[q] + 4);
         }
       }
       f.sc_lo += 16;
@@ -482,6 +506,8 @@ __device__ __forceinline__ void feed_step(const FewParams &p, Shared *sh, Feed &
         f = feed_next<FMT>(p, sh, f);
       }
     }
+  } else if (FMT == Q4) {
+    flush_words(words);
   }
   cp_async_commit();
 }
@@ -497,8 +523,10 @@ __device__ __noinline__ Feed feed_open(const FewParams &p, Shared *sh, Feed f, u
   st.limit = limit;
   __syncwarp();
   if (stopped) f = feed_part<FMT>(p, sh, f, from);
+  Words words{};
 #pragma unroll 1
-  for (uint32_t i = f.issued - f.used; i < DEPTH; ++i) feed_step<FMT, DEPTH>(p, sh, f, ring);
+  for (uint32_t i = f.issued - f.used; i < DEPTH; ++i) feed_step<FMT, DEPTH>(p, sh, f, words, ring);
+  if (FMT == Q4) flush_words(words);
   return f;
 }
 
@@ -763,6 +791,7 @@ template <int FMT, int RFMT, bool PHASE2, int NB, int MAXNB, int DEPTH>
 __device__ __noinline__ Feed consume_run(const FewParams &p, Shared *sh, uint8_t *ring_ptr, Feed f, uint32_t &red_it_ref,
                                          int part, const Geo &geo, Cursor cu, int run) {
   uint32_t red_it = red_it_ref;
+  Words words{};
   constexpr bool LO = PHASE2 && FMT == BF16;
   constexpr int R = ratio_of<FMT>();
   const bool solo = geo.solo;
@@ -830,8 +859,8 @@ __device__ __noinline__ Feed consume_run(const FewParams &p, Shared *sh, uint8_t
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
           const int at = 2 * (w.first + u * SEGS) + c;
-          gsum[n][0] = at < KG ? __ldcg(sums[n] + u * 8) : 0.f;
-          gsum[n][1] = at + 4 < KG ? __ldcg(sums[n] + u * 8 + 4) : 0.f;
+          gsum[n][0] = at < KG ? ld_l1_f32(sums[n] + u * 8) : 0.f;
+          gsum[n][1] = at + 4 < KG ? ld_l1_f32(sums[n] + u * 8 + 4) : 0.f;
         }
       }
       auto segment = [&](int s, const BSeg<FMT, LO>(&bv)[NB], int left, auto check) {
@@ -899,7 +928,7 @@ __device__ __noinline__ Feed consume_run(const FewParams &p, Shared *sh, uint8_t
 #pragma unroll
       for (int n = 0; n < NB; ++n) bp[n] += UNIT * R;
       ++f.used;
-      feed_step<RFMT, DEPTH>(p, sh, f, ring);
+      feed_step<RFMT, DEPTH>(p, sh, f, words, ring);
     }
     if (solo) {
       // accumulators 0, 1: row g, tokens 2c, 2c + 1; 2, 3: row g + 8
@@ -972,6 +1001,7 @@ __device__ __noinline__ Feed consume_run(const FewParams &p, Shared *sh, uint8_t
       }
     }
   }
+  if (RFMT == Q4) flush_words(words);
   red_it_ref = red_it;
   return f;
 }
@@ -1110,9 +1140,8 @@ constexpr int EPL = kMaxExperts / 32;
 
 // One token's choice from its row of `prob` (softmax: shifted logits, made
 // probabilities here; sigmoid: probabilities); ids and weights to shared
-// memory.  A warp; expert lane + 32 j.  keys: this warp's scratch.
-__device__ __forceinline__ void choose(const FewParams &p, Shared *sh, int t, double *prob, unsigned long long *keys,
-                                       int lane) {
+// memory.  A warp; expert lane + 32 j.
+__device__ __forceinline__ void choose(const FewParams &p, Shared *sh, int t, double *prob, int lane) {
   const int E = p.E;
   constexpr unsigned long long LOWEST = 0x000FFFFFFFFFFFFFull;   // key of -infinity
   unsigned long long key[EPL];
@@ -1147,10 +1176,8 @@ __device__ __forceinline__ void choose(const FewParams &p, Shared *sh, int t, do
       const int e = lane + 32 * j;
       if (e < E) {
         key[j] = key_of(prob[e] + (double)sh->bias[e]);
-        keys[e] = key[j];
       }
     }
-    __syncwarp();
     // group score = sum of the two largest selection scores in the group
     const int G = E / p.n_group;
     unsigned long long gkey = 0;
@@ -1158,7 +1185,7 @@ __device__ __forceinline__ void choose(const FewParams &p, Shared *sh, int t, do
       unsigned long long b1 = 0, b2 = 0;
 #pragma unroll 4
       for (int q = 0; q < G; ++q) {
-        const unsigned long long v = keys[lane * G + q];
+        const unsigned long long v = key_of(prob[lane * G + q] + (double)sh->bias[lane * G + q]);
         b2 = max(b2, min(b1, v));
         b1 = max(b1, v);
       }
@@ -1230,11 +1257,12 @@ __device__ __forceinline__ void choose(const FewParams &p, Shared *sh, int t, do
 // Choice for every token and the plan, the same in every block.  The loops
 // that run once per expert stay rolled: a block runs this code once per
 // launch, and fetching its instructions is much of its time.
-__device__ __noinline__ void make_plan(const FewParams &p, Shared *sh, double *prob) {
+__device__ __noinline__ void make_plan(const FewParams &p, Shared *sh) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  static_assert(sizeof(Partial<1>) >= 8 * kMaxExperts * 8 && sizeof(Partial<2>) >= MAX_T * kMaxExperts * 8,
-                "selection scratch: a row of keys per token");
-  unsigned long long *keys = reinterpret_cast<unsigned long long *>(partials(sh)) + warp * kMaxExperts;
+  static_assert(sizeof(Partial<1>) >= 8 * kMaxExperts * sizeof(double) &&
+                    sizeof(Partial<2>) >= MAX_T * kMaxExperts * sizeof(double),
+                "a row of probabilities per token");
+  double *prob = reinterpret_cast<double *>(partials(sh));
   if (tid < kMaxExperts) sh->mask[tid] = 0u;
   static_assert(CT >= kMaxExperts && CW >= MAX_T, "a thread per expert, a warp per token");
   // logits (softmax: with the bias) or sigmoid scores, a thread per (token, expert)
@@ -1259,7 +1287,7 @@ __device__ __noinline__ void make_plan(const FewParams &p, Shared *sh, double *p
     prob[i] = l;
   }
   __syncthreads();
-  if (const int t = warp; t < p.T) choose(p, sh, t, prob + (size_t)t * p.E, keys, lane);
+  if (const int t = warp; t < p.T) choose(p, sh, t, prob + (size_t)t * p.E, lane);
   __syncthreads();
   const int slots = p.T * p.k;
 #pragma unroll 1
@@ -1517,11 +1545,7 @@ __global__ void __launch_bounds__(CT, 1) few_kernel(const __grid_constant__ FewP
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t *ring_ptr = smem_raw + (threadIdx.x >> 5) * DEPTH * unit_bytes(FMT);      // this warp's
   const uint32_t ring = smem_u32(ring_ptr);
-  // the tokens' probabilities: in the slots where nothing is fetched before the
-  // choice (no shared expert with 4-bit weights), else behind them
-  uint8_t *behind = smem_raw + CW * DEPTH * unit_bytes(FMT);
-  double *prob = reinterpret_cast<double *>(FMT == Q4 ? smem_raw : behind);
-  Shared *sh = reinterpret_cast<Shared *>(behind + (FMT == Q4 ? 0 : scratch_bytes(p.T, p.E)));
+  Shared *sh = reinterpret_cast<Shared *>(smem_raw + CW * DEPTH * unit_bytes(FMT));
   volatile int *abort_flag = &sh->abort_flag;
   if (threadIdx.x == 0) {
     sh->abort_flag = 0;
@@ -1546,7 +1570,7 @@ __global__ void __launch_bounds__(CT, 1) few_kernel(const __grid_constant__ FewP
   if (p.Fs) feed = consume_part<BF16, FMT, false, NB, DEPTH>(p, sh, ring_ptr, feed, red_it, S1);
   grid_arrive(p.bar);
   grid_wait(p.bar, abort_flag, p);
-  make_plan(p, sh, prob);
+  make_plan(p, sh);
   feed = feed_open<FMT, DEPTH>(p, sh, feed, ring, END);
   if (p.Fs) feed = consume_part<BF16, FMT, true, NB, DEPTH>(p, sh, ring_ptr, feed, red_it, S2);
   feed = consume_part<FMT, FMT, false, NB, DEPTH>(p, sh, ring_ptr, feed, red_it, R1);
@@ -1567,14 +1591,14 @@ __global__ void __launch_bounds__(CT, 1) few_kernel(const __grid_constant__ FewP
 }
 
 template <int FMT, int TP>
-__host__ constexpr size_t smem_bytes(int T, int E) {
-  return (size_t)CW * depth_of(FMT, TP) * unit_bytes(FMT) + (FMT == Q4 ? 0 : scratch_bytes(T, E)) + sizeof(Shared) +
+__host__ constexpr size_t smem_bytes() {
+  return (size_t)CW * depth_of(FMT, TP) * unit_bytes(FMT) + sizeof(Shared) +
          (TP > 8 ? sizeof(Partial<2>) : sizeof(Partial<1>));
 }
 
 template <int FMT, int TP>
 cudaError_t run(const FewParams &p, cudaStream_t s) {
-  const size_t smem = smem_bytes<FMT, TP>(p.T, p.E);
+  const size_t smem = smem_bytes<FMT, TP>();
   auto kern = few_kernel<FMT, TP>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
@@ -1591,8 +1615,8 @@ cudaError_t run(const FewParams &p, cudaStream_t s) {
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
-static_assert(smem_bytes<BF16, 4>(4, kMaxExperts) <= SMEM_LIMIT && smem_bytes<BF16, 16>(MAX_T, kMaxExperts) <= SMEM_LIMIT &&
-                  smem_bytes<Q4, 16>(MAX_T, kMaxExperts) <= SMEM_LIMIT,
+static_assert(smem_bytes<BF16, 8>() <= SMEM_LIMIT && smem_bytes<BF16, 16>() <= SMEM_LIMIT &&
+                  smem_bytes<Q4, 8>() <= SMEM_LIMIT && smem_bytes<Q4, 16>() <= SMEM_LIMIT,
               "shared memory");
 
 template <int FMT>
