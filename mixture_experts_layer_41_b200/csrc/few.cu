@@ -170,7 +170,7 @@ __device__ __forceinline__ uint32_t *partials(const Shared *sh) {
 __device__ __forceinline__ void grid_arrive(unsigned *ctr) {
   __syncthreads();
   if (threadIdx.x == 0) {
-    __threadfence();
+    // (the release covers what the other threads wrote before the barrier above)
     asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(ctr) : "memory");
   }
 }
@@ -188,7 +188,6 @@ __device__ __forceinline__ void grid_wait(unsigned *ctr, volatile int *abort_fla
         break;
       }
     }
-    __threadfence();
   }
   __syncthreads();
 }
@@ -1508,34 +1507,41 @@ __device__ __forceinline__ void quantize_h(const FewParams &p, const Shared *sh)
   }
 }
 
-// out[t] = sum_j w_j y[slot_row] in slot order (+ the shared expert's row), 4 columns per thread
+// out[t] = sum_j w_j y[slot_row] in slot order (+ the shared expert's row), 4
+// columns per thread, the loads of four slots (and their parts of K) in flight
+// together
 __device__ __forceinline__ void combine(const FewParams &p, const Shared *sh, int ks) {
   const int nv = p.d / 4;
-  for (int i = blockIdx.x * CT + threadIdx.x; i < p.T * nv; i += gridDim.x * CT) {
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = blockIdx.x + gridDim.x * threadIdx.x; i < p.T * nv; i += gridDim.x * CT) {
     const int t = i / nv, c = i - t * nv;
-    float a[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < p.k; ++j) {
-      const int row = sh->slot_row[t * p.k + j];
-      if (row < 0) continue;
-      const float w = sh->sel_w[t * p.k + j];
-      float4 v = __ldcg(reinterpret_cast<const float4 *>(p.y + (size_t)row * p.d) + c);
-      for (int q = 1; q < ks; ++q) {
-        const float4 u = __ldcg(reinterpret_cast<const float4 *>(p.y + ((size_t)q * p.y_rows + row) * p.d) + c);
-        v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+    float4 a = zero, shared = zero;
+    if (p.Fs) shared = __ldcg(reinterpret_cast<const float4 *>(p.y + ((size_t)p.ksplit * p.y_rows + t) * p.d) + c);
+#pragma unroll 1
+    for (int j0 = 0; j0 < p.k; j0 += 4) {
+      float4 v[4][MAX_KSPLIT];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int row = j0 + u < p.k ? sh->slot_row[t * p.k + j0 + u] : -1;
+#pragma unroll
+        for (int q = 0; q < MAX_KSPLIT; ++q)
+          v[u][q] = row >= 0 && q < ks
+                        ? __ldcg(reinterpret_cast<const float4 *>(p.y + ((size_t)q * p.y_rows + row) * p.d) + c)
+                        : zero;
       }
-      a[0] = fmaf(w, v.x, a[0]);
-      a[1] = fmaf(w, v.y, a[1]);
-      a[2] = fmaf(w, v.z, a[2]);
-      a[3] = fmaf(w, v.w, a[3]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (j0 + u >= p.k || sh->slot_row[t * p.k + j0 + u] < 0) continue;
+        const float w = sh->sel_w[t * p.k + j0 + u];
+        float4 s = v[u][0];
+#pragma unroll
+        for (int q = 1; q < MAX_KSPLIT; ++q)
+          s = make_float4(s.x + v[u][q].x, s.y + v[u][q].y, s.z + v[u][q].z, s.w + v[u][q].w);
+        a = make_float4(fmaf(w, s.x, a.x), fmaf(w, s.y, a.y), fmaf(w, s.z, a.z), fmaf(w, s.w, a.w));
+      }
     }
-    if (p.Fs) {
-      const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.y + ((size_t)p.ksplit * p.y_rows + t) * p.d) + c);
-      a[0] += v.x;
-      a[1] += v.y;
-      a[2] += v.z;
-      a[3] += v.w;
-    }
-    *reinterpret_cast<uint2 *>(p.out + (size_t)t * p.d + 4 * c) = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+    a = make_float4(a.x + shared.x, a.y + shared.y, a.z + shared.z, a.w + shared.w);
+    *reinterpret_cast<uint2 *>(p.out + (size_t)t * p.d + 4 * c) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
   }
 }
 
