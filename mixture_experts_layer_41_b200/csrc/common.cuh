@@ -397,7 +397,10 @@ struct MmI8Args {
   const float *ws0, *ws1;   // channel scales, same rows
   void *out;                // [rows_cap, N]
   int *status;
+  int set_status;           // nothing has cleared the status word: the few-rows kernel writes it
 };
+bool mm_i8_is_few(const MmI8Args &a);                            // which of the two it is
+cudaError_t launch_mm_i8_few(const MmI8Args &a, cudaStream_t s);
 cudaError_t launch_mm_i8_tc(const MmI8Args &a, cudaStream_t s);
 cudaError_t launch_mm_i8(const MmI8Args &a, cudaStream_t s);     // picks the kernel
 cudaError_t launch_ffn_i8(const FfnArgs &a, cudaStream_t s);

@@ -15,7 +15,9 @@
 
 namespace moe {
 
-cudaError_t launch_mm_i8(const MmI8Args &a, cudaStream_t s) { return launch_mm_i8_tc(a, s); }
+cudaError_t launch_mm_i8(const MmI8Args &a, cudaStream_t s) {
+  return mm_i8_is_few(a) ? launch_mm_i8_few(a, s) : launch_mm_i8_tc(a, s);
+}
 
 cudaError_t launch_ffn_i8(const FfnArgs &a, cudaStream_t s) {
   const int32_t *present = a.offsets + a.E;

@@ -622,7 +622,6 @@ moe_status moe_quantized_matmul(int32_t groups, int32_t rows, int32_t n, int32_t
   if (rows > 0 && (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(out))) return MOE_ERR_INVALID_ARG;
   if (!aligned16(ws) || ws_bytes < moe_quantized_matmul_workspace_size(groups, rows, n, k)) return MOE_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if ((st = clear_status(ws, s)) != MOE_OK || rows == 0) return st;
   MmI8Args m{};
   m.offsets = group_offsets;
   m.G = groups;
@@ -637,6 +636,9 @@ moe_status moe_quantized_matmul(int32_t groups, int32_t rows, int32_t n, int32_t
   m.ws0 = w_scales;
   m.out = out;
   m.status = ws_ptr<int>(ws, 0);
+  // the few-rows kernel waits for nothing and writes the whole status itself
+  m.set_status = rows > 0 && mm_i8_is_few(m);
+  if (!m.set_status && ((st = clear_status(ws, s)) != MOE_OK || rows == 0)) return st;
   cudaError_t err = launch_mm_i8(m, s);
   return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_quantized_matmul");
 }

@@ -170,6 +170,11 @@ GROUPS = [
     (256, 300, 33, 48, [0] * 128 + list(range(129))),
     (3, 20, 130, 96, [0, 0, 0, 0]),
     (1, 50, 130, 96, [0, 20]),
+    (4, 30, 520, 2064, [0, 1, 1, 12, 30]),
+    (3, 24, 33, 4112, [0, 8, 17, 24]),
+    (8, 32, 200, 2048, [0, 0, 0, 0, 32, 32, 32, 32, 32]),
+    (8, 32, 5, 2304, [0, 3, 4, 4, 4, 5, 6, 30, 31]),
+    (1, 16, 40, 8208, [0, 13]),
 ]
 
 
@@ -260,6 +265,8 @@ LAYER = {
     "groups_shared": workload("deepseek_v3", T=300, d=448, F=256, E=32, n_group=8, topk_group=4, shared_F=256),
     "many_experts": workload("mixtral_prefill", T=64, d=512, F=192, E=128, k=8),
     "few_rows": workload("mixtral_prefill", T=9, d=1040, F=528, E=6, k=2),
+    "few_long_rows": workload("mixtral_prefill", T=5, d=2320, F=2064, E=4, k=3),
+    "few_relu": workload("switch_top1", T=14, d=2064, F=208, E=4, k=1, capacity_factor=1.25),
 }
 
 
