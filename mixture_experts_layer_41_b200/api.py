@@ -8,6 +8,7 @@ as in C; ``MoELayer`` is a convenience holder that allocates them.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 from dataclasses import dataclass
 from typing import Optional
 
@@ -47,12 +48,31 @@ def _p(t: Optional[torch.Tensor]):
 
 def _s(stream) -> Optional[int]:
     if stream is None:
+        if torch.cuda.is_initialized():
+            # the handle alone: building torch's Stream object costs 8 us a call, this 0.3 us
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
 def _nbytes(t: torch.Tensor) -> int:
     return t.numel() * t.element_size()
+
+
+@functools.lru_cache(maxsize=None)
+def _have_gpu() -> bool:
+    return torch.cuda.is_available()
+
+
+def _on_current(*tensors) -> None:
+    """Refuses tensors that are not on the current device: a kernel launched
+    there cannot be expected to read them."""
+    if not _have_gpu():
+        return
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors must be on the current CUDA device (cuda:{dev}); got one on {t.device}")
 
 
 # ---------------------------------------------------------------- host-only calls
@@ -240,6 +260,7 @@ def moe_quantize_rows(x, codes, scales, stream=None):
         raise ValueError("codes must be an int8 tensor of x's shape")
     if scales.dtype != torch.float32 or scales.shape != x.shape[:-1]:
         raise ValueError("scales must be a float32 tensor with one element per row of x")
+    _on_current(x, codes, scales)
     cols = x.shape[-1]
     check(L.lib().moe_quantize_rows(_p(x), _MOE_DT[x.dtype], scales.numel(), cols, _p(codes), _p(scales), _s(stream)),
           "moe_quantize_rows")
@@ -266,6 +287,7 @@ def moe_quantized_matmul(x_codes, x_scales, w_codes, w_scales, out, ws, group_of
         raise ValueError("out must be a float32 or bfloat16 tensor [rows, n]")
     if group_offsets is not None and (group_offsets.dtype != torch.int32 or group_offsets.numel() != groups + 1):
         raise ValueError("group_offsets must be an int32 tensor [groups + 1]")
+    _on_current(x_codes, x_scales, w_codes, w_scales, out, ws, group_offsets)
     check(L.lib().moe_quantized_matmul(groups, rows, n, k, _p(x_codes), _p(x_scales), _p(group_offsets), _p(w_codes),
                                        _p(w_scales), _MOE_DT[out.dtype], _p(out), _p(ws), _nbytes(ws), _s(stream)),
           "moe_quantized_matmul")
@@ -292,6 +314,8 @@ def moe_forward(cfg, x, w_router, router_bias, weights: dict, out, topk_ids, top
 
 def moe_forward_few(cfg, x, w_router, router_bias, weights: dict, out, topk_ids, topk_w, stats, ws, stream=None):
     """``moe_forward`` for at most ``MOE_FEW_TOKENS`` tokens, in one kernel."""
+    if cfg.num_tokens <= L.MOE_FEW_TOKENS:      # (larger batches are refused below)
+        _on_current(x, w_router, router_bias, out, topk_ids, topk_w, ws, *weights.values(), *(stats or {}).values())
     w = _weights_struct(weights)
     st = _stats_struct(stats)
     code = L.lib().moe_forward_few(C.byref(cfg), _p(x), _p(w_router), _p(router_bias), C.byref(w), _p(out),

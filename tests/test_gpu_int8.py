@@ -403,3 +403,18 @@ def test_layer_8_bit_barrier_timeout_reports_and_recovers():
     run.staged()
     assert run.status() == 0
     check_layer(run)
+
+
+def test_quantized_calls_refuse_tensors_elsewhere():
+    """A tensor left on the host is refused before any launch, whichever it is."""
+    q = torch.zeros((4, 32), dtype=torch.int8, device="cuda")
+    args = [torch.zeros((4, 32), device="cuda"), q, torch.zeros(4, device="cuda")]
+    for i in range(3):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            api.moe_quantize_rows(*(a.cpu() if j == i else a for j, a in enumerate(args)))
+    args = [q, torch.zeros(4, device="cuda"), torch.zeros((2, 8, 32), dtype=torch.int8, device="cuda"),
+            torch.zeros((2, 8), device="cuda"), torch.zeros((4, 8), device="cuda"),
+            torch.zeros(4096, dtype=torch.uint8, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")]
+    for i in range(7):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            api.moe_quantized_matmul(*(a.cpu() if j == i else a for j, a in enumerate(args)))
