@@ -399,9 +399,12 @@ struct MmI8Args {
   int *status;
   int set_status;           // nothing has cleared the status word: the few-rows kernel writes it
 };
-bool mm_i8_is_few(const MmI8Args &a);                            // which of the two it is
+bool mm_i8_is_few(const MmI8Args &a);                            // which kernel a call's sizes ask for
+bool mm_i8_is_large(const MmI8Args &a);
 cudaError_t launch_mm_i8_few(const MmI8Args &a, cudaStream_t s);
 cudaError_t launch_mm_i8_tc(const MmI8Args &a, cudaStream_t s);
+int mm_i8_pairs();                                               // pairs of SMs that can be resident at once
+cudaError_t launch_mm_i8_pair(const MmI8Args &a, int pairs, cudaStream_t s);
 cudaError_t launch_mm_i8(const MmI8Args &a, cudaStream_t s);     // picks the kernel
 cudaError_t launch_ffn_i8(const FfnArgs &a, cudaStream_t s);
 

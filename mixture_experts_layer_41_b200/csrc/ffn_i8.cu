@@ -16,7 +16,9 @@
 namespace moe {
 
 cudaError_t launch_mm_i8(const MmI8Args &a, cudaStream_t s) {
-  return mm_i8_is_few(a) ? launch_mm_i8_few(a, s) : launch_mm_i8_tc(a, s);
+  if (mm_i8_is_few(a)) return launch_mm_i8_few(a, s);
+  static const int pairs = mm_i8_pairs();
+  return pairs > 0 && mm_i8_is_large(a) ? launch_mm_i8_pair(a, pairs, s) : launch_mm_i8_tc(a, s);
 }
 
 cudaError_t launch_ffn_i8(const FfnArgs &a, cudaStream_t s) {

@@ -21,12 +21,13 @@
 // Bound by latency for one matrix (one launch, one round of tasks: 4096 x 4096
 // takes 6.4 us against 2.6 us of reading), by HBM for long ones: 65536 x 2048
 // and one row 24.6 us, 5.5 TB/s.
-#include "tc_ptx.cuh"
+#include "mm_i8.cuh"
 
 namespace moe {
 namespace {
 
 using namespace ptx;
+using i8::silu_f;
 
 constexpr int CW = 16, GW = 8;              // warps, and those that share a task of long rows
 constexpr int CT = 32 * CW;
@@ -59,7 +60,6 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
       : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float silu_f(float g) { return g / (1.f + __expf(-g)); }
 
 // Where a walk over the tasks first .. end - 1 stands: task = (group, pass, row block)
 struct Walk {

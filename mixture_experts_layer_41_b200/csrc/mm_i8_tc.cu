@@ -21,22 +21,21 @@
 //   warps 2-5   epilogue: tcgen05.ld, scales, activation, store.  Each warp
 //               keeps its own copy of the tile's channel scales in shared
 //               memory, fetched while the accumulator is still being built.
-// BN is 256 unless that leaves SMs without a tile (see pick_bn).
+// BN is 256 unless that leaves SMs without a tile (launch_mm_i8_tc).
 //
 // A tile's rows past its group's end belong to the next group (or are
 // zero-filled by TMA past the buffer); their results are never stored.
 // Every mbarrier wait is bounded (moe_set_wait_timeout_ns); on expiry the
 // thread records a status code, raises a CTA-wide abort flag, drains what it
 // issued, and the CTA frees its TMEM and exits.
-#include "tc_ptx.cuh"
+#include "mm_i8.cuh"
 
 namespace moe {
 namespace {
 
 using namespace ptx;
+using namespace i8;
 
-constexpr int BM = 128;
-constexpr int BK = 128;                       // 128 int8 = one swizzle row
 constexpr int THREADS = 192;
 
 template <int BN>
@@ -112,40 +111,6 @@ __device__ __forceinline__ TileInfo decode_tile(const SharedState<BN> *st, int G
   ti.row0 = st->off[lo] + (local % mt) * BM;
   ti.rows = min(BM, st->off[lo + 1] - ti.row0);
   return ti;
-}
-
-__device__ __forceinline__ float silu_f(float g) { return g / (1.f + __expf(-g)); }
-
-// 32 consecutive outputs of a row from column col0 (columns >= N dropped);
-// vectors where the row pitch keeps them aligned
-__device__ __forceinline__ void store32(void *out, bool f32, size_t row, int N, int col0, const float (&y)[32]) {
-  if (f32) {
-    float *o = static_cast<float *>(out) + row * N + col0;
-    if ((N & 3) == 0) {
-#pragma unroll
-      for (int v = 0; v < 8; ++v)
-        if (col0 + 4 * v < N)
-          *reinterpret_cast<float4 *>(o + 4 * v) = make_float4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (col0 + i < N) o[i] = y[i];
-    }
-  } else {
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(out) + row * N + col0;
-    if ((N & 7) == 0) {
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        if (col0 + 8 * v < N)
-          *reinterpret_cast<uint4 *>(o + 8 * v) =
-              make_uint4(pack_bf16x2(y[8 * v], y[8 * v + 1]), pack_bf16x2(y[8 * v + 2], y[8 * v + 3]),
-                         pack_bf16x2(y[8 * v + 4], y[8 * v + 5]), pack_bf16x2(y[8 * v + 6], y[8 * v + 7]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (col0 + i < N) o[i] = __float2bfloat16_rn(y[i]);
-    }
-  }
 }
 
 template <int BN>
@@ -284,55 +249,11 @@ i8_grouped_gemm(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
       const bool valid = rloc < ti.rows;
       const size_t row = (size_t)(ti.row0 + (valid ? rloc : 0));
       const int col0 = ti.n * (swiglu ? BN / 2 : BN);
-      const size_t sbase = (size_t)ti.g * p.b_stride;
-      __syncwarp();                         // the previous tile's scales have been read
-#pragma unroll
-      for (int i = 0; i < BN; i += 32) {
-        const int j = i + lane;             // accumulator column
-        const float *src = swiglu && j >= BN / 2 ? p.ws1 : p.ws0;
-        const int col = col0 + (swiglu && j >= BN / 2 ? j - BN / 2 : j);
-        sc[j] = col < p.N ? __ldg(src + sbase + col) : 0.f;
-      }
+      load_scales<BN>(sc, p.ws0, p.ws1, (size_t)ti.g * p.b_stride, p.mode, p.N, col0);
       const float xs = valid ? __ldg(p.xs + row) : 0.f;
-      __syncwarp();
       if (!wait_bounded(&st->acc_full[buf], use & 1u, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns)) break;
       tc_fence_after();
-      const uint32_t tb = tmem_base + buf * BN + ((uint32_t)(q * 32) << 16);
-      if (swiglu) {
-#pragma unroll 1
-        for (int c = 0; c < BN / 2; c += 32) {
-          uint32_t g[32], u[32];
-          tmem_ld32(tb + c, g);
-          tmem_ld32(tb + BN / 2 + c, u);
-          tmem_wait_ld();
-          if (valid && col0 + c < p.N) {
-            float y[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float gv = (float)(int)g[i] * (xs * sc[c + i]);
-              const float uv = (float)(int)u[i] * (xs * sc[BN / 2 + c + i]);
-              y[i] = silu_f(gv) * uv;
-            }
-            store32(p.out, false, row, p.N, col0 + c, y);
-          }
-        }
-      } else {
-#pragma unroll 1
-        for (int c = 0; c < BN; c += 32) {
-          uint32_t a[32];
-          tmem_ld32(tb + c, a);
-          tmem_wait_ld();
-          if (valid && col0 + c < p.N) {
-            float y[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              y[i] = (float)(int)a[i] * (xs * sc[c + i]);
-              if (p.mode == I8_RELU) y[i] = y[i] < 0.f ? 0.f : y[i];     // a NaN stays one
-            }
-            store32(p.out, p.mode == I8_F32, row, p.N, col0 + c, y);
-          }
-        }
-      }
+      store_tile<BN>(tmem_base + buf * BN + ((uint32_t)(q * 32) << 16), sc, xs, p.mode, p.out, p.N, row, col0, valid);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&st->acc_empty[buf]);

@@ -132,7 +132,8 @@ def check_mm(out, ref, dt, fill=0.0):
 
 MM = [(1, 64, 64), (1, 4096, 4096), (1, 2051, 1424), (3, 8, 16), (5, 1, 48), (16, 256, 272), (17, 129, 144),
       (31, 520, 2048), (33, 7, 400), (64, 300, 96), (100, 1024, 528), (128, 256, 128), (129, 257, 144), (130, 4100, 64),
-      (500, 1000, 1040), (777, 2051, 1424), (1300, 4096, 256)]
+      (500, 1000, 1040), (777, 2051, 1424), (1300, 4096, 256), (500, 4100, 1040), (1090, 2310, 1072), (257, 6500, 1024),
+      (320, 3200, 2064)]
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
@@ -175,6 +176,9 @@ GROUPS = [
     (8, 32, 200, 2048, [0, 0, 0, 0, 32, 32, 32, 32, 32]),
     (8, 32, 5, 2304, [0, 3, 4, 4, 4, 5, 6, 30, 31]),
     (1, 16, 40, 8208, [0, 13]),
+    (3, 900, 2600, 1056, [0, 300, 301, 900]),
+    (4, 1000, 1603, 1040, [0, 0, 640, 641, 950]),
+    (2, 513, 2500, 1024, [0, 513, 513]),
 ]
 
 
@@ -266,6 +270,8 @@ LAYER = {
     "many_experts": workload("mixtral_prefill", T=64, d=512, F=192, E=128, k=8),
     "few_rows": workload("mixtral_prefill", T=9, d=1040, F=528, E=6, k=2),
     "few_long_rows": workload("mixtral_prefill", T=5, d=2320, F=2064, E=4, k=3),
+    "large_groups": workload("mixtral_prefill", T=900, d=1040, F=1056, E=4, k=2),
+    "large_relu": workload("switch_top1", T=1500, d=1040, F=1040, E=4, k=1, capacity_factor=1.25),
     "few_relu": workload("switch_top1", T=14, d=2064, F=208, E=4, k=1, capacity_factor=1.25),
 }
 
@@ -388,10 +394,12 @@ def test_layer_8_bit_in_a_graph():
         assert layer.status() == 0
 
 
-def test_layer_8_bit_barrier_timeout_reports_and_recovers():
+@pytest.mark.parametrize("sizes", [dict(T=700, d=512, F=640), dict(T=900, d=1040, F=1056, E=4)])
+def test_layer_8_bit_barrier_timeout_reports_and_recovers(sizes):
     """A 1 ns bound on the barrier waits makes the product give up: a device
-    status, and the context and workspace stay good."""
-    w = workload("mixtral_prefill", T=700, d=512, F=640)
+    status, and the context and workspace stay good.  On one SM a tile, and on
+    pairs of SMs."""
+    w = workload("mixtral_prefill", **sizes)
     run = I8Run(w, seed=35).staged()
     try:
         api.moe_set_wait_timeout_ns(1)
