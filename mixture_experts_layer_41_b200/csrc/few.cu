@@ -1513,7 +1513,9 @@ __device__ __forceinline__ void quantize_h(const FewParams &p, const Shared *sh)
 __device__ __forceinline__ void combine(const FewParams &p, const Shared *sh, int ks) {
   const int nv = p.d / 4;
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = blockIdx.x + gridDim.x * threadIdx.x; i < p.T * nv; i += gridDim.x * CT) {
+  // a warp's 32 vectors are neighbours, the warps' pieces go round the blocks
+  const int lane = threadIdx.x & 31;
+  for (int i = (blockIdx.x + gridDim.x * (threadIdx.x >> 5)) * 32 + lane; i < p.T * nv; i += gridDim.x * CT) {
     const int t = i / nv, c = i - t * nv;
     float4 a = zero, shared = zero;
     if (p.Fs) shared = __ldcg(reinterpret_cast<const float4 *>(p.y + ((size_t)p.ksplit * p.y_rows + t) * p.d) + c);

@@ -17,8 +17,11 @@
 //
 // Bound by HBM: each element is read once (a row stays in registers between
 // the maximum and the codes) and each code written once.  A warp takes a row
-// of up to 1024 elements, a block of 256 threads one of up to 16384; longer
-// rows are read a second time, from L2.
+// of up to 1024 elements, and from 1024 rows on one of up to 4096 (fp32:
+// 2048); a block of 256 threads one of up to 16384; longer rows are read a
+// second time, from L2.  bf16, 8192 rows of 2048: 18.2 us (28.9 with a block to
+// a row, whose two barriers every row waits for), 2.8 TB/s; 8192 of 14336:
+// 68 us, 5.2 TB/s.
 //
 // The layer's use: rows of the expert-sorted matrix up to the device-side row
 // count, or (scatter) token rows whose codes go straight to their slots' rows
@@ -30,6 +33,7 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int VECS = 8;       // 8-element vectors a thread keeps in registers
+constexpr int WARP_ROWS = 1024;   // 256 rows of 4096: 3.0 us by blocks, one wave of long chains by warps
 
 struct QuantParams {
   const void *x;
@@ -118,12 +122,12 @@ __device__ __forceinline__ uint2 codes8(const Vec8<BF16> &v, const Row &w) {
   return make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
 }
 
-// TPR threads per row (32 or THREADS); MORE: rows longer than the registers hold
-template <bool BF16, int TPR, bool MORE>
+// TPR threads per row (32 or THREADS), each with KEEP vectors in registers;
+// MORE: rows longer than the registers hold
+template <bool BF16, int TPR, int KEEP, bool MORE>
 __global__ void __launch_bounds__(THREADS)
 quantize_rows_kernel(const QuantParams p) {
   pdl_enter();
-  constexpr int KEEP = TPR == 32 ? 4 : VECS;
   __shared__ uint32_t red[THREADS / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i0 = TPR == 32 ? lane : threadIdx.x;
@@ -193,15 +197,18 @@ quantize_rows_kernel(const QuantParams p) {
 
 template <bool BF16>
 cudaError_t run(const QuantParams &p, cudaStream_t s) {
-  const bool warp_rows = p.K <= 4 * 32 * 8;
+  constexpr int LONG = BF16 ? 16 : 8;       // vectors of a warp's lane in longer rows (64 registers)
+  const bool warp_rows = p.K <= 4 * 32 * 8 || (p.K <= LONG * 32 * 8 && p.rows >= WARP_ROWS);
   const long long blocks = warp_rows ? (p.rows + THREADS / 32 - 1) / (THREADS / 32) : p.rows;
   const int grid = (int)(blocks < 148 * 64 ? blocks : 148 * 64);
-  if (warp_rows)
-    launch_pdl(quantize_rows_kernel<BF16, 32, false>, grid, THREADS, 0, s, p);
+  if (p.K <= 4 * 32 * 8)
+    launch_pdl(quantize_rows_kernel<BF16, 32, 4, false>, grid, THREADS, 0, s, p);
+  else if (warp_rows)
+    launch_pdl(quantize_rows_kernel<BF16, 32, LONG, false>, grid, THREADS, 0, s, p);
   else if (p.K <= VECS * THREADS * 8)
-    launch_pdl(quantize_rows_kernel<BF16, THREADS, false>, grid, THREADS, 0, s, p);
+    launch_pdl(quantize_rows_kernel<BF16, THREADS, VECS, false>, grid, THREADS, 0, s, p);
   else
-    launch_pdl(quantize_rows_kernel<BF16, THREADS, true>, grid, THREADS, 0, s, p);
+    launch_pdl(quantize_rows_kernel<BF16, THREADS, VECS, true>, grid, THREADS, 0, s, p);
   return cudaGetLastError();
 }
 
