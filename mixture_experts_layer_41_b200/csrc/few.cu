@@ -28,16 +28,17 @@
 // phase's weights when a barrier opens).  Measured on 466 MB of 16-row tasks:
 // 6.49 TB/s four units deep; one bulk copy per row piece, with a producer
 // warp, cost 55 ns each whatever its size (5.1 TB/s at 2 KB, 1.3 at 512 B).
-// A block takes a run of consecutive tasks, so most are one expert's and its
-// tokens' rows stay in L1.
+// A block's sixteen warps are two groups of eight, or sixteen on their own; each
+// takes a run of consecutive tasks, so most are one expert's and its tokens'
+// rows stay in L1.
 //
 // The product.  mma.sync m16n8: 16 weight rows times 8 tokens.  A thread's
 // 16 bytes of rows g and g + 8 and of token g's row are one A and one B
 // operand for a permuted order of K (a sum over K has no order), so nothing is
 // transposed or shuffled.  At 23 bytes of weights per clock and SM the legacy
 // unit (2 clocks a product) is mostly idle.
-//   long rows   the warps split a task's K; their partial 16 x 8 results meet
-//               in shared memory, one barrier per task;
+//   long rows   the eight warps of a group split a task's K; their partial
+//               16 x 8 results meet in shared memory, one barrier per task;
 //   short rows  (solo) each warp takes whole tasks.
 //
 // Precision: bf16 weights take h as the sum of two bf16 (16 bits).  8-bit
@@ -49,6 +50,14 @@
 // below the codes' own), in two digits of 8 bits: v = 256 hi + lo.  Per group
 // of 64, s sum(q v) + b sum(v), the sums exact in int32, scaled and added in
 // fp32.  Expert outputs stay fp32 until the combine.
+//
+// Measured (graph replays): one token of d 4096, F 14336, top 2 of 8 in bf16
+// 137 us (5.1 TB/s of the weights; the nine launches of the staged layer 297);
+// four of d 7168, F 2048, top 8 of 256 in 8 bits with a bf16 shared expert
+// 283 us (5.1 TB/s; staged 379); two of d 448, F 256 37 us, all of it launch,
+// barriers and latency.  4-bit experts are bound by the unpacking and by how
+// evenly few tasks divide: one token of d 2048, F 768, top 8 of 128 48 us
+// (staged 51), 16 tokens 158 us (staged 112, with weights rounded to bf16).
 //
 // Results do not depend on timing: every sum has a fixed order, and the row
 // maxima behind the 8-bit codes of h are integer maxima.
@@ -882,16 +891,22 @@ __device__ __noinline__ Feed consume_run(const FewParams &p, Shared *sh, uint8_t
       };
       if (u < whole) {
         if constexpr (FMT == Q4) {
+          // (rolled: the body is long, and fetching instructions would cost more);
+          // the token operand is a segment ahead
+          BSeg<FMT, LO> bv[NB], next[NB];
+#pragma unroll
+          for (int n = 0; n < NB; ++n) load_b<FMT, LO, false>(bv[n], bp[n], lo_bytes, SEG, c);
           cp_async_wait<DEPTH - 1>();
           __syncwarp();
-          // (rolled: the body is long, and fetching instructions would cost more)
 #pragma unroll 1
           for (int s = 0; s < SEGS; ++s) {
-            BSeg<FMT, LO> bv[NB];
+            const int ahead = min(s + 1, SEGS - 1);
 #pragma unroll
             for (int n = 0; n < NB; ++n)
-              load_b<FMT, LO, false>(bv[n], bp[n] + s * SEG * R, lo_bytes, SEG, c);
+              load_b<FMT, LO, false>(next[n], bp[n] + ahead * SEG * R, lo_bytes, SEG, c);
             segment(s, bv, SEG, std::false_type{});
+#pragma unroll
+            for (int n = 0; n < NB; ++n) bv[n] = next[n];
           }
         } else {
           // the token operand is on its way while the weights are waited for
