@@ -135,8 +135,8 @@ typedef struct moe_config {
  * token row, in front of both products (see moe_grouped_ffn).
  * With weight_layout = MOE_LAYOUT_FUSED_GATE_UP the gate and up matrices
  * come as ONE tensor in w1, [E, 2F, d] (Q4: codes [E, 2F, d/8], scale1 /
- * bias1 [E, 2F, d/64]; 8-bit: codes [E, 2F, d], scale1 [E, 2F]): expert e's F gate rows are followed by its F up rows,
- * so splitting one expert's projection into two halves along the output axis
+ * bias1 [E, 2F, d/64]; 8-bit: codes [E, 2F, d], scale1 [E, 2F]): expert e's
+ * F gate rows are followed by its F up rows, so splitting one expert's projection into two halves along the output axis
  * gives (gate, up), and the experts' blocks are interleaved, not two stacked
  * tensors.  w2, scale2 and bias2 must then be NULL.  The shared expert always
  * uses the separate layout.
@@ -525,7 +525,10 @@ moe_status moe_forward(const moe_config *cfg, const void *x, const float *w_rout
  * status.  The kernel's blocks wait for one another, so it is launched
  * cooperatively: it starts when every SM has room for its block, and two
  * such calls on different streams run one after the other.  No phase events
- * are recorded.  Uses ws. */
+ * are recorded.  Uses ws, which holds the counters that the blocks meet at:
+ * calls, or replays of captured calls, that may overlap need a workspace each
+ * (as with every call; here an overlap on one runs into the wait limit and a
+ * device status). */
 #define MOE_FEW_TOKENS 16
 moe_status moe_forward_few(const moe_config *cfg, const void *x, const float *w_router, const float *router_bias,
                            const moe_weights *w, void *out, int32_t *topk_ids, float *topk_w, const moe_stats *stats,

@@ -310,6 +310,35 @@ def test_few_graph_and_streams(name):
     assert run.status() == 0 and other.status() == 0
 
 
+def test_few_two_graphs_at_once():
+    """Two captured layers, a workspace each, replayed on two streams without
+    waiting for one another."""
+    layers, want, graphs = [], [], []
+    for name, seed in (("groups_shared", 1), ("i8_shared", 2)):
+        run = make_run(name, seed=seed)
+        layer = api.MoELayer(run.cfg, run.inp["w_router"], run.weights, router_bias=run.bias)
+        layer.forward_few(run.inp["x"])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            layer.forward_few(run.inp["x"])
+        layers.append((layer, run))
+        want.append(layer.o.out.clone())
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for layer, _ in layers:
+        layer.o.out.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for (layer, _), out in zip(layers, want):
+        assert layer.status() == 0
+        assert torch.equal(layer.o.out, out)
+
+
 @pytest.mark.parametrize("name", ["long_rows", "i8_long", "q4_long", "groups_shared"])
 def test_few_wait_timeout_reports_and_recovers(name):
     """With a 1 ns bound the first wait that is not already over gives up: a

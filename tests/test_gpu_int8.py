@@ -223,6 +223,18 @@ def test_quantized_matmul_nan_rows_stay_apart():
         check_mm(out[torch.from_numpy(~bad).cuda()], ref[~bad], "f32")
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_quantized_matmul_bits_do_not_depend_on_the_batch(dt):
+    """A row's result is the same bits in a batch of one, of sixteen, of a
+    hundred and of a thousand rows, which run in different kernels."""
+    q, s, wq, ws = mm_inputs(1000, 2312, 1040)
+    full, st = run_mm(q, s, wq, ws, dt)
+    assert st == 0
+    for rows in (1, 16, 100):
+        part, st = run_mm(q[:rows], s[:rows], wq, ws, dt)
+        assert st == 0 and torch.equal(part, full[:rows])
+
+
 def test_quantized_matmul_no_rows():
     w = torch.full((256,), 0xA5, dtype=torch.uint8, device="cuda")
     e8 = lambda *s: torch.zeros(s, dtype=torch.int8, device="cuda")
