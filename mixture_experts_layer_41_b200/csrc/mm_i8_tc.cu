@@ -303,7 +303,8 @@ cudaError_t run(const MmI8Args &a, cudaStream_t s) {
   const int grid = (int)(upper < sms ? upper : sms);
   err = cudaFuncSetAttribute(i8_grouped_gemm<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<BN>());
   if (err != cudaSuccess) return err;
-  launch_plain(i8_grouped_gemm<BN>, grid, THREADS, smem_bytes<BN>(), s, ma, mb0, mb1, p);
+  // (scheduled while the row quantisation ends, as the pairs' launch explains)
+  launch_pdl(i8_grouped_gemm<BN>, grid, THREADS, smem_bytes<BN>(), s, ma, mb0, mb1, p);
   return cudaGetLastError();
 }
 

@@ -17,8 +17,8 @@
 //
 // Bound by HBM: each element is read once (a row stays in registers between
 // the maximum and the codes) and each code written once.  A warp takes a row
-// of up to 1024 elements, and from 1024 rows on one of up to 4096 (fp32:
-// 2048); a block of 256 threads one of up to 16384; longer rows are read a
+// of up to 1024 elements, and of a matrix of many rows one of up to 4096
+// (fp32: 2048); a block of 256 threads one of up to 16384; longer rows are read a
 // second time, from L2.  bf16, 8192 rows of 2048: 18.2 us (28.9 with a block to
 // a row, whose two barriers every row waits for), 2.8 TB/s; 8192 of 14336:
 // 68 us, 5.2 TB/s.
@@ -33,7 +33,10 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int VECS = 8;       // 8-element vectors a thread keeps in registers
-constexpr int WARP_ROWS = 1024;   // 256 rows of 4096: 3.0 us by blocks, one wave of long chains by warps
+// rows from which a warp takes each.  us by blocks to by warps: bf16, 512 rows of
+// 4096 3.8 to 5.9, 1024 6.4 to 6.6, 2048 10.9 to 9.3; fp32, 256 rows of 2048
+// 2.8 (by blocks), 384 4.5 to 4.3, 777 6.8 to 4.8
+constexpr int warp_rows_from(bool bf16) { return bf16 ? 1024 : 384; }
 
 struct QuantParams {
   const void *x;
@@ -198,7 +201,7 @@ quantize_rows_kernel(const QuantParams p) {
 template <bool BF16>
 cudaError_t run(const QuantParams &p, cudaStream_t s) {
   constexpr int LONG = BF16 ? 16 : 8;       // vectors of a warp's lane in longer rows (64 registers)
-  const bool warp_rows = p.K <= 4 * 32 * 8 || (p.K <= LONG * 32 * 8 && p.rows >= WARP_ROWS);
+  const bool warp_rows = p.K <= 4 * 32 * 8 || (p.K <= LONG * 32 * 8 && p.rows >= warp_rows_from(BF16));
   const long long blocks = warp_rows ? (p.rows + THREADS / 32 - 1) / (THREADS / 32) : p.rows;
   const int grid = (int)(blocks < 148 * 64 ? blocks : 148 * 64);
   if (p.K <= 4 * 32 * 8)
