@@ -251,7 +251,9 @@ i8_grouped_gemm(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
       const int col0 = ti.n * (swiglu ? BN / 2 : BN);
       load_scales<BN>(sc, p.ws0, p.ws1, (size_t)ti.g * p.b_stride, p.mode, p.N, col0);
       const float xs = valid ? __ldg(p.xs + row) : 0.f;
-      if (!wait_bounded(&st->acc_full[buf], use & 1u, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns)) break;
+      // the warp goes on together or not at all
+      const bool ok = wait_bounded(&st->acc_full[buf], use & 1u, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       store_tile<BN>(tmem_base + buf * BN + ((uint32_t)(q * 32) << 16), sc, xs, p.mode, p.out, p.N, row, col0, valid);
       tc_fence_before();
