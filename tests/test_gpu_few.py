@@ -310,6 +310,17 @@ def test_few_graph_and_streams(name):
     assert run.status() == 0 and other.status() == 0
 
 
+def test_few_refuses_tensors_elsewhere():
+    """A tensor left on the host is refused before the launch."""
+    run = make_run("groups_shared")
+    args = [run.cfg, run.inp["x"], run.inp["w_router"], run.bias, run.weights, run.out, None, None, None, run.ws]
+    for i in (1, 2, 3, 5, 9):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            api.moe_forward_few(*(a.cpu() if j == i else a for j, a in enumerate(args)))
+    with pytest.raises(ValueError, match="current CUDA device"):
+        api.moe_forward_few(*args[:4], dict(run.weights, w3=run.weights["w3"].cpu()), *args[5:])
+
+
 def test_few_two_graphs_at_once():
     """Two captured layers, a workspace each, replayed on two streams without
     waiting for one another."""

@@ -438,3 +438,29 @@ def test_quantized_calls_refuse_tensors_elsewhere():
     for i in range(7):
         with pytest.raises(ValueError, match="current CUDA device"):
             api.moe_quantized_matmul(*(a.cpu() if j == i else a for j, a in enumerate(args)))
+
+
+def test_quantized_matmul_calls_at_once():
+    """A large product on one stream and many small ones on another, a
+    workspace each: the bits of the calls one after the other."""
+    d = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    calls = []
+    for rows, n, k in ((1090, 2312, 1040), (5, 520, 2320)):
+        q, s, wq, ws = (d(a) for a in mm_inputs(rows, n, k))
+        w = torch.empty(api.moe_quantized_matmul_workspace_size(1, rows, n, k), dtype=torch.uint8, device="cuda")
+        calls.append((q, s, wq, ws, torch.zeros((rows, n), device="cuda"), w))
+    want = []
+    for c in calls:
+        api.moe_quantized_matmul(*c)
+        want.append(c[4].clone())
+        c[4].zero_()
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(10):
+        api.moe_quantized_matmul(*calls[0], stream=streams[0])
+        for _ in range(5):
+            api.moe_quantized_matmul(*calls[1], stream=streams[1])
+    torch.cuda.synchronize()
+    for c, out in zip(calls, want):
+        assert api.moe_workspace_status(c[5]) == 0
+        assert torch.equal(c[4], out)
