@@ -30,8 +30,9 @@
 // No copy multicasts.
 //
 // Every mbarrier wait is bounded (moe_set_wait_timeout_ns); on expiry the
-// thread records a status code, raises its CTA's abort flag and drains what it
-// issued; both CTAs meet at the final cluster barrier and free their TMEM.
+// thread records a status code, raises its CTA's abort flag and stops.  Either
+// way the CTAs leave only when nothing comes to their shared memory any more
+// (pair_leave), and free their TMEM.
 #include "mm_i8.cuh"
 
 namespace moe {
@@ -67,6 +68,7 @@ struct PairShared {
   uint64_t acc_full[2];      // every CTA: an accumulator holds a finished tile
   uint64_t acc_empty[2];     // even CTA: both CTAs' epilogues have read it
   uint64_t drain;
+  __align__(16) PairWork mine, theirs;
   uint32_t tmem_base;
   int abort_flag;
   int32_t off[kMaxExperts + 1];
@@ -169,6 +171,7 @@ i8_pair_gemm(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__ 
     }
     mbar_init(&st->drain, 1);
     st->abort_flag = 0;
+    st->mine = {};
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -232,19 +235,7 @@ i8_pair_gemm(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__ 
           }
         }
       }
-      if (!ok) {
-        if (leader) {
-          const uint32_t first = it > (uint32_t)STAGES ? it - STAGES : 0u;
-          for (uint32_t i = first; i < it; ++i)
-            if (!wait_drain<true>(&st->full[i % STAGES], (i / STAGES) & 1u)) record_status(p.status, kDevTimeoutDrain);
-        } else {
-          // the odd CTA's copies complete on the even CTA's barriers: give
-          // the ones in flight time to land before this CTA can leave
-          const uint64_t t0 = global_ns();
-          while (global_ns() - t0 < 1000000ull) {
-          }
-        }
-      }
+      st->mine.issued = (int)it;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -284,6 +275,8 @@ i8_pair_gemm(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__ 
       }
       // every MMA this thread issued has completed once `drain` flips
       tc_commit_pair(&st->drain);
+      st->mine.committed = (int)it;
+      st->mine.tiles = (int)tcount;
       if (!wait_drain<true>(&st->drain, 0u)) record_status(p.status, kDevTimeoutDrain);
     }
     __syncwarp();
@@ -357,9 +350,10 @@ i8_pair_gemm(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__ 
   }
 
   tc_fence_before();
-  __syncthreads();
-  pdl_trigger();                         // tiles done: the next kernel may be scheduled
-  cluster_sync();                        // the pair's MMAs and remote arrivals are over
+  pair_leave<STAGES>(st->full, st->empty, st->acc_full, &st->drain, &st->mine, &st->theirs, abort_flag, p.status,
+                     [&](int i) {
+                       return (uint32_t)(A_BYTES + decode_tile(st, G, cluster + i / kb_n * n_clusters).cols / 2 * BK);
+                     });
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS)

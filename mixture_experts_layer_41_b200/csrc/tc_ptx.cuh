@@ -138,6 +138,65 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t *bar) {
       "h"((uint16_t)3)
       : "memory");
 }
+// counts bytes as arrived that no copy will bring
+__device__ __forceinline__ void mbar_complete_tx(uint64_t *bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
+               : "memory");
+}
+// What a CTA of a pair has under way when its roles have ended: K-blocks its
+// producer issued, and K-blocks and tiles the even CTA's issuer committed.
+struct PairWork {
+  int issued, committed, tiles, aborted;
+};
+// The way out of a pair's kernel, for all threads of both CTAs, once thread 0
+// of each has its own `mine` (zeros at the start) complete but for `aborted`.
+// Neither CTA may leave while anything still comes to its shared memory, and
+// a cluster barrier alone does not say so: it orders the threads, not the
+// commits' arrivals at the other CTA nor, after an abort, the copies.  The
+// CTAs tell one another what they had under way; each waits for its own last
+// arrivals, and after an abort the even CTA, on whose barriers both CTAs'
+// copies complete, for the copies of both: where only one of them issued a
+// K-block, the barrier is armed for that half, or told that the other will
+// not come.  `half` (K-block): bytes of one CTA's copies.
+template <int STAGES, class Bytes>
+__device__ __forceinline__ void pair_leave(uint64_t *full, uint64_t *empty, uint64_t *acc_full, uint64_t *drain,
+                                           PairWork *mine, PairWork *theirs, const volatile int *abort_flag,
+                                           int *status, Bytes half) {
+  const uint32_t rank = cluster_rank();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    mine->aborted = *abort_flag;
+    const uint32_t to = map_to_rank(smem_u32(theirs), rank ^ 1u);
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(mine->issued), "r"(mine->committed),
+                 "r"(mine->tiles), "r"(mine->aborted)
+                 : "memory");
+  }
+  __syncwarp();
+  pdl_trigger();                         // tiles done: the next kernel may be scheduled
+  cluster_sync();
+  const bool aborted = mine->aborted || theirs->aborted;
+  if (threadIdx.x == 0) {
+    const PairWork &w = rank == 0 ? *mine : *theirs;
+    bool ok = true;
+    for (int i = max(0, w.committed - STAGES); i < w.committed; ++i)
+      ok &= wait_drain<true>(&empty[i % STAGES], (i / STAGES) & 1);
+    for (int t = max(0, w.tiles - 2); t < w.tiles; ++t) ok &= wait_drain<true>(&acc_full[t & 1], (t >> 1) & 1);
+    ok &= wait_drain<true>(drain, 0u);
+    if (aborted && rank == 0) {
+      const int n = max(mine->issued, theirs->issued);
+      for (int i = max(0, n - STAGES); i < n; ++i) {
+        uint64_t *bar = &full[i % STAGES];
+        if (i >= mine->issued) mbar_expect_tx(bar, half(i));
+        if (i >= theirs->issued) mbar_complete_tx(bar, half(i));
+        ok &= wait_drain<true>(bar, (i / STAGES) & 1);
+      }
+    }
+    if (!ok) record_status(status, kDevTimeoutDrain);
+  }
+  __syncwarp();
+  if (aborted) cluster_sync();           // the odd CTA stays until its copies have landed
+}
+
 // Shared-memory matrix descriptor for a K-major tile written by TMA with the
 // 128-byte swizzle: 8-row core groups 1024 bytes apart (stride byte offset),
 // descriptor version 1, layout SWIZZLE_128B.  Advancing K by 32 int8 inside

@@ -1,0 +1,82 @@
+"""Barrier waits that run out at different points of the tensor-core kernels.
+
+Under a limit between 1 ns and a few tens of us a call gives up early, in the
+middle, or not at all.  Whatever it does, it has to say so (a status, or the
+right bits), let what it has under way land, and return long before any of its
+drains runs out; the next call under the default limit has to be right."""
+from __future__ import annotations
+
+import time
+
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_layer_41_b200 import _lib as L
+from mixture_experts_layer_41_b200 import api
+from mixture_experts_layer_41_b200.inputs import workload
+from test_gpu_int8 import I8Run, mm_inputs
+
+pytestmark = pytest.mark.gpu
+
+LIMITS_NS = (1, 200, 1000, 2000, 4000, 8000, 16000, 32000)
+DRAIN_S = 0.2          # one drain that runs out takes this long
+
+
+def i8_product(rows, n, k, groups=1, offsets=None):
+    d = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    q, s, wq, ws = (d(a) for a in mm_inputs(rows, n, k, groups))
+    out = torch.zeros((rows, n), dtype=torch.bfloat16, device="cuda")
+    ws8 = torch.empty(api.moe_quantized_matmul_workspace_size(groups, rows, n, k), dtype=torch.uint8, device="cuda")
+    off = None if offsets is None else torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    return lambda: api.moe_quantized_matmul(q, s, wq, ws, out, ws8, group_offsets=off), out, ws8
+
+
+def ffn(run):
+    run.staged()
+    assert run.status() == 0
+    call = lambda: api.moe_grouped_ffn(run.cfg, run.x_perm, run.offsets, run.weights, run.y_perm, run.ws)
+    return call, run.y_perm, run.ws
+
+
+CALLS = {
+    # 8-bit product on pairs of SMs: one group, ragged groups (last tiles of 64 to 256 tokens), SwiGLU
+    "i8_pair": lambda: i8_product(1090, 2312, 2320),
+    "i8_pair_groups": lambda: i8_product(1100, 1544, 1040, 4, [0, 300, 310, 900, 1100]),
+    "i8_pair_swiglu": lambda: ffn(I8Run(workload("mixtral_prefill", T=900, d=1040, F=1056, E=4), seed=35)),
+}
+
+
+def timed(call, ws):
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    call()
+    torch.cuda.synchronize()
+    return time.perf_counter() - t0, api.moe_workspace_status(ws)
+
+
+@pytest.mark.parametrize("name", sorted(CALLS))
+def test_waits_that_run_out(name):
+    call, out, ws = CALLS[name]()
+    assert timed(call, ws)[1] == 0
+    want = out.clone()
+    gave_up = 0
+    for limit in LIMITS_NS:
+        for _ in range(6):
+            out.zero_()
+            api.moe_set_wait_timeout_ns(limit)
+            try:
+                seconds, status = timed(call, ws)
+            finally:
+                api.moe_set_wait_timeout_ns(0)
+            assert seconds < DRAIN_S, (limit, seconds)
+            if status == 0:
+                assert torch.equal(out.view(torch.int16), want.view(torch.int16)), limit
+            else:
+                assert status == L.MOE_ERR_DEVICE, (limit, status)
+                text = L.lib().moe_last_error().decode()
+                assert "wait timed out" in text, (limit, text)
+                gave_up += 1
+        assert timed(call, ws)[1] == 0
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16)), limit
+    assert gave_up >= 6, gave_up
