@@ -24,12 +24,10 @@
 // No copy multicasts: each CTA loads only its own tiles.
 //
 // Every mbarrier wait is bounded by %globaltimer (2 s unless moe_set_wait_timeout_ns says otherwise); on expiry the thread
-// records a status code, raises its CTA's abort flag and drains what it
-// issued; both CTAs meet at the final cluster barrier and free TMEM.
-#include "common.cuh"
-
-#include <cuda.h>
-#include <cudaTypedefs.h>
+// records a status code, raises its CTA's abort flag and stops.  Either way the
+// CTAs leave only when nothing comes to their shared memory any more
+// (pair_leave), and free their TMEM.
+#include "tc_ptx.cuh"
 
 namespace moe {
 namespace {
@@ -65,6 +63,7 @@ struct Shared2 {
   uint64_t acc_full[2];      // every CTA: an accumulator holds a finished tile
   uint64_t acc_empty[2];     // even CTA: both CTAs' epilogues have read it
   uint64_t drain;
+  __align__(16) ptx::PairWork mine, theirs;
   uint32_t tmem_base;
   int abort_flag;
   int32_t off[kMaxExperts + 1];
@@ -231,6 +230,7 @@ tc2_grouped_gemm(const __grid_constant__ CUtensorMap mapA, const __grid_constant
     }
     mbar_init(&st->drain, 1);
     st->abort_flag = 0;
+    st->mine = {};
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -297,19 +297,7 @@ tc2_grouped_gemm(const __grid_constant__ CUtensorMap mapA, const __grid_constant
           tma_load_2d_pair(smem_u32(sa + A_BYTES), mb, fb, kb * BK, brow);
         }
       }
-      if (!ok) {
-        if (leader) {
-          const uint32_t first = it > (uint32_t)STAGES ? it - STAGES : 0u;
-          for (uint32_t i = first; i < it; ++i)
-            if (!wait_drain(&st->full[i % STAGES], (i / STAGES) & 1u)) record_status(p.status, kDevTimeoutDrain);
-        } else {
-          // the odd CTA's copies complete on the even CTA's barriers: give
-          // the ones in flight time to land before this CTA can leave
-          const uint64_t t0 = global_ns();
-          while (global_ns() - t0 < 1000000ull) {
-          }
-        }
-      }
+      st->mine.issued = (int)it;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -346,6 +334,8 @@ tc2_grouped_gemm(const __grid_constant__ CUtensorMap mapA, const __grid_constant
         ++tcount;
       }
       tc_commit_pair(&st->drain);
+      st->mine.committed = (int)it;
+      st->mine.tiles = (int)tcount;
       if (!wait_drain(&st->drain, 0u)) record_status(p.status, kDevTimeoutDrain);
     }
     __syncwarp();
@@ -427,9 +417,8 @@ tc2_grouped_gemm(const __grid_constant__ CUtensorMap mapA, const __grid_constant
   }
 
   tc_fence_before();
-  __syncthreads();
-  pdl_trigger();                         // tiles done: the next kernel may be scheduled
-  cluster_sync();                        // the pair's MMAs and remote arrivals are over
+  ptx::pair_leave<STAGES>(st->full, st->empty, st->acc_full, &st->drain, &st->mine, &st->theirs, abort_flag, p.status,
+                          [](int) { return (uint32_t)STAGE_BYTES; });
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS)

@@ -1,6 +1,7 @@
 // Device wrappers of the barrier, bulk-copy and tensor-core instructions, and
 // the host call that encodes a tensor map, shared by the 8-bit and few-token
-// kernels.  Internal to the library.
+// kernels, and the way out of a pair, also the bf16 pairs'.  Internal to the
+// library.
 #pragma once
 
 #include "common.cuh"

@@ -12,6 +12,7 @@ import numpy as np
 import pytest
 import torch
 
+from gpu_harness import Run
 from mixture_experts_layer_41_b200 import _lib as L
 from mixture_experts_layer_41_b200 import api
 from mixture_experts_layer_41_b200.inputs import workload
@@ -44,7 +45,12 @@ CALLS = {
     "i8_pair": lambda: i8_product(1090, 2312, 2320),
     "i8_pair_groups": lambda: i8_product(1100, 1544, 1040, 4, [0, 300, 310, 900, 1100]),
     "i8_pair_swiglu": lambda: ffn(I8Run(workload("mixtral_prefill", T=900, d=1040, F=1056, E=4), seed=35)),
+    "bf16_pair": lambda: ffn(Run(workload("mixtral_prefill", T=1100, d=1032, F=1160, E=4), seed=35)),
+    "bf16_pair_relu": lambda: ffn(Run(workload("switch_top1", T=1300, d=1032, F=1160, E=4, capacity_factor=0.0), seed=35)),
 }
+
+# the environment that selects a kernel
+ENV = {"bf16_pair": {"MOE_TC_PAIR": "1"}, "bf16_pair_relu": {"MOE_TC_PAIR": "1"}}
 
 
 def timed(call, ws):
@@ -56,7 +62,9 @@ def timed(call, ws):
 
 
 @pytest.mark.parametrize("name", sorted(CALLS))
-def test_waits_that_run_out(name):
+def test_waits_that_run_out(name, monkeypatch):
+    for key, value in ENV.get(name, {}).items():
+        monkeypatch.setenv(key, value)
     call, out, ws = CALLS[name]()
     assert timed(call, ws)[1] == 0
     want = out.clone()
