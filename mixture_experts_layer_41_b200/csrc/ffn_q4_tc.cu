@@ -144,6 +144,12 @@ __device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, vol
   }
   return true;
 }
+// The same for a warp, which goes on together or not at all: the tensor-memory
+// instructions that follow need all of its lanes.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status, int code,
+                                          uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, status, code, limit_ns));
+}
 __device__ __forceinline__ bool wait_drain(uint64_t *bar, uint32_t parity) {
   const uint64_t t0 = global_ns();
   while (!mbar_try_wait(bar, parity))
@@ -448,7 +454,7 @@ q4_tc_gemm(const __grid_constant__ CUtensorMap mapC0, const __grid_constant__ CU
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x, ++tc) {
       const Tile ti = decode_tile(st, nE, m_tiles, tile);
       const uint32_t sb = tc & 1u;
-      if (!wait_bounded(&st->sc_full[sb], (tc >> 1) & 1u, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns)) {
+      if (!wait_warp(&st->sc_full[sb], (tc >> 1) & 1u, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns)) {
         ok = false;
         break;
       }
@@ -461,7 +467,7 @@ q4_tc_gemm(const __grid_constant__ CUtensorMap mapC0, const __grid_constant__ CU
         const int s = (int)(it % STAGES);
         const uint32_t ph = (it / STAGES) & 1u;
         const uint32_t j = it % SLOTS, use = it / SLOTS;
-        if (!wait_bounded(&st->full[s], ph, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns)) {
+        if (!wait_warp(&st->full[s], ph, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns)) {
           ok = false;
           break;
         }
@@ -488,7 +494,7 @@ q4_tc_gemm(const __grid_constant__ CUtensorMap mapC0, const __grid_constant__ CU
           const uint4 d = dequant8(wv[w], s2, b2);
           av[4 * w] = d.x; av[4 * w + 1] = d.y; av[4 * w + 2] = d.z; av[4 * w + 3] = d.w;
         }
-        if (!wait_bounded(&st->a_empty[j], (use & 1u) ^ 1u, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns)) {
+        if (!wait_warp(&st->a_empty[j], (use & 1u) ^ 1u, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns)) {
           ok = false;
           break;
         }
@@ -517,7 +523,7 @@ q4_tc_gemm(const __grid_constant__ CUtensorMap mapC0, const __grid_constant__ CU
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++tc) {
       const Tile ti = decode_tile(st, nE, m_tiles, tile);
       const uint32_t abuf = tc & 1u;
-      if (!wait_bounded(&st->acc_full[abuf], (tc >> 1) & 1u, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns)) break;
+      if (!wait_warp(&st->acc_full[abuf], (tc >> 1) & 1u, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns)) break;
       tc_fence_after();
       const uint32_t ta = tmem_base + ((uint32_t)(q * 32) << 16) + abuf * S::ACC_COLS;
       const int f = ti.m * BM + row;

@@ -144,6 +144,13 @@ __device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, vol
   return true;
 }
 
+// The same for a warp, which goes on together or not at all: the tensor-memory
+// instructions that follow need all of its lanes.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status, int code,
+                                          uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, status, code, limit_ns));
+}
+
 // Wait used only while draining after an abort: ignores the abort flag.
 __device__ __forceinline__ bool wait_drain(uint64_t *bar, uint32_t parity) {
   const uint64_t t0 = global_ns();
@@ -460,7 +467,7 @@ tc_grouped_gemm(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
       const TileInfo ti = decode_tile(st, nE, p.n_tiles, p.shared_rows, tile);
       const uint32_t buf = tcount & 1u, use = tcount >> 1;
-      if (!wait_bounded(&st->acc_full[buf], use & 1u, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns)) break;
+      if (!wait_warp(&st->acc_full[buf], use & 1u, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns)) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + buf * BN + ((uint32_t)(q * 32) << 16);
       const bool valid = rloc < ti.rows;

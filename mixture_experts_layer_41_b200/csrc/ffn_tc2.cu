@@ -129,6 +129,12 @@ __device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, vol
   }
   return true;
 }
+// The same for a warp, which goes on together or not at all: the tensor-memory
+// instructions that follow need all of its lanes.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status, int code,
+                                          uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, status, code, limit_ns));
+}
 __device__ __forceinline__ bool wait_drain(uint64_t *bar, uint32_t parity) {
   const uint64_t t0 = global_ns();
   while (!mbar_try_wait(bar, parity))
@@ -347,7 +353,7 @@ tc2_grouped_gemm(const __grid_constant__ CUtensorMap mapA, const __grid_constant
     for (int tile = cluster; tile < total; tile += n_clusters) {
       const Tile2 ti = decode_tile2(st, nE, tile);
       const uint32_t buf = tcount & 1u, use = tcount >> 1;
-      if (!wait_bounded(&st->acc_full[buf], use & 1u, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns)) break;
+      if (!wait_warp(&st->acc_full[buf], use & 1u, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns)) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + buf * BN + ((uint32_t)(q * 32) << 16);
       const int row = ti.row0 + (int)rank * BM + rloc;

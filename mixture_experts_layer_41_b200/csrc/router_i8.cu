@@ -186,6 +186,12 @@ __device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, vol
   }
   return true;
 }
+// The same for a warp, which goes on together or not at all: the tensor-memory
+// instructions that follow need all of its lanes.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status, int code,
+                                          uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, status, code, limit_ns));
+}
 __device__ __forceinline__ bool wait_drain(uint64_t *bar, uint32_t parity) {
   const uint64_t t0 = global_ns();
   while (!mbar_try_wait(bar, parity))
@@ -853,7 +859,7 @@ route_i8_gemm(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ 
     const int q = warp & 3, h = cw >> 2;
     const int r = q * 32 + lane;
     const bool have_tmem =
-        wait_bounded(&st->tmem_full, 0u, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns);
+        wait_warp(&st->tmem_full, 0u, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns);
     tc_fence_after();
     const uint32_t tmem_base = st->tmem_base;
     // (the row's scale is read here, so the copies start without waiting for it)
@@ -870,8 +876,8 @@ route_i8_gemm(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ 
     bool ok = have_tmem;
     for (int it = 0; ok && it < kb_n; ++it) {
       const int xs = it % XS, as = it % AS;
-      if (!wait_bounded(&st->x_full[xs], (it / XS) & 1, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns) ||
-          !wait_bounded(&st->k_empty[as], ((it / AS) & 1) ^ 1, abort_flag, p.status, kDevTimeoutEpilogue,
+      if (!wait_warp(&st->x_full[xs], (it / XS) & 1, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns) ||
+          !wait_warp(&st->k_empty[as], ((it / AS) & 1) ^ 1, abort_flag, p.status, kDevTimeoutEpilogue,
                         p.timeout_ns)) {
         ok = false;
         break;
@@ -913,7 +919,7 @@ route_i8_gemm(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ 
     }
     // ---------------------------------------------------------- epilogue
     const bool acc_ok = ok && kb_n > 0 &&
-                        wait_bounded(&st->acc_full, 0u, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns);
+                        wait_warp(&st->acc_full, 0u, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns);
     if (!acc_ok) {
       if (have_tmem) {
         tmem_wait_st();

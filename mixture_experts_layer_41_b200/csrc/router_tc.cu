@@ -115,6 +115,12 @@ __device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, vol
   }
   return true;
 }
+// The same for a warp, which goes on together or not at all: the tensor-memory
+// instructions that follow need all of its lanes.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status, int code,
+                                          uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, status, code, limit_ns));
+}
 __device__ __forceinline__ bool wait_drain(uint64_t *bar, uint32_t parity) {
   const uint64_t t0 = global_ns();
   while (!mbar_try_wait(bar, parity))
@@ -315,7 +321,7 @@ route_tc_gemm(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ 
     const int n_chunks = (kb_n + FLUSH - 1) / FLUSH;
     for (int chunk = 0; chunk < n_chunks; ++chunk) {
       const uint32_t buf = chunk & 1, use = chunk >> 1;
-      if (!wait_bounded(&st->acc_full[buf], use & 1, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns)) {
+      if (!wait_warp(&st->acc_full[buf], use & 1, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns)) {
         ok = false;
         break;
       }
