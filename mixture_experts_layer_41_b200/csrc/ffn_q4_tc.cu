@@ -386,14 +386,14 @@ q4_tc_gemm(const __grid_constant__ CUtensorMap mapC0, const __grid_constant__ CU
           tma_load_2d(smem_u32(sp + MATS * CODE_BYTES), &mapB, fb, kb * BK, ti.row0);
         }
       }
-      if (!ok) {
-        const uint32_t first = it > (uint32_t)STAGES ? it - STAGES : 0u;
-        for (uint32_t i = first; i < it; ++i)
-          if (!wait_drain(&st->full[i % STAGES], (i / STAGES) & 1u)) record_status(p.status, kDevTimeoutDrain);
-        for (uint32_t b = 0; b < 2 && b < sc_issued; ++b) {
-          const uint32_t last = sc_issued - 1 - b;
-          if (!wait_drain(&st->sc_full[last & 1u], (last >> 1) & 1u)) record_status(p.status, kDevTimeoutDrain);
-        }
+      // let the copies already issued land before the CTA goes away: all of them
+      // have when the converters used them, but they may have given up
+      const uint32_t first = it > (uint32_t)STAGES ? it - STAGES : 0u;
+      for (uint32_t i = first; i < it; ++i)
+        if (!wait_drain(&st->full[i % STAGES], (i / STAGES) & 1u)) record_status(p.status, kDevTimeoutDrain);
+      for (uint32_t b = 0; b < 2 && b < sc_issued; ++b) {
+        const uint32_t last = sc_issued - 1 - b;
+        if (!wait_drain(&st->sc_full[last & 1u], (last >> 1) & 1u)) record_status(p.status, kDevTimeoutDrain);
       }
     }
     __syncwarp();

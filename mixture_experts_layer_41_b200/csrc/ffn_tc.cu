@@ -380,7 +380,8 @@ tc_grouped_gemm(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
         }
       }
     }
-    if (!ok && lane == 0) {
+    if (lane == 0) {
+      // let the copies already issued land, as below
       const uint32_t first = it > (uint32_t)STAGES ? it - STAGES : 0u;
       for (uint32_t i = first; i < it; ++i)
         if (!wait_drain(&st->full[i % STAGES], (i / STAGES) & 1u)) record_status(p.status, kDevTimeoutDrain);
@@ -413,12 +414,11 @@ tc_grouped_gemm(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
           tma_load_2d(smem_u32(sa + A_BYTES + BH_BYTES), mb1, fb, kb * BK, b1);
         }
       }
-      if (!ok) {
-        // let the copies already issued land before the CTA goes away
-        const uint32_t first = it > (uint32_t)STAGES ? it - STAGES : 0u;
-        for (uint32_t i = first; i < it; ++i)
-          if (!wait_drain(&st->full[i % STAGES], (i / STAGES) & 1u)) record_status(p.status, kDevTimeoutDrain);
-      }
+      // let the copies already issued land before the CTA goes away: all of them
+      // have when the issuer used them, but it may have given up
+      const uint32_t first = it > (uint32_t)STAGES ? it - STAGES : 0u;
+      for (uint32_t i = first; i < it; ++i)
+        if (!wait_drain(&st->full[i % STAGES], (i / STAGES) & 1u)) record_status(p.status, kDevTimeoutDrain);
     }
     __syncwarp();
   } else if (warp == 1) {

@@ -799,12 +799,12 @@ route_i8_gemm(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ 
           ok = false;
         }
       }
-      if (!ok) {
-        for (int i = ix > XS ? ix - XS : 0; i < ix; ++i)
-          if (!wait_drain(&st->x_full[i % XS], (i / XS) & 1)) record_status(p.status, kDevTimeoutDrain);
-        for (int i = iw > WS ? iw - WS : 0; i < iw; ++i)
-          if (!wait_drain(&st->w_full[i % WS], (i / WS) & 1)) record_status(p.status, kDevTimeoutDrain);
-      }
+      // let the copies already issued land before the CTA goes away: all of them
+      // have when the converters and the issuer used them, but they may have given up
+      for (int i = ix > XS ? ix - XS : 0; i < ix; ++i)
+        if (!wait_drain(&st->x_full[i % XS], (i / XS) & 1)) record_status(p.status, kDevTimeoutDrain);
+      for (int i = iw > WS ? iw - WS : 0; i < iw; ++i)
+        if (!wait_drain(&st->w_full[i % WS], (i / WS) & 1)) record_status(p.status, kDevTimeoutDrain);
     }
     __syncwarp();
   } else if (warp == 1) {

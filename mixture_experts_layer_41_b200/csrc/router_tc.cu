@@ -250,13 +250,10 @@ route_tc_gemm(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ 
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       int it = 0;
-      bool ok = true;
       for (; it < kb_n; ++it) {
         const int s = it % STAGES;
-        if (!wait_bounded(&st->empty[s], ((it / STAGES) & 1) ^ 1, abort_flag, p.status, kDevTimeoutProducer, p.timeout_ns)) {
-          ok = false;
+        if (!wait_bounded(&st->empty[s], ((it / STAGES) & 1) ^ 1, abort_flag, p.status, kDevTimeoutProducer, p.timeout_ns))
           break;
-        }
         uint8_t *sp = tiles + (size_t)s * S::STAGE_BYTES;
         const uint32_t fb = smem_u32(&st->full[s]);
         const int kx = (kb0 + it) * BK;
@@ -266,11 +263,11 @@ route_tc_gemm(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ 
         for (int part = 0; part < NSPLIT; ++part)
           tma_load_2d(smem_u32(sp + S::A_BYTES + part * S::B_BYTES), &mapW, fb, kx, part * p.e_pad + e0);
       }
-      if (!ok) {
-        const int first = it > STAGES ? it - STAGES : 0;
-        for (int i = first; i < it; ++i)
-          if (!wait_drain(&st->full[i % STAGES], (i / STAGES) & 1)) record_status(p.status, kDevTimeoutDrain);
-      }
+      // let the copies already issued land before the CTA goes away: all of them
+      // have when the issuer used them, but it may have given up
+      const int first = it > STAGES ? it - STAGES : 0;
+      for (int i = first; i < it; ++i)
+        if (!wait_drain(&st->full[i % STAGES], (i / STAGES) & 1)) record_status(p.status, kDevTimeoutDrain);
     }
     __syncwarp();
   } else if (warp == 1) {
