@@ -185,7 +185,10 @@ int64_t moe_capacity(int32_t num_tokens, int32_t top_k, int32_t num_experts, flo
  * with F32, BF16 and I8 weights. */
 moe_status moe_validate(const moe_config *cfg);
 
-/* Bytes of workspace any call below needs for this config (0 if invalid). */
+/* Bytes of workspace any call below needs for this config (0 if invalid).
+ * For bf16 layers of at most MOE_FEW_TOKENS tokens the last part is
+ * moe_forward_few's own; the other calls also take a workspace without it,
+ * such as one made for a larger batch. */
 size_t moe_workspace_size(const moe_config *cfg);
 
 /* Balancing loss from host copies of the stats: aux_raw = E * sum_e f_e P_e

@@ -175,7 +175,7 @@ struct WsLayout {
   size_t out_stage;    // act[T][d]
   size_t q_rows;       // int8[T*k][max(d, F)]  8-bit experts: codes of the rows a product reads
   size_t q_scale;      // float[T*k]            and their scales
-  size_t few;          // moe_forward_few's intermediates
+  size_t few;          // moe_forward_few's intermediates, last: no other call needs them
   size_t total;
   size_t region_bytes[MOE_WS_REGION_COUNT];   // unpadded sizes of the moe_ws_region buffers
 };

@@ -63,9 +63,13 @@ moe_status check_weights(const moe_config &c, const moe_weights *w) {
   return MOE_OK;
 }
 
-moe_status check_ws(const moe_config &c, const void *ws, size_t ws_bytes) {
+// The last part of the workspace is moe_forward_few's own, and only it needs
+// it: a workspace made for a larger batch (which has no such part) also serves
+// the other calls with few rows, as expert parallelism makes them.
+moe_status check_ws(const moe_config &c, const void *ws, size_t ws_bytes, bool few = false) {
   if (!aligned16(ws)) return MOE_ERR_WORKSPACE;
-  if (ws_bytes < ws_layout(c).total) return MOE_ERR_WORKSPACE;
+  const WsLayout L = ws_layout(c);
+  if (ws_bytes < (few ? L.total : L.few)) return MOE_ERR_WORKSPACE;
   return MOE_OK;
 }
 
@@ -752,7 +756,7 @@ moe_status moe_forward_few(const moe_config *cfg, const void *x, const float *w_
                 !aligned16_or_null(stats->prob_sum) || !aligned16_or_null(stats->dropped)))
     return MOE_ERR_INVALID_ARG;
   if ((st = check_weights(c, w)) != MOE_OK) return st;
-  if ((st = check_ws(c, ws, ws_bytes)) != MOE_OK) return st;
+  if ((st = check_ws(c, ws, ws_bytes, true)) != MOE_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if ((st = clear_status(ws, s)) != MOE_OK) return st;
   const WsLayout L = ws_layout(c);
