@@ -75,6 +75,55 @@ def _on_current(*tensors) -> None:
             raise ValueError(f"tensors must be on the current CUDA device (cuda:{dev}); got one on {t.device}")
 
 
+def _holds(needs) -> None:
+    """Refuses tensors of another type than the call takes them for, or with
+    fewer elements than it reads or writes: ``needs`` are (name, tensor, type,
+    elements).  A missing tensor passes: the library knows which may be."""
+    for name, t, dtype, n in needs:
+        if t is not None and (t.dtype is not dtype or t.numel() < n):
+            raise ValueError(f"{name} must be {dtype} with {n} elements for this config, not {t.dtype} with {t.numel()}")
+
+
+def _check_rows(cfg, x, out) -> None:
+    """The token rows of a layer call: [num_tokens, hidden] of the activations' type."""
+    dt, n = _TORCH_DT.get(cfg.act_dtype), cfg.num_tokens * cfg.hidden
+    if dt is not None:                                  # (else no valid config: the library says so)
+        _holds((("x", x, dt, n), ("out", out, dt, n)))
+
+
+def _check_few(cfg, x, w_router, router_bias, weights: dict, out, topk_ids, topk_w, stats) -> None:
+    """Every tensor of a few-token call (bf16 activations)."""
+    T, d, F, E, k, Fs = (cfg.num_tokens, cfg.hidden, cfg.intermediate, cfg.num_experts, cfg.top_k,
+                         cfg.shared_intermediate)
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    w, st = weights.get, (stats or {}).get
+    n = E * F * d
+    n1 = 2 * n if cfg.weight_layout == L.MOE_LAYOUT_FUSED_GATE_UP else n
+    relu, fmt = cfg.act == L.MOE_ACT_RELU, cfg.weight_dtype
+    w1, w2, w3 = w("w1"), None if relu else w("w2"), w("w3")
+    needs = [("x", x, bf16, T * d), ("out", out, bf16, T * d), ("w_router", w_router, f32, E * d),
+             ("router_bias", router_bias, f32, E), ("topk_ids", topk_ids, i32, T * k), ("topk_w", topk_w, f32, T * k)]
+    if stats is not None:
+        needs += [("raw_counts", st("raw_counts"), i32, E), ("kept_counts", st("kept_counts"), i32, E),
+                  ("prob_sum", st("prob_sum"), f32, E), ("dropped", st("dropped"), i32, 1)]
+    if fmt == L.MOE_BF16:
+        needs += [("w1", w1, bf16, n1), ("w2", w2, bf16, n), ("w3", w3, bf16, n)]
+    elif fmt == L.MOE_I8_CHANNEL:
+        needs += [("w1", w1, torch.int8, n1), ("w2", w2, torch.int8, n), ("w3", w3, torch.int8, n),
+                  ("s1", w("s1"), f32, n1 // d), ("s2", None if relu else w("s2"), f32, E * F), ("s3", w("s3"), f32, E * d)]
+    else:
+        for name, t, codes in (("w1", w1, n1), ("w2", w2, n), ("w3", w3, n)):       # in words of any width
+            if t is not None and (t.is_floating_point() or 2 * _nbytes(t) < codes):
+                raise ValueError(f"{name} must hold {codes} 4-bit codes in integer words, not {tuple(t.shape)} of {t.dtype}")
+        needs += [(p + i, w(p + i), bf16, g // 64) for p in "sb" for i, g in (("1", n1), ("2", n), ("3", n))]
+    if Fs > 0:
+        needs += [("ws1", w("ws1"), bf16, Fs * d), ("ws2", w("ws2"), bf16, Fs * d), ("ws3", w("ws3"), bf16, Fs * d)]
+    _holds(needs)
+    for name, t, n in (("x", x, T), ("out", out, T)):
+        if t is not None and t.numel() != n * d:
+            raise ValueError(f"{name} must be [{n}, {d}] for this config, not {tuple(t.shape)}")
+
+
 # ---------------------------------------------------------------- host-only calls
 
 def moe_capacity(num_tokens: int, top_k: int, num_experts: int, capacity_factor: float) -> int:
@@ -305,6 +354,7 @@ def moe_combine(cfg, y_perm, slot_row, topk_w, shared_out, out, stream=None):
 
 
 def moe_forward(cfg, x, w_router, router_bias, weights: dict, out, topk_ids, topk_w, stats, ws, stream=None):
+    _check_rows(cfg, x, out)
     w = _weights_struct(weights)
     st = _stats_struct(stats)
     check(L.lib().moe_forward(C.byref(cfg), _p(x), _p(w_router), _p(router_bias), C.byref(w), _p(out),
@@ -313,9 +363,12 @@ def moe_forward(cfg, x, w_router, router_bias, weights: dict, out, topk_ids, top
 
 
 def moe_forward_few(cfg, x, w_router, router_bias, weights: dict, out, topk_ids, topk_w, stats, ws, stream=None):
-    """``moe_forward`` for at most ``MOE_FEW_TOKENS`` tokens, in one kernel."""
-    if cfg.num_tokens <= L.MOE_FEW_TOKENS:      # (larger batches are refused below)
+    """``moe_forward`` for at most ``MOE_FEW_TOKENS`` tokens, in one kernel.
+    Tensors whose type or size is not the config's are refused (ValueError):
+    a batch of another size needs a config of its own."""
+    if cfg.num_tokens <= L.MOE_FEW_TOKENS and cfg.act_dtype == L.MOE_BF16:      # (others are refused below)
         _on_current(x, w_router, router_bias, out, topk_ids, topk_w, ws, *weights.values(), *(stats or {}).values())
+        _check_few(cfg, x, w_router, router_bias, weights, out, topk_ids, topk_w, stats)
     w = _weights_struct(weights)
     st = _stats_struct(stats)
     code = L.lib().moe_forward_few(C.byref(cfg), _p(x), _p(w_router), _p(router_bias), C.byref(w), _p(out),
@@ -386,7 +439,9 @@ class MoELayer:
                         o.topk_w, self.stats(), self.ws, stream)
             return o
         cfg = self.cfg
+        _check_rows(cfg, x, o.out)
         T, k, d = cfg.num_tokens, cfg.top_k, cfg.hidden
+        _holds((("forced_ids", forced_ids, torch.int32, T * k),))
         if not hasattr(self, "_stage"):
             i32 = dict(dtype=torch.int32, device=self.device)
             dt = _TORCH_DT[cfg.act_dtype]
