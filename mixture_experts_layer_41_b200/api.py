@@ -324,6 +324,8 @@ def moe_quantized_matmul(x_codes, x_scales, w_codes, w_scales, out, ws, group_of
     the rows of each group.  ``w_codes`` [n, k] or [groups, n, k]; ``out``
     [rows, n] bf16 or fp32; ``group_offsets`` [groups + 1] int32, needed when
     there is more than one group."""
+    if w_codes.dim() not in (2, 3):
+        raise ValueError(f"w_codes must be [n, k] or [groups, n, k], not {tuple(w_codes.shape)}")
     groups = w_codes.shape[0] if w_codes.dim() == 3 else 1
     n, k = w_codes.shape[-2:]
     rows = x_codes.shape[0]
