@@ -215,9 +215,12 @@ const char *moe_last_error(void);
 int64_t moe_kernel_launches(void);
 
 /* Bound on every on-chip barrier wait of the tensor-core kernels (grouped
- * GEMMs, the 4-bit tcgen05 FFN, the router's integer and bf16 tensor-core
- * logits and the integer plan's token-row streaming), in nanoseconds of the GPU's global
- * timer, for the launches that follow (process-wide, all threads).  When a
+ * GEMMs, 8-bit products, the 4-bit tcgen05 FFN, the router's integer and bf16
+ * tensor-core logits and the integer plan's token-row streaming) and on each
+ * wait of moe_forward_few's blocks for one another, which in a healthy call
+ * lasts until the slowest block has done its share of a phase (up to hundreds
+ * of us); in nanoseconds of the GPU's global timer, for the launches that
+ * follow (process-wide, all threads).  When a
  * wait runs out, the kernel records where in the workspace status word
  * (moe_workspace_status: MOE_ERR_DEVICE, "... wait timed out"), lets the
  * copies and tensor-core work it already issued finish (waiting at most

@@ -32,7 +32,8 @@ enum DeviceStatus : int {
   kDevTimeoutMma = 11,       // tensor-core kernel: MMA issuer waited too long
   kDevTimeoutEpilogue = 12,  // tensor-core kernel: epilogue / converter waited too long
   kDevTimeoutDrain = 13,     // tensor-core kernel: in-flight work did not drain after an abort
-  kDevBadOffsets = 20,       // grouped FFN: expert_offsets not 0-based / non-decreasing / in range
+  kDevTimeoutGrid = 14,      // few-token kernel: a block waited too long for the others
+  kDevBadOffsets = 20,       // grouped FFN, 8-bit product: offsets not 0-based / non-decreasing / in range
 };
 
 __device__ __forceinline__ void record_status(int *status, int code) {

@@ -193,7 +193,7 @@ __device__ __forceinline__ void grid_wait(unsigned *ctr, volatile int *abort_fla
       if (v >= gridDim.x || *abort_flag) break;
       if (((++spins & 31u) == 0 || p.timeout_ns < 1000u) && global_ns() - t0 > p.timeout_ns) {
         *abort_flag = 1;
-        record_status(p.status, kDevTimeoutEpilogue);
+        record_status(p.status, kDevTimeoutGrid);
         break;
       }
     }

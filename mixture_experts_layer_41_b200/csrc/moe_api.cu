@@ -414,7 +414,12 @@ moe_status moe_workspace_status(const void *ws, moe_stream_t stream) {
     case kDevTimeoutMma: what = "tensor-core kernel: MMA issuer wait timed out"; break;
     case kDevTimeoutEpilogue: what = "tensor-core kernel: epilogue / converter wait timed out"; break;
     case kDevTimeoutDrain: what = "tensor-core kernel: in-flight work did not drain after an abort"; break;
-    case kDevBadOffsets: what = "grouped FFN: expert_offsets not 0-based, non-decreasing and within T*k"; break;
+    case kDevTimeoutGrid:
+      what = "few-token kernel: a block's wait for the others timed out (do calls overlap on one workspace?)";
+      break;
+    case kDevBadOffsets:
+      what = "group offsets (the grouped FFN's expert_offsets) not 0-based, non-decreasing and within the rows";
+      break;
   }
   char num[32];
   snprintf(num, sizeof(num), "%d", code);
