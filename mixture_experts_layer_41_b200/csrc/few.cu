@@ -1583,19 +1583,23 @@ __global__ void __launch_bounds__(CT, 1) few_kernel(const __grid_constant__ FewP
   __syncthreads();
   Feed feed{};
   uint32_t red_it = 0;
-  if (p.Fs) feed = feed_open<FMT, DEPTH>(p, sh, feed, ring, R1);
+  constexpr bool SHARED = FMT != Q4;        // (4-bit layers have no shared expert)
+  if constexpr (SHARED)
+    if (p.Fs) feed = feed_open<FMT, DEPTH>(p, sh, feed, ring, R1);
   if (FMT != BF16) {
     quantize_x<FMT>(p, sh);
     if (blockIdx.x == 0)
       for (int i = threadIdx.x; i < p.T * p.k; i += CT) p.rowmax[i] = 0u;
   }
   route_logits<TP>(p, sh);
-  if (p.Fs) feed = consume_part<BF16, FMT, false, NB, DEPTH>(p, sh, ring_ptr, feed, red_it, S1);
+  if constexpr (SHARED)
+    if (p.Fs) feed = consume_part<BF16, FMT, false, NB, DEPTH>(p, sh, ring_ptr, feed, red_it, S1);
   grid_arrive(p.bar);
   grid_wait(p.bar, abort_flag, p);
   make_plan(p, sh);
   feed = feed_open<FMT, DEPTH>(p, sh, feed, ring, END);
-  if (p.Fs) feed = consume_part<BF16, FMT, true, NB, DEPTH>(p, sh, ring_ptr, feed, red_it, S2);
+  if constexpr (SHARED)
+    if (p.Fs) feed = consume_part<BF16, FMT, true, NB, DEPTH>(p, sh, ring_ptr, feed, red_it, S2);
   feed = consume_part<FMT, FMT, false, NB, DEPTH>(p, sh, ring_ptr, feed, red_it, R1);
   grid_arrive(p.bar + 8);
   grid_wait(p.bar + 8, abort_flag, p);
