@@ -876,12 +876,12 @@ route_i8_gemm(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ 
     bool ok = have_tmem;
     for (int it = 0; ok && it < kb_n; ++it) {
       const int xs = it % XS, as = it % AS;
-      if (!wait_warp(&st->x_full[xs], (it / XS) & 1, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns) ||
-          !wait_warp(&st->k_empty[as], ((it / AS) & 1) ^ 1, abort_flag, p.status, kDevTimeoutEpilogue,
-                        p.timeout_ns)) {
-        ok = false;
-        break;
-      }
+      // (one vote on both waits)
+      ok = __all_sync(0xffffffffu,
+                      wait_bounded(&st->x_full[xs], (it / XS) & 1, abort_flag, p.status, kDevTimeoutEpilogue, p.timeout_ns) &&
+                          wait_bounded(&st->k_empty[as], ((it / AS) & 1) ^ 1, abort_flag, p.status, kDevTimeoutEpilogue,
+                                       p.timeout_ns));
+      if (!ok) break;
       tc_fence_after();
       const uint8_t *xrow = xt + xs * S::X_BYTES + r * 128;
       uint32_t pl[XD][8];   // [digit plane][4-element word]
