@@ -527,6 +527,13 @@ moe_status moe_forward(const moe_config *cfg, const void *x, const float *w_rout
  * significant bits (8-bit experts: bf16, which is then quantised; 4-bit
  * experts: x and the intermediate as 16-bit integers over the largest
  * magnitude of their row).
+ * Faster than moe_forward where reading the weights is most of the time: on
+ * one B200, bf16 experts of d 4096, F 14336, top 2 of 8 take 141 us for 306 at
+ * one token and 493 for 549 at 16; 8-bit ones of d 7168, F 2048, top 8 of 256
+ * 125 for 201 and 730 for 741.  4-bit experts (d 2048, F 768, top 8 of 128) gain
+ * below four tokens only: 42 for 53 at one, 71 for 71 at four, 150 for 112 at 16
+ * (where moe_forward rounds each weight to bf16); layers of a few MB likewise
+ * (37 for 41 at one, 51 for 43 at 16).
  * A token whose router scores are NaN chooses no expert: ids -1, and a device
  * status.  The kernel's blocks wait for one another, so it is launched
  * cooperatively: it starts when every SM has room for its block, and two

@@ -52,12 +52,13 @@
 // fp32.  Expert outputs stay fp32 until the combine.
 //
 // Measured (graph replays): one token of d 4096, F 14336, top 2 of 8 in bf16
-// 137 us (5.1 TB/s of the weights; the nine launches of the staged layer 297);
+// 141 us (5.0 TB/s of the weights; the nine launches of the staged layer 306);
 // four of d 7168, F 2048, top 8 of 256 in 8 bits with a bf16 shared expert
-// 283 us (5.1 TB/s; staged 379); two of d 448, F 256 37 us, all of it launch,
-// barriers and latency.  4-bit experts are bound by the unpacking and by how
-// evenly few tasks divide: one token of d 2048, F 768, top 8 of 128 48 us
-// (staged 51), 16 tokens 158 us (staged 112, with weights rounded to bf16).
+// 287 us (5.0 TB/s; staged 378); two of d 448, F 256 37 us, all of it launch,
+// barriers and latency (16 of them 51, staged 43).  4-bit experts are bound by
+// the unpacking and by how evenly few tasks divide: one token of d 2048, F 768,
+// top 8 of 128 42 us (staged 53), four 71 (staged 71), 16 tokens 150 us
+// (staged 112, with weights rounded to bf16).
 //
 // Results do not depend on timing: every sum has a fixed order, and the row
 // maxima behind the 8-bit codes of h are integer maxima.

@@ -8,7 +8,11 @@
 //
 // The intermediate is bf16, as with every other weight type; its row maximum
 // spans all of the first product's output tiles, so it is quantised by a pass
-// of its own (2 F bytes read, F written per row).  Inside moe_forward the
+// of its own (2 F bytes read, F written per row).  y is rounded to bf16 before
+// the combine, as with every other weight type, because the staged calls hand
+// it on in act_dtype: against 64 bits a top-8 layer's output is 2.3e-3 off, and
+// 1.7e-3 (its own rounding alone) where moe_forward_few keeps y in fp32.
+// Inside moe_forward the
 // token rows are quantised once each and their codes written straight to the
 // rows of their slots, which takes the place of the dispatch's row copy.
 #include "common.cuh"

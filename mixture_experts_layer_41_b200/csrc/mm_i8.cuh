@@ -11,7 +11,8 @@ namespace i8 {
 constexpr int BM = 128;                       // accumulator rows of a CTA
 constexpr int BK = 128;                       // 128 int8 = one swizzle row
 
-// the approximate quotient is within 2 ulp (0 past 2^126, where silu is below
+// (moe_forward_few, which waits for its weights anyway, divides exactly: its h
+// can differ by a bf16 step.)  The approximate quotient is within 2 ulp (0 past 2^126, where silu is below
 // 2^-119); the IEEE one branches, and cost the product of 8192 x 28672 x 4096
 // a sixth of its time in the epilogue
 __device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.f + __expf(-g)); }

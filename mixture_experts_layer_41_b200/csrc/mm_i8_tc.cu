@@ -21,7 +21,9 @@
 //   warps 2-5   epilogue: tcgen05.ld, scales, activation, store.  Each warp
 //               keeps its own copy of the tile's channel scales in shared
 //               memory, fetched while the accumulator is still being built.
-// BN is 256 unless that leaves SMs without a tile (launch_mm_i8_tc).
+// BN is 256 unless that leaves SMs without a tile (launch_mm_i8_tc).  K is not
+// cut, so a few rows times a narrow matrix run on as many SMs as there are
+// 128 x 64 tiles.
 //
 // A tile's rows past its group's end belong to the next group (or are
 // zero-filled by TMA past the buffer); their results are never stored.
@@ -312,8 +314,7 @@ cudaError_t run(const MmI8Args &a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_mm_i8_tc(const MmI8Args &a, cudaStream_t s) {
-  // output columns a 256-wide tile covers; the narrowest tile that still
-  // gives every SM work is not needed once 256-wide tiles do
+  // the widest tile that gives every SM one, else the narrowest
   const int G = a.offsets ? a.G : 1;
   const long long m_tiles = (long long)(a.rows_cap + BM - 1) / BM + (G > 1 ? G / 2 : 0);
   auto tiles = [&](int bn) {

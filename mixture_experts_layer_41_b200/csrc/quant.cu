@@ -15,13 +15,14 @@
 // very small or very large are scaled by a power of two first, so that
 // neither r nor t leaves the normal range.
 //
-// Bound by HBM: each element is read once (a row stays in registers between
-// the maximum and the codes) and each code written once.  A warp takes a row
-// of up to 1024 elements, and of a matrix of many rows one of up to 4096
-// (fp32: 2048); a block of 256 threads one of up to 16384; longer rows are read a
+// Long rows are bound by HBM: each element is read once (a row stays in
+// registers between the maximum and the codes) and each code written once.  A
+// warp takes a row of up to 1024 elements, and of a matrix of many rows one of
+// up to 4096 (fp32: 2048); a block of 256 threads one of up to 16384; longer rows are read a
 // second time, from L2.  bf16, 8192 rows of 2048: 18.2 us (28.9 with a block to
-// a row, whose two barriers every row waits for), 2.8 TB/s; 8192 of 14336:
-// 68 us, 5.2 TB/s.
+// a row, whose two barriers every row waits for), 2.8 TB/s: bound by a warp's
+// own chain of load, maximum, codes and store, with two blocks to an SM (119
+// registers) beside it; 8192 of 14336: 68 us, 5.2 TB/s.
 //
 // The layer's use: rows of the expert-sorted matrix up to the device-side row
 // count, or (scatter) token rows whose codes go straight to their slots' rows
